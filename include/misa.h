@@ -234,6 +234,170 @@ misa_status misa_hisa_score_topk(const misa_shape* shape, int32_t h, int32_t m, 
                                  float* block_scores_out, int32_t* idx, float* scores_out,
                                  void* ws, size_t ws_bytes, hipStream_t stream);
 
+/* ------------------------------------------------------------------ serving
+ * What stands around the indexer in a serving step: the root-mean-square norm
+ * that makes its 8-bit inputs, the paged cache of keys and values, and the
+ * attention of the new token over the cached tokens the indexer selected (or
+ * over all of them).
+ *
+ * Conventions on top of those above:
+ *  - The limits on d, H, h and k above are the indexer's; each entry point
+ *    below states its own.
+ *  - Integer arrays the calls read on the device (tables, lengths, lists) are
+ *    checked there: an entry that names nothing (a row outside [0, rows), a
+ *    page outside [0, pages), a position beyond the table) is skipped, and
+ *    nothing outside the described arrays is read or written.
+ *  - 8-bit codes are OCP e4m3fn, value = code * scale, rounded to nearest even
+ *    from x * (448 / amax); scale = amax / 448, with amax the largest magnitude
+ *    of the values that share the scale (NaN left out), and scale = 1 when
+ *    amax < 2^-100 (zeros).  A NaN becomes a NaN code; an infinity makes its
+ *    scale infinite and itself a NaN code.
+ */
+
+/* A paged cache.  Sequence r of `rows` owns row r of the page table: token s
+ * of it lives in slot s % page_tokens of page table[r, s / page_tokens].
+ *   table    [rows, row_pages]  int32, -1 = no page
+ *   lengths  [rows]             int32, cached tokens of the row
+ *   refs     [pages]            int32, table entries that name the page; a
+ *                               page with refs <= 0 is free
+ *   k_pages  [pages, kv_heads, page_tokens, dk]  kv_dtype
+ *   v_pages  [pages, kv_heads, page_tokens, dv]  kv_dtype
+ *   k_scale, v_scale  [pages, kv_heads, page_tokens]  fp32 (fp8 only, > 0)
+ * Head dimensions: dk = dv in {64, 128, 256}; or the latent form dk = 576, dv
+ * = 512, kv_heads = 1, where one cached row serves every head and the values
+ * are its first 512 elements: v_pages, v_new and v_scale are then NULL.
+ * kv_dtype is MISA_BF16 or MISA_FP8_E4M3.  Limits: rows, row_pages, pages and
+ * page_tokens >= 1, page_tokens <= 4096, kv_heads <= 256, rows * row_pages <
+ * 2^31, row_pages * page_tokens < 2^31, rows <= 2^20, pages <= 2^24.  The
+ * calls that touch only tables, lengths and refs ignore kv_heads, dk, dv and
+ * kv_dtype. */
+typedef struct {
+  int32_t rows, row_pages, pages, page_tokens;
+  int32_t kv_heads, dk, dv;
+  int32_t kv_dtype;
+} misa_cache;
+
+/* Attention of one new token per row over its cached tokens:
+ *   o[r, j, :] = sum_s p_s v[r, s, g, :],  p = softmax_s(scale * q[r,j,:] . k[r,s,g,:]),
+ *   lse[r, j] = log sum_s exp(scale * q . k),   g = j / (heads / kv_heads),
+ * over the visible tokens s: all s < lengths[r], or with k > 0 the entries of
+ * idx[r, :] that lie in [0, lengths[r]) -- a list in any order, -1 padded, as
+ * the indexer's entry points write it (a token listed twice counts twice).
+ * Tokens whose table entry names no page are not visible.  A row without
+ * visible tokens gets o = 0 and lse = -INFINITY.  What the cache holds at
+ * invisible slots is never used, NaN or not.
+ *   q    [rows, heads, dk]  bf16      out [rows, heads, dv]  bf16, written
+ *   idx  [rows, k]  int32 (k > 0; k = 0: NULL)
+ *   lse  [rows, heads]  fp32, written if non-NULL
+ * Scores, softmax and sums are fp32.  Limits: heads a multiple of kv_heads,
+ * heads <= 1024, rows <= 65535, 0 <= k <= 2^20.  ws must hold
+ * misa_attend_workspace_bytes(cache, heads, k) bytes (0: invalid arguments or
+ * no workspace needed); it carries nothing from one call to the next. */
+size_t misa_attend_workspace_bytes(const misa_cache* cache, int32_t heads, int32_t k);
+misa_status misa_attend(const misa_cache* cache, int32_t heads, int32_t k, float scale,
+                        const void* q, const void* k_pages, const float* k_scale,
+                        const void* v_pages, const float* v_scale, const int32_t* table,
+                        const int32_t* lengths, const int32_t* idx, void* out, float* lse,
+                        void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* Write n new tokens into their pages: token i goes to position pos[i] of row
+ * row[i].  fp8 caches get codes and one scale per (token, kv head), from that
+ * head's dk (dv) values.  Entries with row outside [0, rows), pos outside the
+ * table or no page at that position are skipped (padding of a captured
+ * batch); two entries must not name the same slot.  lengths is not looked at:
+ * misa_page_extend keeps it, once per step for every layer.
+ *   row, pos  [n]  int32
+ *   k_new  [n, kv_heads, dk]  bf16        v_new  [n, kv_heads, dv]  bf16
+ * n = 0 is a no-op; n * kv_heads < 2^31. */
+misa_status misa_page_write(const misa_cache* cache, int32_t n, const int32_t* row,
+                            const int32_t* pos, const void* k_new, const void* v_new,
+                            void* k_pages, float* k_scale, void* v_pages, float* v_scale,
+                            const int32_t* table, hipStream_t stream);
+
+/* Make room for count[i] more tokens of row[i], and count them: the pages
+ * that positions lengths .. lengths + count - 1 newly need are taken from the
+ * free ones, lowest ids first, in list order, entered into the table with
+ * refs = 1, and lengths grows by count.  ok[i] = 1, or 0 with the row left as
+ * it was: a row outside [0, rows) or listed before, a negative count, a table
+ * row too short, or an entry that needs pages when the pages needed by the
+ * list up to and including it exceed the free ones.  n <= 4096. */
+misa_status misa_page_extend(const misa_cache* cache, int32_t n, const int32_t* row,
+                             const int32_t* count, int32_t* table, int32_t* lengths,
+                             int32_t* refs, int32_t* ok, hipStream_t stream);
+
+/* Fork rows: child[i] becomes a sequence with the tokens of parent[i].  Pages
+ * that the parent has filled are shared (refs + 1); a partly filled last page
+ * is replaced by a free one (lowest ids first, in list order), and the pair to
+ * copy is written to src[i], dst[i] for misa_page_copy (-1, -1: nothing to
+ * copy), so that both rows can go on to write.  ok[i] = 1, or 0 with the child
+ * left as it was: a row outside [0, rows), a child that is not empty (lengths
+ * != 0), is listed before or is its own parent, or -- when a page is needed --
+ * no free page left, counted as in misa_page_extend.  Parents are read as
+ * they were before the call.
+ *   parent, child, src, dst, ok  [n]  int32; n <= 4096 */
+misa_status misa_page_fork(const misa_cache* cache, int32_t n, const int32_t* parent,
+                           const int32_t* child, int32_t* table, int32_t* lengths, int32_t* refs,
+                           int32_t* src, int32_t* dst, int32_t* ok, hipStream_t stream);
+
+/* Free rows: refs of the pages that hold the row's tokens falls by one, their
+ * table entries become -1 and lengths 0.  A row listed twice is freed once; n
+ * <= 4096. */
+misa_status misa_page_free(const misa_cache* cache, int32_t n, const int32_t* row, int32_t* table,
+                           int32_t* lengths, int32_t* refs, hipStream_t stream);
+
+/* Compact the pool: with `live` pages in use, the i-th live page with id >=
+ * live (ascending) moves to the i-th free id < live, so that pages 0 .. live-1
+ * are the ones in use and the pool can be cut there.
+ *   map        [pages]  int32, written: each page's id afterwards, -1 = free
+ *   live       [1]      int32, written
+ *   src, dst   [max(1, pages / 2)]  int32, written: the moves, for
+ *              misa_page_copy, then -1
+ *   table_out, refs_out  written: table and refs with the new ids (they may
+ *              be the same arrays as table and refs); entries that name a free
+ *              page become -1
+ * Rows and lengths stay as they are.  ws must hold
+ * misa_page_workspace_bytes(cache) bytes. */
+size_t misa_page_workspace_bytes(const misa_cache* cache);
+misa_status misa_page_compact(const misa_cache* cache, const int32_t* table, const int32_t* refs,
+                              int32_t* table_out, int32_t* refs_out, int32_t* map, int32_t* live,
+                              int32_t* src, int32_t* dst, void* ws, size_t ws_bytes,
+                              hipStream_t stream);
+
+/* One buffer of pages: `planes` (layers, say) of `pages` pages of page_bytes
+ * bytes each, [planes, pages, page_bytes]. */
+typedef struct {
+  void* data;
+  int64_t page_bytes; /* a positive multiple of 4 */
+  int32_t planes;
+} misa_page_buffer;
+
+/* Copy page src[i] onto page dst[i], i < n, in every plane of n_buffers (1 ..
+ * 8) buffers of `pages` pages each.  `buffers` is a HOST array.  Pairs with an
+ * id outside [0, pages) are skipped; a page written by one pair must not be
+ * read or written by another. */
+misa_status misa_page_copy(const misa_page_buffer* buffers, int32_t n_buffers, int32_t pages,
+                           int32_t n, const int32_t* src, const int32_t* dst, hipStream_t stream);
+
+/* Root-mean-square norm of rows, with the residual's addition before it and an
+ * 8-bit output after it.  Per row of n elements in `groups` equal parts:
+ *   y = x + residual,   z_part = y_part / sqrt(mean(y_part^2) + eps) * weight,
+ *   out = z, or e4m3 codes of z with one scale per row.
+ * groups = 1 is the norm of a residual stream or of the indexer's keys (n = d:
+ * out and out_scale are misa_*'s k and k_scale); groups = H with n = H * d
+ * norms each head by itself and gives the indexer's q and q_scale.
+ *   x, residual  [rows, n]  x_dtype (MISA_F32 or MISA_BF16); residual may be NULL
+ *   weight       [n / groups]  fp32
+ *   sum_out      [rows, n]  x_dtype, y, written if non-NULL (may be x or residual)
+ *   out          [rows, n]  out_dtype (any misa_dtype), written
+ *   out_scale    [rows]     fp32, written (fp8 only, else ignored)
+ * fp32 throughout: y^2 must stay in fp32's range.  rows >= 0 (0: no-op), 1 <=
+ * n <= 32768, groups divides n, eps >= 0; an all-zero part with eps = 0 gives
+ * NaN. */
+misa_status misa_rms_norm(int32_t rows, int32_t n, int32_t groups, int32_t x_dtype,
+                          int32_t out_dtype, float eps, const void* x, const void* residual,
+                          const float* weight, void* sum_out, void* out, float* out_scale,
+                          hipStream_t stream);
+
 /* A static, human-readable name of a status code. */
 const char* misa_status_string(misa_status status);
 

@@ -31,6 +31,9 @@ EXPORTED = (
     "misa_workspace_bytes", "misa_pool_keys", "misa_pool_keys_range", "misa_route",
     "misa_score_topk", "misa_decode_step", "misa_decode_step_noalloc", "misa_rerank",
     "dsa_index_dense", "misa_hisa_workspace_bytes", "misa_hisa_score_topk", "misa_status_string",
+    "misa_attend_workspace_bytes", "misa_attend", "misa_page_write", "misa_page_extend",
+    "misa_page_fork", "misa_page_free", "misa_page_workspace_bytes", "misa_page_compact",
+    "misa_page_copy", "misa_rms_norm",
 )
 MISA_NOALLOC_SCRATCH_BYTES = 64 << 20
 
@@ -43,6 +46,15 @@ class MisaError(RuntimeError):
 
 class misa_shape(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("batch", "L", "T", "H", "d", "B", "qk_dtype")]
+
+
+class misa_cache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("rows", "row_pages", "pages", "page_tokens", "kv_heads",
+                                              "dk", "dv", "kv_dtype")]
+
+
+class misa_page_buffer(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("page_bytes", ctypes.c_int64), ("planes", ctypes.c_int32)]
 
 
 if not os.path.exists(LIB_PATH):
@@ -70,9 +82,25 @@ _lib.misa_hisa_workspace_bytes.restype = _SZ
 _lib.misa_hisa_score_topk.argtypes = [_SHP, _I32, _I32, _I32] + [_P] * 12 + [_SZ, _P]
 _lib.misa_rerank.argtypes = [_SHP, _I32, _I32, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]
 _lib.dsa_index_dense.argtypes = [_SHP, _I32, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]
+_CHE = ctypes.POINTER(misa_cache)
+_F32 = ctypes.c_float
+_lib.misa_attend_workspace_bytes.argtypes = [_CHE, _I32, _I32]
+_lib.misa_attend_workspace_bytes.restype = _SZ
+_lib.misa_attend.argtypes = [_CHE, _I32, _I32, _F32] + [_P] * 11 + [_SZ, _P]
+_lib.misa_page_write.argtypes = [_CHE, _I32] + [_P] * 10
+_lib.misa_page_extend.argtypes = [_CHE, _I32] + [_P] * 7
+_lib.misa_page_fork.argtypes = [_CHE, _I32] + [_P] * 9
+_lib.misa_page_free.argtypes = [_CHE, _I32] + [_P] * 5
+_lib.misa_page_workspace_bytes.argtypes = [_CHE]
+_lib.misa_page_workspace_bytes.restype = _SZ
+_lib.misa_page_compact.argtypes = [_CHE] + [_P] * 9 + [_SZ, _P]
+_lib.misa_page_copy.argtypes = [ctypes.POINTER(misa_page_buffer), _I32, _I32, _I32, _P, _P, _P]
+_lib.misa_rms_norm.argtypes = [_I32] * 5 + [_F32] + [_P] * 7
 for _f in ("misa_pool_keys", "misa_pool_keys_range", "misa_route", "misa_score_topk",
            "misa_decode_step", "misa_decode_step_noalloc", "misa_rerank", "dsa_index_dense",
-           "misa_hisa_score_topk"):
+           "misa_hisa_score_topk", "misa_attend", "misa_page_write", "misa_page_extend",
+           "misa_page_fork", "misa_page_free", "misa_page_compact", "misa_page_copy",
+           "misa_rms_norm"):
     getattr(_lib, _f).restype = ctypes.c_int
 _lib.misa_status_string.argtypes = [ctypes.c_int]
 _lib.misa_status_string.restype = ctypes.c_char_p
@@ -188,3 +216,75 @@ def misa_hisa_score_topk(shp, h, m, k, q, q_scale, w, pooled, kk, k_scale, heads
                                      _ptr(blocks_out), _ptr(block_scores_out), _ptr(idx),
                                      _ptr(scores_out), _ptr(ws), _nbytes(ws), _stream(stream)),
            "misa_hisa_score_topk")
+
+
+# ------------------------------------------------------------------ serving
+
+
+def cache(rows, row_pages, pages, page_tokens, kv_heads, dk, dv, kv_dtype) -> misa_cache:
+    return misa_cache(rows, row_pages, pages, page_tokens, kv_heads, dk, dv, kv_dtype)
+
+
+def page_buffers(buffers):
+    """The `buffers` argument of misa_page_copy, from (data, planes, page_bytes) triples.  It holds
+    addresses: the tensors must outlive it."""
+    return (misa_page_buffer * len(buffers))(*(misa_page_buffer(_ptr(d), b, p) for d, p, b in buffers))
+
+
+def misa_attend_workspace_bytes(cache: misa_cache, heads: int, k: int) -> int:
+    return int(_lib.misa_attend_workspace_bytes(ctypes.byref(cache), heads, k))
+
+
+def misa_attend(cache, heads, k, scale, q, k_pages, k_scale, v_pages, v_scale, table, lengths, idx,
+                out, lse, ws, stream=None):
+    _check(_lib.misa_attend(ctypes.byref(cache), heads, k, scale, _ptr(q), _ptr(k_pages),
+                            _ptr(k_scale), _ptr(v_pages), _ptr(v_scale), _ptr(table),
+                            _ptr(lengths), _ptr(idx), _ptr(out), _ptr(lse), _ptr(ws),
+                            _nbytes(ws), _stream(stream)), "misa_attend")
+
+
+def misa_page_write(cache, n, row, pos, k_new, v_new, k_pages, k_scale, v_pages, v_scale, table,
+                    stream=None):
+    _check(_lib.misa_page_write(ctypes.byref(cache), n, _ptr(row), _ptr(pos), _ptr(k_new),
+                                _ptr(v_new), _ptr(k_pages), _ptr(k_scale), _ptr(v_pages),
+                                _ptr(v_scale), _ptr(table), _stream(stream)), "misa_page_write")
+
+
+def misa_page_extend(cache, n, row, count, table, lengths, refs, ok, stream=None):
+    _check(_lib.misa_page_extend(ctypes.byref(cache), n, _ptr(row), _ptr(count), _ptr(table),
+                                 _ptr(lengths), _ptr(refs), _ptr(ok), _stream(stream)),
+           "misa_page_extend")
+
+
+def misa_page_fork(cache, n, parent, child, table, lengths, refs, src, dst, ok, stream=None):
+    _check(_lib.misa_page_fork(ctypes.byref(cache), n, _ptr(parent), _ptr(child), _ptr(table),
+                               _ptr(lengths), _ptr(refs), _ptr(src), _ptr(dst), _ptr(ok),
+                               _stream(stream)), "misa_page_fork")
+
+
+def misa_page_free(cache, n, row, table, lengths, refs, stream=None):
+    _check(_lib.misa_page_free(ctypes.byref(cache), n, _ptr(row), _ptr(table), _ptr(lengths),
+                               _ptr(refs), _stream(stream)), "misa_page_free")
+
+
+def misa_page_workspace_bytes(cache: misa_cache) -> int:
+    return int(_lib.misa_page_workspace_bytes(ctypes.byref(cache)))
+
+
+def misa_page_compact(cache, table, refs, table_out, refs_out, map, live, src, dst, ws, stream=None):
+    _check(_lib.misa_page_compact(ctypes.byref(cache), _ptr(table), _ptr(refs), _ptr(table_out),
+                                  _ptr(refs_out), _ptr(map), _ptr(live), _ptr(src), _ptr(dst),
+                                  _ptr(ws), _nbytes(ws), _stream(stream)), "misa_page_compact")
+
+
+def misa_page_copy(buffers, pages, n, src, dst, stream=None):
+    """`buffers`: what page_buffers() gives."""
+    _check(_lib.misa_page_copy(buffers, len(buffers), pages, n, _ptr(src), _ptr(dst),
+                               _stream(stream)), "misa_page_copy")
+
+
+def misa_rms_norm(rows, n, groups, x_dtype, out_dtype, eps, x, residual, weight, sum_out, out,
+                  out_scale, stream=None):
+    _check(_lib.misa_rms_norm(rows, n, groups, x_dtype, out_dtype, eps, _ptr(x), _ptr(residual),
+                              _ptr(weight), _ptr(sum_out), _ptr(out), _ptr(out_scale),
+                              _stream(stream)), "misa_rms_norm")

@@ -8,17 +8,20 @@
 #include <algorithm>
 #include <cstdint>
 
+#include "checks.hpp"
 #include "launch.hpp"
 
 namespace {
 
+using misa::aligned16;
+using misa::check_out;
+using misa::check_ws;
+using misa::from_hip;
 using misa::Shape;
 
 constexpr int32_t kMaxTopk = 8192;
 constexpr int32_t kMaxRouted = 16;
 constexpr int32_t kMaxHeads = 64;
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Validates the shape; on success fills `out`.
 misa_status check_shape(const misa_shape* sh, Shape& out) {
@@ -44,31 +47,11 @@ misa_status check_inputs(const Shape& s, const void* q, const float* q_scale, co
   return MISA_OK;
 }
 
-misa_status check_out(const void* p, bool required) {
-  if (!p) return required ? MISA_ERR_INVALID_ARG : MISA_OK;
-  return aligned16(p) ? MISA_OK : MISA_ERR_INVALID_ARG;
-}
-
 misa_status check_topk(int32_t k) {
   if (k < 1) return MISA_ERR_INVALID_ARG;
   if (k > kMaxTopk) return MISA_ERR_UNSUPPORTED;
   return MISA_OK;
 }
-
-misa_status check_ws(const void* ws, size_t ws_bytes, size_t need) {
-  if (need == 0) return MISA_OK;
-  if (!ws || ws_bytes < need) return MISA_ERR_WORKSPACE;
-  if (!aligned16(ws)) return MISA_ERR_INVALID_ARG;
-  return MISA_OK;
-}
-
-misa_status from_hip(hipError_t e) { return e == hipSuccess ? MISA_OK : MISA_ERR_HIP; }
-
-#define MISA_TRY(expr)                   \
-  do {                                   \
-    const misa_status st_ = (expr);      \
-    if (st_ != MISA_OK) return st_;      \
-  } while (0)
 
 // Argument checks of the decode step (both forms); fills `s` on success.
 misa_status check_decode_step(const misa_shape* shape, int32_t h, int32_t k, const void* q,

@@ -116,6 +116,59 @@ hipError_t launch_hisa_score_topk(const Shape& s, int32_t nh, const int32_t* hea
                                   int32_t* blocks_out, float* block_scores_out, int32_t* idx,
                                   float* scores_out, void* ws, hipStream_t st);
 
+// ---------------------------------------------------------------- serving
+
+struct Cache {
+  int32_t rows, row_pages, pages, P;  // P: tokens per page
+  int32_t kv_heads, dk, dv, dtype;
+  // One cached row per token serves every head; its first dv elements are the value.
+  bool latent() const { return dk == 576 && dv == 512; }
+};
+
+// Attention of one new token per row.  k > 0: over the listed tokens only.
+size_t attend_ws_bytes(const Cache& c, int32_t heads, int32_t k);
+hipError_t launch_attend(const Cache& c, int32_t heads, int32_t k, float scale, const void* q,
+                         const void* k_pages, const float* k_scale, const void* v_pages,
+                         const float* v_scale, const int32_t* table, const int32_t* lengths,
+                         const int32_t* idx, void* out, float* lse, void* ws, hipStream_t st);
+
+hipError_t launch_page_write(const Cache& c, int32_t n, const int32_t* row, const int32_t* pos,
+                             const void* k_new, const void* v_new, void* k_pages, float* k_scale,
+                             void* v_pages, float* v_scale, const int32_t* table, hipStream_t st);
+
+hipError_t launch_page_extend(const Cache& c, int32_t n, const int32_t* row, const int32_t* count,
+                              int32_t* table, int32_t* lengths, int32_t* refs, int32_t* ok,
+                              hipStream_t st);
+hipError_t launch_page_fork(const Cache& c, int32_t n, const int32_t* parent, const int32_t* child,
+                            int32_t* table, int32_t* lengths, int32_t* refs, int32_t* src,
+                            int32_t* dst, int32_t* ok, hipStream_t st);
+hipError_t launch_page_free(const Cache& c, int32_t n, const int32_t* row, int32_t* table,
+                            int32_t* lengths, int32_t* refs, hipStream_t st);
+size_t page_compact_ws_bytes(const Cache& c);
+hipError_t launch_page_compact(const Cache& c, const int32_t* table, const int32_t* refs,
+                               int32_t* table_out, int32_t* refs_out, int32_t* map, int32_t* live,
+                               int32_t* src, int32_t* dst, void* ws, hipStream_t st);
+
+constexpr int32_t kMaxPageBuffers = 8;
+struct PageBuffer {
+  uint8_t* data;
+  int64_t page_bytes;
+  int32_t planes;
+};
+struct PageBuffers {
+  PageBuffer b[kMaxPageBuffers];
+  int32_t n;
+};
+bool page_copy_supported(const PageBuffers& b, int32_t n);
+hipError_t launch_page_copy(const PageBuffers& b, int32_t pages, int32_t n, const int32_t* src,
+                            const int32_t* dst, hipStream_t st);
+
+constexpr int32_t kMaxNorm = 32768;  // elements of a normed row (one row in LDS)
+hipError_t launch_rms_norm(int32_t rows, int32_t n, int32_t groups, int32_t x_dtype,
+                           int32_t out_dtype, float eps, const void* x, const void* residual,
+                           const float* weight, void* sum_out, void* out, float* out_scale,
+                           hipStream_t st);
+
 inline size_t align_up(size_t x, size_t a = 256) { return (x + a - 1) / a * a; }
 
 // The fixed device scratch of the no-allocation decode step: its size, and

@@ -1,0 +1,35 @@
+// e4m3fn codes with a shared fp32 scale: value = code * scale.
+#pragma once
+
+#include "common.hpp"
+
+namespace misa {
+
+constexpr float kE4M3Max = 448.f;
+
+// Scale and code multiplier of values whose largest magnitude is `amax`.
+// Below 2^-100, where 448 / amax nears overflow, the values count as zeros.
+__device__ __forceinline__ void e4m3_scale(float amax, float& scale, float& mult) {
+  const bool some = amax >= 0x1p-100f;
+  scale = some ? amax / kE4M3Max : 1.f;
+  mult = some ? kE4M3Max / amax : 1.f;
+}
+
+// x * mult clamped to +-448 (the product may round past it), NaN kept.
+__device__ __forceinline__ float e4m3_prepare(float x, float mult) {
+  const float y = x * mult;
+  const float c = __builtin_amdgcn_fmed3f(y, -kE4M3Max, kE4M3Max);
+  return y == y ? c : y;
+}
+
+// Four codes in one dword (hardware conversion, round to nearest even).
+__device__ __forceinline__ uint32_t e4m3_pack4(float a, float b, float c, float d, float mult) {
+  int r = __builtin_amdgcn_cvt_pk_fp8_f32(e4m3_prepare(a, mult), e4m3_prepare(b, mult), 0, false);
+  r = __builtin_amdgcn_cvt_pk_fp8_f32(e4m3_prepare(c, mult), e4m3_prepare(d, mult), r, true);
+  return static_cast<uint32_t>(r);
+}
+
+// The larger magnitude, a NaN left out.
+__device__ __forceinline__ float amax_step(float m, float x) { return fmaxf(m, fabsf(x)); }
+
+}  // namespace misa
