@@ -268,7 +268,8 @@ misa_status misa_hisa_score_topk(const misa_shape* shape, int32_t h, int32_t m, 
  * are its first 512 elements: v_pages, v_new and v_scale are then NULL.
  * kv_dtype is MISA_BF16 or MISA_FP8_E4M3.  Limits: rows, row_pages, pages and
  * page_tokens >= 1, page_tokens <= 4096, kv_heads <= 256, rows * row_pages <
- * 2^31, row_pages * page_tokens < 2^31, rows <= 2^20, pages <= 2^24.  The
+ * 2^31, row_pages * page_tokens <= 2^30, rows <= 2^20, pages <= 2^24, pages *
+ * kv_heads * page_tokens < 2^32 - 1.  The
  * calls that touch only tables, lengths and refs ignore kv_heads, dk, dv and
  * kv_dtype. */
 typedef struct {

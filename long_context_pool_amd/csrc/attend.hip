@@ -1,5 +1,7 @@
 // Attention of one new token per row over a paged cache (misa_attend in
 // misa.h): every cached token of the row, or those of an index list.
+#include <algorithm>
+
 #include "common.hpp"
 #include "launch.hpp"
 #include "mfma.hpp"
@@ -8,12 +10,464 @@ namespace misa {
 
 namespace {
 
+typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr uint32_t kHidden = 0xFFFFFFFFu;  // the slot of a token that is not visible
+
+// n / P for 0 <= n < 2^31 by a multiplication: with l = ceil(log2 P), m =
+// floor(2^(31+l) / P) + 1 exceeds 2^(31+l) / P by less than 2^l / P * P, so
+// n * m >> (31+l) is the quotient.
+struct Div {
+  uint32_t m, shift, P;
+};
+
+Div make_div(uint32_t P) {
+  uint32_t l = 0;
+  while ((1u << l) < P) ++l;
+  return {static_cast<uint32_t>((uint64_t{1} << (31 + l)) / P + 1), 31 + l, P};
+}
+
+__device__ __forceinline__ uint32_t div_page(uint32_t n, Div d) {
+  return static_cast<uint32_t>((static_cast<uint64_t>(n) * d.m) >> d.shift);
+}
+
+struct Args {
+  const uint16_t* q;
+  const uint8_t* k_pages;
+  const float* k_scale;
+  const uint8_t* v_pages;
+  const float* v_scale;
+  const int32_t* table;
+  const int32_t* lengths;
+  const int32_t* idx;
+  uint16_t* out;
+  float* lse;
+  float* part_o;   // [rows, heads, splits, dv] unnormalised sums of a split
+  float2* part_ml;  // [rows, heads, splits] maximum (log2) and sum
+  int32_t heads, share, k, splits, row_pages, pages, kv_heads;
+  float scale2;  // scale * log2(e): softmax by powers of two
+  Div div;
+};
+
+// Tokens of row `row` to look at, and the pool slot of the t-th of them.
+__device__ __forceinline__ int32_t tokens_of(const Args& a, int row, int32_t& len) {
+  const int32_t cap = a.row_pages * static_cast<int32_t>(a.div.P);
+  len = min(max(a.lengths[row], 0), cap);
+  return a.idx ? (len > 0 ? a.k : 0) : len;
+}
+
+__device__ __forceinline__ uint32_t slot_of(const Args& a, int row, int kvh, int32_t len, int32_t t) {
+  const int32_t s = a.idx ? a.idx[static_cast<int64_t>(row) * a.k + t] : t;
+  if (s < 0 || s >= len) return kHidden;
+  const uint32_t e = div_page(s, a.div);
+  const int32_t page = a.table[static_cast<int64_t>(row) * a.row_pages + e];
+  if (page < 0 || page >= a.pages) return kHidden;
+  return (static_cast<uint32_t>(page) * a.kv_heads + kvh) * a.div.P + (s - e * a.div.P);
+}
+
+// How the tiles of a row are divided: every split takes `per` tiles, a
+// multiple of the workgroup's four waves.
+constexpr int kTileTokens = 32;
+__device__ __forceinline__ int32_t tiles_per_split(int32_t todo, int32_t splits) {
+  const int32_t tiles = (todo + kTileTokens - 1) / kTileTokens;
+  return (((tiles + splits - 1) / splits) + 3) & ~3;
+}
+
+constexpr int kStage = 2048;  // tokens whose slots (and scales) are in LDS at a time
+
+// ---------------------------------------------------------------- dk = dv
+
+// Eight e4m3 codes -> bf16, exact.
+__device__ __forceinline__ bf16x8 fp8x8_to_bf16(uint32_t lo, uint32_t hi) {
+  uint4 r;
+  r.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, false));
+  r.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, true));
+  r.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, false));
+  r.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, true));
+  return as_bf16x8(r);
+}
+
+// Two columns of V^T from the dwords (two bf16 dimensions each) of eight value
+// rows, and their products with both parts of the weights.
+template <int RT, int NJ>
+__device__ __forceinline__ void columns(const uint32_t (&w)[8], const bf16x8 (&ph)[RT],
+                                        const bf16x8 (&pl)[RT], f32x4 (&acc)[RT][NJ], int j) {
+  uint4 even, odd;
+  even.x = __builtin_amdgcn_perm(w[1], w[0], 0x05040100);
+  even.y = __builtin_amdgcn_perm(w[3], w[2], 0x05040100);
+  even.z = __builtin_amdgcn_perm(w[5], w[4], 0x05040100);
+  even.w = __builtin_amdgcn_perm(w[7], w[6], 0x05040100);
+  odd.x = __builtin_amdgcn_perm(w[1], w[0], 0x07060302);
+  odd.y = __builtin_amdgcn_perm(w[3], w[2], 0x07060302);
+  odd.z = __builtin_amdgcn_perm(w[5], w[4], 0x07060302);
+  odd.w = __builtin_amdgcn_perm(w[7], w[6], 0x07060302);
+  const bf16x8 v0 = as_bf16x8(even), v1 = as_bf16x8(odd);
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    acc[r][j] = mfma16_bf16(v0, ph[r], acc[r][j]);
+    acc[r][j + 1] = mfma16_bf16(v1, ph[r], acc[r][j + 1]);
+    acc[r][j] = mfma16_bf16(v0, pl[r], acc[r][j]);
+    acc[r][j + 1] = mfma16_bf16(v1, pl[r], acc[r][j + 1]);
+  }
+}
+
+// The dimension that product j gives for row c of V^T (the lane that loaded it).
+template <int D, int DT>
+__device__ __forceinline__ int value_dim(int c, int j) {
+  constexpr int per = DT == kFP8 ? D / 16 : (D / 16 < 8 ? D / 16 : 8);  // contiguous per lane
+  return (j / per) * 16 * per + c * per + j % per;
+}
+
+// log of the sum of exponentials from its log2 maximum and scaled sum.
+__device__ __forceinline__ float final_lse(float m, float l) {
+  return (m == -INFINITY ? 0.f : m * kLn2) + __logf(l);
+}
+
+
+// One workgroup of four waves per (split, kv head and chunk of 16 * RT query
+// heads, row); a wave takes every fourth tile of 32 tokens.  All products are
+// transposed, so that a lane keeps one query head (l % 16):
+//   S^T = K Q^T   16x16x32 bf16, rows = tokens, columns = heads,
+//   O^T = V^T P^T with P^T read from S^T's registers as they are: lane group g
+//         holds the tokens 4g .. 4g+3 of both 16-token halves, and V's rows
+//         are loaded in that order.  Eight rows of V make eight columns of V^T
+//         by byte permutes in registers.
+// A weight goes into the product as two bf16 parts (its rounding and the rest,
+// 2^-17 together), or the result would be off by a second bf16 rounding; the
+// cached values are exact in bf16.  Maximum, sums and O stay in fp32 registers.
+template <int D, int DT, int RT>
+__global__ __launch_bounds__(256) void attend_kernel(Args a) {
+  constexpr int EB = DT == kFP8 ? 1 : 2;
+  constexpr int ROW = D * EB;       // bytes of a cached row
+  constexpr int KL = ROW / 64;      // 16-byte loads per lane and key row
+  constexpr int KS = D / 32;        // matrix steps of a dot product
+  constexpr int VB = D / 16 * EB;   // bytes of a value row per lane
+  constexpr int VW = VB / 4;
+  constexpr int NJ = D / 16;        // products of 16 dimensions
+  constexpr int NR = RT * (NJ * 4 + 1);  // registers of a wave's result
+  constexpr bool kFp8 = DT == kFP8;
+  struct Stage {
+    uint32_t slot[kStage];
+    float ks[kFp8 ? kStage : 4];
+    float vs[kFp8 ? kStage : 4];
+  };
+  union Shared {
+    Stage st;
+    float red[2][NR][kWave];
+  };
+  __shared__ __attribute__((aligned(16))) Shared sh;
+  __shared__ float top[4][RT][16];
+
+  const int lane = lane_id(), wave = threadIdx.x / kWave;
+  const int c = lane & 15, g = lane >> 4;
+  const int split = blockIdx.x, row = blockIdx.z;
+  const int chunks = (a.share + 16 * RT - 1) / (16 * RT);
+  const int kvh = blockIdx.y / chunks, chunk = blockIdx.y % chunks;
+  const int head0 = kvh * a.share + chunk * 16 * RT;       // first query head
+  const int nheads = min(16 * RT, a.share - chunk * 16 * RT);
+  int32_t len;
+  const int32_t todo = tokens_of(a, row, len);
+  const int32_t per = tiles_per_split(todo, a.splits) * kTileTokens;
+  const int32_t t0 = split * per, t1 = min(t0 + per, todo);
+  if (t0 >= t1 && split > 0) return;  // nothing here; the join does not look at it
+
+  // Q^T fragments: head c of each row tile, the dimensions that K's loads give.
+  bf16x8 qf[RT][KS];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    const int h = r * 16 + c;
+    const uint16_t* src = a.q + (static_cast<int64_t>(row) * a.heads + head0 + (h < nheads ? h : 0)) * D;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      const int d0 = kFp8 ? 64 * (s / 2) + 16 * g + 8 * (s % 2) : 32 * s + 8 * g;
+      qf[r][s] = as_bf16x8(*reinterpret_cast<const uint4*>(src + d0));
+    }
+  }
+
+  f32x4 acc[RT][NJ];
+  float m[RT], l[RT];  // maximum of the head (all lanes alike), this lane's part of the sum
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    m[r] = -INFINITY;
+    l[r] = 0.f;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) acc[r][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+
+  uint4 kreg[2][KL];
+  uint32_t vreg[8][VW];
+  auto load_k = [&](int tile) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t s = sh.st.slot[tile * 32 + 16 * h + c];
+      const uint8_t* p = a.k_pages + static_cast<uint64_t>(s == kHidden ? 0 : s) * ROW + g * 16;
+#pragma unroll
+      for (int u = 0; u < KL; ++u) kreg[h][u] = *reinterpret_cast<const uint4*>(p + u * 64);
+    }
+  };
+  auto load_v = [&](int tile) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t s = sh.st.slot[tile * 32 + (i / 4) * 16 + 4 * g + i % 4];
+      const uint8_t* p = a.v_pages + static_cast<uint64_t>(s == kHidden ? 0 : s) * ROW;
+      if constexpr (VB == 4) {
+        vreg[i][0] = *reinterpret_cast<const uint32_t*>(p + c * 4);
+      } else if constexpr (VB == 8) {
+        const uint2 x = *reinterpret_cast<const uint2*>(p + c * 8);
+        vreg[i][0] = x.x;
+        vreg[i][1] = x.y;
+      } else {
+#pragma unroll
+        for (int u = 0; u < VB / 16; ++u) {
+          const uint4 x = *reinterpret_cast<const uint4*>(p + u * 256 + c * 16);
+          vreg[i][4 * u] = x.x;
+          vreg[i][4 * u + 1] = x.y;
+          vreg[i][4 * u + 2] = x.z;
+          vreg[i][4 * u + 3] = x.w;
+        }
+      }
+    }
+  };
+
+  for (int32_t base = t0; base < t1; base += kStage) {
+    const int32_t count = min(kStage, t1 - base);
+    const int32_t tiles = (count + kTileTokens - 1) / kTileTokens;
+    if (base != t0) __syncthreads();
+    for (int32_t i = threadIdx.x; i < tiles * kTileTokens; i += 256) {
+      const uint32_t s = i < count ? slot_of(a, row, kvh, len, base + i) : kHidden;
+      sh.st.slot[i] = s;
+      if constexpr (kFp8) {
+        sh.st.ks[i] = s == kHidden ? 0.f : a.k_scale[s];
+        sh.st.vs[i] = s == kHidden ? 0.f : a.v_scale[s];
+      }
+    }
+    __syncthreads();
+    if (wave < tiles) {
+      load_k(wave);
+      load_v(wave);
+    }
+    for (int32_t tile = wave; tile < tiles; tile += 4) {
+      const bool more = tile + 4 < tiles;
+      // scores of this lane's eight tokens (i < 4: token 4g + i, else 16 + 4g + i - 4)
+      f32x4 st[RT][2];
+#pragma unroll
+      for (int r = 0; r < RT; ++r) st[r][0] = st[r][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          bf16x8 kf;
+          if constexpr (kFp8) {
+            const uint4 x = kreg[h][s / 2];
+            kf = fp8x8_to_bf16(s % 2 ? x.z : x.x, s % 2 ? x.w : x.y);
+          } else {
+            kf = as_bf16x8(kreg[h][s]);
+          }
+#pragma unroll
+          for (int r = 0; r < RT; ++r) st[r][h] = mfma16_bf16(kf, qf[r][s], st[r][h]);
+        }
+      if (more) load_k(tile + 4);
+      uint32_t sl[8];
+      float ks[8], vs[8];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int at = tile * 32 + 16 * h + 4 * g;
+        const uint4 x = *reinterpret_cast<const uint4*>(&sh.st.slot[at]);
+        sl[4 * h] = x.x; sl[4 * h + 1] = x.y; sl[4 * h + 2] = x.z; sl[4 * h + 3] = x.w;
+        if constexpr (kFp8) {
+          const float4 y = *reinterpret_cast<const float4*>(&sh.st.ks[at]);
+          ks[4 * h] = y.x; ks[4 * h + 1] = y.y; ks[4 * h + 2] = y.z; ks[4 * h + 3] = y.w;
+          const float4 z = *reinterpret_cast<const float4*>(&sh.st.vs[at]);
+          vs[4 * h] = z.x; vs[4 * h + 1] = z.y; vs[4 * h + 2] = z.z; vs[4 * h + 3] = z.w;
+        }
+      }
+      bool hidden = false;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) hidden |= sl[i] == kHidden;
+      bf16x8 ph[RT], pl[RT];
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        float x[8], high = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float y = st[r][i / 4][i % 4] * a.scale2;
+          if constexpr (kFp8) y *= ks[i];
+          x[i] = sl[i] == kHidden ? -INFINITY : y;
+          high = fmaxf(high, x[i]);
+        }
+        if (__any(high > m[r])) {  // wave-uniform: a new maximum somewhere
+          high = fmaxf(high, __shfl_xor(high, 16, kWave));
+          high = fmaxf(high, __shfl_xor(high, 32, kWave));
+          const float next = fmaxf(m[r], high);
+          const float f = next == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m[r] - next);
+          m[r] = next;
+          l[r] *= f;
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) acc[r][j] *= f;
+        }
+        const float mb = m[r] == -INFINITY ? 0.f : m[r];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float p = __builtin_amdgcn_exp2f(x[i] - mb);
+          l[r] += p;
+          const float w = kFp8 ? p * vs[i] : p;
+          const __bf16 hi = static_cast<__bf16>(w);
+          ph[r][i] = hi;
+          pl[r][i] = static_cast<__bf16>(w - static_cast<float>(hi));
+        }
+      }
+      if (__any(hidden)) {  // hidden slots may hold anything: 0 * NaN must not reach O
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int u = 0; u < VW; ++u) vreg[i][u] = sl[i] == kHidden ? 0u : vreg[i][u];
+      }
+#pragma unroll
+      for (int u = 0; u < VW; ++u) {
+        // dword u of the eight rows: 2 (bf16) or 4 (fp8) columns of V^T
+        if constexpr (kFp8) {
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint32_t w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              w[i] = __builtin_bit_cast(
+                  uint32_t, half ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(vreg[i][u], 1.f, true)
+                                 : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(vreg[i][u], 1.f, false));
+            columns(w, ph, pl, acc, 4 * u + 2 * half);
+          }
+        } else {
+          uint32_t w[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) w[i] = vreg[i][u];
+          columns(w, ph, pl, acc, 2 * u);
+        }
+      }
+      if (more) load_v(tile + 4);
+    }
+  }
+
+  // Join the four waves: common maximum, then a tree through LDS into wave 0.
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    l[r] += __shfl_xor(l[r], 16, kWave);
+    l[r] += __shfl_xor(l[r], 32, kWave);
+    if (g == 0) top[wave][r][c] = m[r];
+  }
+  __syncthreads();
+  float mall[RT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    mall[r] = fmaxf(fmaxf(top[0][r][c], top[1][r][c]), fmaxf(top[2][r][c], top[3][r][c]));
+    const float f = mall[r] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m[r] - mall[r]);
+    if (m[r] != -INFINITY || l[r] != 0.f) {  // a NaN sum under no maximum stays one
+      l[r] *= mall[r] == -INFINITY ? 1.f : f;
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) acc[r][j] *= mall[r] == -INFINITY ? 1.f : f;
+    }
+  }
+#pragma unroll
+  for (int step = 2; step >= 1; step >>= 1) {
+    if (wave >= step && wave < 2 * step) {
+      int n = 0;
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        sh.red[wave - step][n++][lane] = l[r];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sh.red[wave - step][n++][lane] = acc[r][j][e];
+      }
+    }
+    __syncthreads();
+    if (wave < step) {
+      int n = 0;
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        l[r] += sh.red[wave][n++][lane];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[r][j][e] += sh.red[wave][n++][lane];
+      }
+    }
+    __syncthreads();
+  }
+  if (wave != 0) return;
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    const int h = r * 16 + c;
+    if (h >= nheads) continue;
+    const int64_t at = static_cast<int64_t>(row) * a.heads + head0 + h;
+    if (a.splits == 1) {
+      const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];
+      if (g == 0 && a.lse) a.lse[at] = l[r] == 0.f ? -INFINITY : final_lse(mall[r], l[r]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int j = 0; j < NJ; j += 2) {
+          bf16x2 x;
+          x[0] = static_cast<__bf16>(acc[r][j][e] * inv);
+          x[1] = static_cast<__bf16>(acc[r][j + 1][e] * inv);
+          *reinterpret_cast<bf16x2*>(a.out + at * D + value_dim<D, DT>(4 * g + e, j)) = x;
+        }
+    } else {
+      const int64_t part = at * a.splits + split;
+      if (g == 0) a.part_ml[part] = make_float2(mall[r], l[r]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int j = 0; j < NJ; j += 4)
+          *reinterpret_cast<float4*>(a.part_o + part * D + value_dim<D, DT>(4 * g + e, j)) =
+              make_float4(acc[r][j][e], acc[r][j + 1][e], acc[r][j + 2][e], acc[r][j + 3][e]);
+    }
+  }
+}
+
+// The splits of one (row, head), joined by one wave in split order.
+template <int D>
+__global__ __launch_bounds__(256) void attend_join_kernel(Args a) {
+  constexpr int E = D / 64;
+  const int lane = lane_id();
+  const int head = blockIdx.x * 4 + threadIdx.x / kWave, row = blockIdx.y;
+  if (head >= a.heads) return;
+  int32_t len;
+  const int32_t todo = tokens_of(a, row, len);
+  const int32_t per = tiles_per_split(todo, a.splits) * kTileTokens;
+  const int32_t n = todo > 0 ? (todo + per - 1) / per : 1;  // split 0 always writes
+  const int64_t at = static_cast<int64_t>(row) * a.heads + head;
+  const float2* ml = a.part_ml + at * a.splits;
+  float m = -INFINITY;
+  for (int s = lane; s < n; s += kWave) m = fmaxf(m, ml[s].x);
+#pragma unroll
+  for (int o = 1; o < kWave; o <<= 1) m = fmaxf(m, __shfl_xor(m, o, kWave));
+  const float mb = m == -INFINITY ? 0.f : m;
+  float l = 0.f, o[E] = {};
+  for (int s = 0; s < n; ++s) {
+    const float2 x = ml[s];
+    const float f = x.x == -INFINITY && x.y == 0.f ? 0.f : x.x == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(x.x - mb);
+    l += x.y * f;
+    const float* src = a.part_o + (at * a.splits + s) * D + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] += src[e] * f;
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  if (lane == 0 && a.lse) a.lse[at] = l == 0.f ? -INFINITY : final_lse(m, l);
+#pragma unroll
+  for (int e = 0; e < E; ++e)
+    reinterpret_cast<__bf16*>(a.out)[at * D + lane * E + e] = static_cast<__bf16>(o[e] * inv);
+}
+
+// ---------------------------------------------------------------- latent rows
+
 constexpr int kTile = 256;  // tokens per pass: one per thread
 
 // One workgroup per (head, row): scores of 256 tokens, one per thread, then
 // the running maximum and sum, then the values, two dimensions per thread.
 template <int DK, int DV, int DT, bool LATENT>
-__global__ __launch_bounds__(256) void attend_kernel(
+__global__ __launch_bounds__(256) void attend_latent_kernel(
     Cache c, int32_t heads, int32_t k, float scale, const uint16_t* __restrict__ q,
     const void* __restrict__ k_pages, const float* __restrict__ k_scale,
     const void* __restrict__ v_pages, const float* __restrict__ v_scale,
@@ -91,44 +545,104 @@ __global__ __launch_bounds__(256) void attend_kernel(
   if (lse && threadIdx.x == 0) lse[qat] = m == -INFINITY ? -INFINITY : m + logf(l);
 }
 
-template <int DK, int DV, bool LATENT>
-hipError_t launch_dims(const Cache& c, int32_t heads, int32_t k, float scale, const void* q,
-                       const void* k_pages, const float* k_scale, const void* v_pages,
-                       const float* v_scale, const int32_t* table, const int32_t* lengths,
-                       const int32_t* idx, void* out, float* lse, hipStream_t st) {
-  const dim3 grid(heads, c.rows);
-  const auto* qq = static_cast<const uint16_t*>(q);
-  auto* o = static_cast<uint16_t*>(out);
-  if (c.dtype == kFP8)
-    attend_kernel<DK, DV, kFP8, LATENT><<<grid, 256, 0, st>>>(
-        c, heads, k, scale, qq, k_pages, k_scale, v_pages, v_scale, table, lengths, idx, o, lse);
-  else
-    attend_kernel<DK, DV, kBF16, LATENT><<<grid, 256, 0, st>>>(
-        c, heads, k, scale, qq, k_pages, k_scale, v_pages, v_scale, table, lengths, idx, o, lse);
+constexpr int kMinSplitTokens = 128;  // a split gives each wave a tile
+
+// Query heads per workgroup / 16.
+int row_tiles(const Cache& c, int32_t share) { return share > 16 && c.dk <= 128 ? 2 : 1; }
+
+struct Plan {
+  int32_t chunks, splits;
+};
+
+Plan plan(const Cache& c, int32_t heads, int32_t k) {
+  const int32_t share = heads / c.kv_heads;
+  const int32_t per = 16 * row_tiles(c, share);
+  Plan p;
+  p.chunks = (share + per - 1) / per;
+  const int64_t groups = static_cast<int64_t>(c.rows) * c.kv_heads * p.chunks;
+  const int64_t most = k > 0 ? k : static_cast<int64_t>(c.row_pages) * c.P;
+  int64_t s = (1024 + groups - 1) / groups;
+  s = std::min<int64_t>(s, (most + kMinSplitTokens - 1) / kMinSplitTokens);
+  p.splits = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(s, 128)));
+  return p;
+}
+
+template <int D, int DT>
+hipError_t launch_dim(const Cache& c, const Args& a, const Plan& p, hipStream_t st) {
+  const dim3 grid(p.splits, c.kv_heads * p.chunks, c.rows);
+  if constexpr (D <= 128) {
+    if (row_tiles(c, a.share) == 2)
+      attend_kernel<D, DT, 2><<<grid, 256, 0, st>>>(a);
+    else
+      attend_kernel<D, DT, 1><<<grid, 256, 0, st>>>(a);
+  } else {
+    attend_kernel<D, DT, 1><<<grid, 256, 0, st>>>(a);
+  }
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.splits == 1) return e;
+  attend_join_kernel<D><<<dim3((a.heads + 3) / 4, c.rows), 256, 0, st>>>(a);
   return hipGetLastError();
+}
+
+template <int D>
+hipError_t launch_type(const Cache& c, const Args& a, const Plan& p, hipStream_t st) {
+  return c.dtype == kFP8 ? launch_dim<D, kFP8>(c, a, p, st) : launch_dim<D, kBF16>(c, a, p, st);
 }
 
 }  // namespace
 
-size_t attend_ws_bytes(const Cache&, int32_t, int32_t) { return 0; }
+size_t attend_ws_bytes(const Cache& c, int32_t heads, int32_t k) {
+  if (c.latent()) return 0;
+  const Plan p = plan(c, heads, k);
+  if (p.splits == 1) return 0;
+  const size_t parts = static_cast<size_t>(c.rows) * heads * p.splits;
+  return align_up(parts * sizeof(float2)) + parts * c.dv * sizeof(float);
+}
 
 hipError_t launch_attend(const Cache& c, int32_t heads, int32_t k, float scale, const void* q,
                          const void* k_pages, const float* k_scale, const void* v_pages,
                          const float* v_scale, const int32_t* table, const int32_t* lengths,
-                         const int32_t* idx, void* out, float* lse, void*, hipStream_t st) {
+                         const int32_t* idx, void* out, float* lse, void* ws, hipStream_t st) {
+  if (c.latent()) {
+    const dim3 grid(heads, c.rows);
+    const auto* qq = static_cast<const uint16_t*>(q);
+    auto* o = static_cast<uint16_t*>(out);
+    if (c.dtype == kFP8)
+      attend_latent_kernel<576, 512, kFP8, true><<<grid, 256, 0, st>>>(
+          c, heads, k, scale, qq, k_pages, k_scale, v_pages, v_scale, table, lengths, idx, o, lse);
+    else
+      attend_latent_kernel<576, 512, kBF16, true><<<grid, 256, 0, st>>>(
+          c, heads, k, scale, qq, k_pages, k_scale, v_pages, v_scale, table, lengths, idx, o, lse);
+    return hipGetLastError();
+  }
+  const Plan p = plan(c, heads, k);
+  Args a{};
+  a.q = static_cast<const uint16_t*>(q);
+  a.k_pages = static_cast<const uint8_t*>(k_pages);
+  a.k_scale = k_scale;
+  a.v_pages = static_cast<const uint8_t*>(v_pages);
+  a.v_scale = v_scale;
+  a.table = table;
+  a.lengths = lengths;
+  a.idx = idx;
+  a.out = static_cast<uint16_t*>(out);
+  a.lse = lse;
+  const size_t parts = static_cast<size_t>(c.rows) * heads * p.splits;
+  a.part_ml = static_cast<float2*>(ws);
+  a.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + align_up(parts * sizeof(float2)));
+  a.heads = heads;
+  a.share = heads / c.kv_heads;
+  a.k = k;
+  a.splits = p.splits;
+  a.row_pages = c.row_pages;
+  a.pages = c.pages;
+  a.kv_heads = c.kv_heads;
+  a.scale2 = scale * kLog2e;
+  a.div = make_div(c.P);
   switch (c.dk) {
-    case 64:
-      return launch_dims<64, 64, false>(c, heads, k, scale, q, k_pages, k_scale, v_pages, v_scale,
-                                        table, lengths, idx, out, lse, st);
-    case 128:
-      return launch_dims<128, 128, false>(c, heads, k, scale, q, k_pages, k_scale, v_pages, v_scale,
-                                          table, lengths, idx, out, lse, st);
-    case 256:
-      return launch_dims<256, 256, false>(c, heads, k, scale, q, k_pages, k_scale, v_pages, v_scale,
-                                          table, lengths, idx, out, lse, st);
-    default:
-      return launch_dims<576, 512, true>(c, heads, k, scale, q, k_pages, k_scale, v_pages, v_scale,
-                                         table, lengths, idx, out, lse, st);
+    case 64: return launch_type<64>(c, a, p, st);
+    case 128: return launch_type<128>(c, a, p, st);
+    default: return launch_type<256>(c, a, p, st);
   }
 }
 
