@@ -11,6 +11,8 @@ namespace misa {
 namespace {
 
 typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
+typedef __attribute__((ext_vector_type(4))) short s16x4;
+typedef __attribute__((ext_vector_type(2))) int i32x2;
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -46,7 +48,7 @@ struct Args {
   float* lse;
   float* part_o;   // [rows, heads, splits, dv] unnormalised sums of a split
   float2* part_ml;  // [rows, heads, splits] maximum (log2) and sum
-  int32_t heads, share, k, splits, row_pages, pages, kv_heads;
+  int32_t rows, heads, share, k, splits, row_pages, pages, kv_heads;
   float scale2;  // scale * log2(e): softmax by powers of two
   Div div;
 };
@@ -120,6 +122,14 @@ __device__ __forceinline__ int value_dim(int c, int j) {
   return (j / per) * 16 * per + c * per + j % per;
 }
 
+// What the sums of a part with maximum m and sum l count under the common
+// maximum.  A part without tokens counts nothing; a NaN sum without a maximum
+// (every score NaN) stays one.
+__device__ __forceinline__ float part_factor(float m, float l, float mall) {
+  if (m == -INFINITY) return l == 0.f ? 0.f : 1.f;
+  return __builtin_amdgcn_exp2f(m - mall);
+}
+
 // log of the sum of exponentials from its log2 maximum and scaled sum.
 __device__ __forceinline__ float final_lse(float m, float l) {
   return (m == -INFINITY ? 0.f : m * kLn2) + __logf(l);
@@ -160,7 +170,7 @@ __global__ __launch_bounds__(256) void attend_kernel(Args a) {
   __shared__ __attribute__((aligned(16))) Shared sh;
   __shared__ float top[4][RT][16];
 
-  const int lane = lane_id(), wave = threadIdx.x / kWave;
+  const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int c = lane & 15, g = lane >> 4;
   const int split = blockIdx.x, row = blockIdx.z;
   const int chunks = (a.share + 16 * RT - 1) / (16 * RT);
@@ -361,12 +371,10 @@ __global__ __launch_bounds__(256) void attend_kernel(Args a) {
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
     mall[r] = fmaxf(fmaxf(top[0][r][c], top[1][r][c]), fmaxf(top[2][r][c], top[3][r][c]));
-    const float f = mall[r] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m[r] - mall[r]);
-    if (m[r] != -INFINITY || l[r] != 0.f) {  // a NaN sum under no maximum stays one
-      l[r] *= mall[r] == -INFINITY ? 1.f : f;
+    const float f = part_factor(m[r], l[r], mall[r]);
+    l[r] *= f;
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) acc[r][j] *= mall[r] == -INFINITY ? 1.f : f;
-    }
+    for (int j = 0; j < NJ; ++j) acc[r][j] *= f;
   }
 #pragma unroll
   for (int step = 2; step >= 1; step >>= 1) {
@@ -443,11 +451,10 @@ __global__ __launch_bounds__(256) void attend_join_kernel(Args a) {
   for (int s = lane; s < n; s += kWave) m = fmaxf(m, ml[s].x);
 #pragma unroll
   for (int o = 1; o < kWave; o <<= 1) m = fmaxf(m, __shfl_xor(m, o, kWave));
-  const float mb = m == -INFINITY ? 0.f : m;
   float l = 0.f, o[E] = {};
   for (int s = 0; s < n; ++s) {
     const float2 x = ml[s];
-    const float f = x.x == -INFINITY && x.y == 0.f ? 0.f : x.x == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(x.x - mb);
+    const float f = part_factor(x.x, x.y, m);
     l += x.y * f;
     const float* src = a.part_o + (at * a.splits + s) * D + lane * E;
 #pragma unroll
@@ -462,93 +469,272 @@ __global__ __launch_bounds__(256) void attend_join_kernel(Args a) {
 
 // ---------------------------------------------------------------- latent rows
 
-constexpr int kTile = 256;  // tokens per pass: one per thread
+constexpr int kLatentK = 576, kLatentV = 512;
+constexpr int kLatentHeads = 64;  // query heads of a workgroup
+constexpr int kLatentStage = 512;  // tokens whose slots are in LDS at a time
 
-// One workgroup per (head, row): scores of 256 tokens, one per thread, then
-// the running maximum and sum, then the values, two dimensions per thread.
-template <int DK, int DV, int DT, bool LATENT>
-__global__ __launch_bounds__(256) void attend_latent_kernel(
-    Cache c, int32_t heads, int32_t k, float scale, const uint16_t* __restrict__ q,
-    const void* __restrict__ k_pages, const float* __restrict__ k_scale,
-    const void* __restrict__ v_pages, const float* __restrict__ v_scale,
-    const int32_t* __restrict__ table, const int32_t* __restrict__ lengths,
-    const int32_t* __restrict__ idx, uint16_t* __restrict__ out, float* __restrict__ lse) {
-  __shared__ float qs[DK];
-  __shared__ float ps[kTile];
-  __shared__ int64_t slots[kTile];
-  __shared__ float red[4];
-  const int row = blockIdx.y, head = blockIdx.x;
-  const int kvh = head / (heads / c.kv_heads);
-  const int64_t qat = (static_cast<int64_t>(row) * heads + head);
-  for (int e = threadIdx.x; e < DK; e += 256) qs[e] = bf16_bits_to_f32(q[qat * DK + e]);
-  const int32_t len = min(lengths[row], c.row_pages * c.P);
-  const int32_t todo = k > 0 ? k : len;
-  float m = -INFINITY, l = 0.f, o[2] = {0.f, 0.f};
-  for (int32_t t0 = 0; t0 < todo; t0 += kTile) {
-    __syncthreads();
-    const int32_t t = t0 + threadIdx.x;
-    int32_t s = t < todo ? (k > 0 ? idx[static_cast<int64_t>(row) * k + t] : t) : -1;
-    int64_t slot = -1;
-    if (s >= 0 && s < len) {
-      const int32_t page = table[static_cast<int64_t>(row) * c.row_pages + s / c.P];
-      if (page >= 0 && page < c.pages)
-        slot = (static_cast<int64_t>(page) * c.kv_heads + kvh) * c.P + s % c.P;
+// One workgroup of eight waves per (split, 64 query heads, row): waves 0-3 and
+// 4-7 are two token groups, and wave w of a group has the query heads 16 (w %
+// 4) .. +15.  A group's tile of 32 cached rows goes to LDS once, by direct
+// loads into one of two buffers while the other is worked on, and its four
+// waves read it twice: as K for the scores, and its first 512 elements, by
+// transposing reads, as V^T.  The products are those of attend_kernel.
+//
+// LDS rows are 72 (bf16) or 36 (fp8) chunks of 16 bytes without padding, since
+// a direct load fills 64 consecutive chunks; chunk x of row r sits at x ^ swz(r),
+// which spreads the 16 rows that a score fragment reads over all banks.
+template <int DT>
+__global__ __launch_bounds__(512) void attend_latent_kernel(Args a) {
+  constexpr bool kFp8 = DT == kFP8;
+  constexpr int EB = kFp8 ? 1 : 2;
+  constexpr int CH = kLatentK * EB / 16;     // chunks of a cached row
+  constexpr int KU = kLatentK * EB / 64;     // key chunks per lane
+  constexpr int KS = kLatentK / 32;          // matrix steps of a score
+  constexpr int NJ = kLatentV / 16;
+  constexpr int QL = 3;  // query fragments in LDS: in registers they spill
+  struct Shared {
+    union {
+      uint4 tile[2][2][32 * CH];    // [buffer][token group]
+      float red[NJ * 4][4][kWave];  // group 1's sums, at the end
+    };
+    uint4 q[4][QL][kWave];
+    uint32_t slot[kLatentStage];
+    float ks[kFp8 ? kLatentStage : 4];
+    float top[4][16], sum[4][16];
+  };
+  __shared__ Shared sh;
+
+  const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int c = lane & 15, g = lane >> 4;
+  const int hw = wave & 3, grp = wave >> 2;
+  // Workgroups go round the 8 XCDs: the head chunks of one (row, split) are 8
+  // apart, on one XCD, so that the second reads the cache rows from its L2.
+  const int chunks = (a.heads + kLatentHeads - 1) / kLatentHeads;
+  const int chunk = blockIdx.x / 8 % chunks;
+  const int unit = blockIdx.x / (8 * chunks) * 8 + blockIdx.x % 8;
+  const int row = unit / a.splits, split = unit - row * a.splits;
+  if (row >= a.rows) return;
+  const int head0 = chunk * kLatentHeads + hw * 16;
+  int32_t len;
+  const int32_t todo = tokens_of(a, row, len);
+  const int32_t per = tiles_per_split(todo, a.splits) * kTileTokens;
+  const int32_t t0 = split * per, t1 = min(t0 + per, todo);
+  if (t0 >= t1 && split > 0) return;
+
+  bf16x8 qf[KS - QL];
+  {
+    const int h = head0 + c < a.heads ? head0 + c : 0;
+    const uint16_t* src = a.q + (static_cast<int64_t>(row) * a.heads + h) * kLatentK;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      const int d0 = kFp8 ? 64 * (s / 2) + 16 * g + 8 * (s % 2) : 32 * s + 8 * g;
+      const uint4 x = *reinterpret_cast<const uint4*>(src + d0);
+      if (s < KS - QL)
+        qf[s] = as_bf16x8(x);
+      else if (grp == 0)
+        sh.q[hw][s - (KS - QL)][lane] = x;
     }
-    float score = -INFINITY;
-    if (slot >= 0) {
-      float dot = 0.f;
-      for (int e = 0; e < DK; ++e) dot += qs[e] * load_elem<DT>(k_pages, slot * DK + e);
-      if (DT == kFP8) dot *= k_scale[slot];
-      score = dot * scale;
+  }
+  auto query = [&](int s) {
+    return s < KS - QL ? qf[s < KS - QL ? s : 0] : as_bf16x8(sh.q[hw][s < KS - QL ? 0 : s - (KS - QL)][lane]);
+  };
+  f32x4 acc[NJ];
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  float m = -INFINITY, l = 0.f;
+
+  auto swz = [](int r) { return kFp8 ? (r >> 2) & 3 : (r >> 1) & 7; };
+  // The group's four waves load its tile of pair `it` into buffer it % 2.
+  auto issue = [&](int it) {
+    const int first = (2 * it + grp) * 32;
+    uint4* buf = sh.tile[it & 1][grp];
+    int ln = lane;
+    asm volatile("" : "+v"(ln));  // addresses are computed here each time: kept over the loop they cost registers
+#pragma unroll
+    for (int n = 0; n < (CH / 2 + 3) / 4; ++n) {
+      const int i = n * 4 + hw;  // 64 chunks each
+      if (i < CH / 2) {
+        const int p = i * 64 + ln;
+        const int r = (p / (CH / 9)) * 57 >> 9;  // p / CH: x * 57 >> 9 = x / 9 below 288
+        const int x = (p - r * CH) ^ swz(r);
+        const uint32_t s = sh.slot[first + r];
+        const uint8_t* src = a.k_pages + static_cast<uint64_t>(s == kHidden ? 0 : s) * (kLatentK * EB) + x * 16;
+        __builtin_amdgcn_global_load_lds(
+            (const __attribute__((address_space(1))) void*)src,
+            (__attribute__((address_space(3))) void*)(buf + i * 64), 16, 0, 0);
+      }
     }
-    float top = score;
-#pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) top = fmaxf(top, __shfl_xor(top, d, kWave));
-    if (lane_id() == 0) red[threadIdx.x / kWave] = top;
+  };
+
+  // LDS bytes of this lane's first key and value chunks.  A row is a multiple
+  // of 8 (fp8: 4) chunks, so the swizzled bits of an address are 4-6 (4-5), and
+  // a step within those bits is an exclusive or; every other step is an
+  // immediate offset.
+  constexpr int kVStep = 16 * EB;  // bytes of 16 dimensions
+  const int koff = c * CH * 16 + ((g ^ swz(c)) * 16);
+  int voff;  // the row that this lane reads for its 16 lanes' transposed 4 x 16 (fp8: 8 x 16)
+  if constexpr (kFp8) {
+    const int i = c / 2, r = (i / 4) * 16 + 4 * g + i % 4;
+    voff = r * CH * 16 + swz(r) * 16 + c % 2 * 8;
+  } else {
+    const int r = 4 * g + c / 4;
+    voff = r * CH * 16 + ((c / 2 % 2) ^ swz(r)) * 16 + c % 2 * 8;
+  }
+
+  for (int32_t base = t0; base < t1; base += kLatentStage) {
+    const int32_t count = min(kLatentStage, t1 - base);
+    const int32_t pairs = (count + 63) / 64;
+    if (base != t0) __syncthreads();
+    for (int32_t i = threadIdx.x; i < pairs * 64; i += 512) {
+      const uint32_t s = i < count ? slot_of(a, row, 0, len, base + i) : kHidden;
+      sh.slot[i] = s;
+      if constexpr (kFp8) sh.ks[i] = s == kHidden ? 0.f : a.k_scale[s];
+    }
     __syncthreads();
-    top = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-    const float mn = fmaxf(m, top);
-    const float base = mn == -INFINITY ? 0.f : mn;
-    const float a = expf(m - base);
-    const float p = slot >= 0 ? expf(score - base) : 0.f;
-    ps[threadIdx.x] = p;
-    slots[threadIdx.x] = slot;
-    float sum = p;
+    issue(0);
+    for (int32_t it = 0; it < pairs; ++it) {
+      __builtin_amdgcn_s_waitcnt(0x0F70);  // this wave's loads have landed ...
+      __syncthreads();                     // ... and every wave's, and the other buffer is free
+      if (it + 1 < pairs) issue(it + 1);
+      if (__any(sh.slot[2 * it * 32 + lane] == kHidden)) {
+        // Hidden slots may hold anything, and 0 * NaN must not reach O: clear
+        // their rows.  Both tiles are looked at: all eight waves agree.
+        for (int r = hw; r < 32; r += 4)
+          if (sh.slot[(2 * it + grp) * 32 + r] == kHidden)
+            for (int x = lane; x < CH; x += kWave) sh.tile[it & 1][grp][r * CH + x] = make_uint4(0, 0, 0, 0);
+        __syncthreads();
+      }
+      const uint8_t* buf = reinterpret_cast<const uint8_t*>(sh.tile[it & 1][grp]);
+      const int first = (2 * it + grp) * 32;
+      f32x4 st[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) sum += __shfl_xor(sum, d, kWave);
-    __syncthreads();
-    if (lane_id() == 0) red[threadIdx.x / kWave] = sum;
-    __syncthreads();
-    l = l * a + red[0] + red[1] + red[2] + red[3];
-    m = mn;
-    o[0] *= a;
-    o[1] *= a;
-    for (int i = 0; i < min(kTile, todo - t0); ++i) {
-      const int64_t sl = slots[i];
-      if (sl < 0) continue;
-      float w = ps[i];
-      if (DT == kFP8) w *= LATENT ? k_scale[sl] : v_scale[sl];
+      for (int u = 0; u < KU; ++u)
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int e = u * 256 + threadIdx.x;
-        if (e < DV)
-          o[u] += w * (LATENT ? load_elem<DT>(k_pages, sl * DK + e) : load_elem<DT>(v_pages, sl * DV + e));
+        for (int h = 0; h < 2; ++h) {
+          const uint4 x = *reinterpret_cast<const uint4*>(
+              buf + (koff ^ (kFp8 ? 0 : u % 2 * 64)) + 16 * h * CH * 16 + (kFp8 ? u : u / 2 * 2) * 64);
+          if constexpr (kFp8) {
+            st[h] = mfma16_bf16(fp8x8_to_bf16(x.x, x.y), query(2 * u), st[h]);
+            st[h] = mfma16_bf16(fp8x8_to_bf16(x.z, x.w), query(2 * u + 1), st[h]);
+          } else {
+            st[h] = mfma16_bf16(as_bf16x8(x), query(u), st[h]);
+          }
+        }
+      uint32_t sl[8];
+      float ks[8];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int at = first + 16 * h + 4 * g;
+        const uint4 x = *reinterpret_cast<const uint4*>(&sh.slot[at]);
+        sl[4 * h] = x.x; sl[4 * h + 1] = x.y; sl[4 * h + 2] = x.z; sl[4 * h + 3] = x.w;
+        if constexpr (kFp8) {
+          const float4 y = *reinterpret_cast<const float4*>(&sh.ks[at]);
+          ks[4 * h] = y.x; ks[4 * h + 1] = y.y; ks[4 * h + 2] = y.z; ks[4 * h + 3] = y.w;
+        }
+      }
+      float x[8], high = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float y = st[i / 4][i % 4] * a.scale2;
+        if constexpr (kFp8) y *= ks[i];
+        x[i] = sl[i] == kHidden ? -INFINITY : y;
+        high = fmaxf(high, x[i]);
+      }
+      if (__any(high > m)) {
+        high = fmaxf(high, __shfl_xor(high, 16, kWave));
+        high = fmaxf(high, __shfl_xor(high, 32, kWave));
+        const float next = fmaxf(m, high);
+        const float f = next == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - next);
+        m = next;
+        l *= f;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) acc[j] *= f;
+      }
+      const float mb = m == -INFINITY ? 0.f : m;
+      bf16x8 ph, pl;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float p = __builtin_amdgcn_exp2f(x[i] - mb);
+        l += p;
+        const float w = kFp8 ? p * ks[i] : p;
+        const __bf16 hi = static_cast<__bf16>(w);
+        ph[i] = hi;
+        pl[i] = static_cast<__bf16>(w - static_cast<float>(hi));
+      }
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        const uint8_t* p = buf + (voff ^ (j % 4 * kVStep)) + j / 4 * (4 * kVStep);
+        bf16x8 v;
+        if constexpr (kFp8) {
+          const i32x2 y = __builtin_amdgcn_ds_read_tr8_b64_v2i32((__attribute__((address_space(3))) i32x2*)p);
+          v = fp8x8_to_bf16(y[0], y[1]);
+        } else {
+          const s16x4 y0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)p);
+          const s16x4 y1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              (__attribute__((address_space(3))) s16x4*)(p + 16 * CH * 16));
+          v = __builtin_bit_cast(bf16x8, __builtin_shufflevector(y0, y1, 0, 1, 2, 3, 4, 5, 6, 7));
+        }
+        acc[j] = mfma16_bf16(v, ph, acc[j]);
+        acc[j] = mfma16_bf16(v, pl, acc[j]);
       }
     }
   }
+
+  // Join the two token groups: group 1 hands its sums to group 0 through LDS.
+  l += __shfl_xor(l, 16, kWave);
+  l += __shfl_xor(l, 32, kWave);
+  __syncthreads();
+  if (grp == 1) {
+    if (g == 0) {
+      sh.top[hw][c] = m;
+      sh.sum[hw][c] = l;
+    }
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const int e = u * 256 + threadIdx.x;
-    if (e < DV)
-      reinterpret_cast<__bf16*>(out)[qat * DV + e] = static_cast<__bf16>(l > 0.f || l != l ? o[u] / l : 0.f);
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sh.red[4 * j + e][hw][lane] = acc[j][e];
   }
-  if (lse && threadIdx.x == 0) lse[qat] = m == -INFINITY ? -INFINITY : m + logf(l);
+  __syncthreads();
+  if (grp == 1 || head0 + c >= a.heads) return;
+  const float m1 = sh.top[hw][c], l1 = sh.sum[hw][c];
+  const float mall = fmaxf(m, m1);
+  const float f0 = part_factor(m, l, mall), f1 = part_factor(m1, l1, mall);
+  const float lall = l * f0 + l1 * f1;
+  const int64_t at = static_cast<int64_t>(row) * a.heads + head0 + c;
+  const float inv = a.splits > 1 ? 1.f : lall == 0.f ? 0.f : 1.f / lall;
+  const int64_t part = at * a.splits + split;
+  if (g == 0) {
+    if (a.splits > 1)
+      a.part_ml[part] = make_float2(mall, lall);
+    else if (a.lse)
+      a.lse[at] = lall == 0.f ? -INFINITY : final_lse(mall, lall);
+  }
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    const int d = 16 * j + 4 * g;
+    float o[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] = (acc[j][e] * f0 + sh.red[4 * j + e][hw][lane] * f1) * inv;
+    if (a.splits > 1) {
+      *reinterpret_cast<float4*>(a.part_o + part * kLatentV + d) = make_float4(o[0], o[1], o[2], o[3]);
+    } else {
+      bf16x2 y[2];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[e / 2][e % 2] = static_cast<__bf16>(o[e]);
+      *reinterpret_cast<uint2*>(a.out + at * kLatentV + d) =
+          make_uint2(__builtin_bit_cast(uint32_t, y[0]), __builtin_bit_cast(uint32_t, y[1]));
+    }
+  }
 }
 
 constexpr int kMinSplitTokens = 128;  // a split gives each wave a tile
 
-// Query heads per workgroup / 16.
-int row_tiles(const Cache& c, int32_t share) { return share > 16 && c.dk <= 128 ? 2 : 1; }
+// Query heads of a workgroup: a matrix tile of 16, or two where a kv head has
+// more and the registers hold them.
+int group_heads(const Cache& c, int32_t share) {
+  if (c.latent()) return kLatentHeads;
+  return share > 16 && c.dk <= 128 ? 32 : 16;
+}
 
 struct Plan {
   int32_t chunks, splits;
@@ -556,12 +742,12 @@ struct Plan {
 
 Plan plan(const Cache& c, int32_t heads, int32_t k) {
   const int32_t share = heads / c.kv_heads;
-  const int32_t per = 16 * row_tiles(c, share);
+  const int32_t per = group_heads(c, share);
   Plan p;
   p.chunks = (share + per - 1) / per;
   const int64_t groups = static_cast<int64_t>(c.rows) * c.kv_heads * p.chunks;
   const int64_t most = k > 0 ? k : static_cast<int64_t>(c.row_pages) * c.P;
-  int64_t s = (1024 + groups - 1) / groups;
+  int64_t s = c.latent() ? (k > 0 ? 256 : 512) / groups : (1024 + groups - 1) / groups;
   s = std::min<int64_t>(s, (most + kMinSplitTokens - 1) / kMinSplitTokens);
   p.splits = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(s, 128)));
   return p;
@@ -571,7 +757,7 @@ template <int D, int DT>
 hipError_t launch_dim(const Cache& c, const Args& a, const Plan& p, hipStream_t st) {
   const dim3 grid(p.splits, c.kv_heads * p.chunks, c.rows);
   if constexpr (D <= 128) {
-    if (row_tiles(c, a.share) == 2)
+    if (group_heads(c, a.share) == 32)
       attend_kernel<D, DT, 2><<<grid, 256, 0, st>>>(a);
     else
       attend_kernel<D, DT, 1><<<grid, 256, 0, st>>>(a);
@@ -584,6 +770,19 @@ hipError_t launch_dim(const Cache& c, const Args& a, const Plan& p, hipStream_t 
   return hipGetLastError();
 }
 
+hipError_t launch_latent(const Cache& c, const Args& a, const Plan& p, hipStream_t st) {
+  const int64_t units = (static_cast<int64_t>(c.rows) * p.splits + 7) / 8 * 8;
+  const uint32_t grid = static_cast<uint32_t>(units * p.chunks);
+  if (c.dtype == kFP8)
+    attend_latent_kernel<kFP8><<<grid, 512, 0, st>>>(a);
+  else
+    attend_latent_kernel<kBF16><<<grid, 512, 0, st>>>(a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.splits == 1) return e;
+  attend_join_kernel<kLatentV><<<dim3((a.heads + 3) / 4, c.rows), 256, 0, st>>>(a);
+  return hipGetLastError();
+}
+
 template <int D>
 hipError_t launch_type(const Cache& c, const Args& a, const Plan& p, hipStream_t st) {
   return c.dtype == kFP8 ? launch_dim<D, kFP8>(c, a, p, st) : launch_dim<D, kBF16>(c, a, p, st);
@@ -592,7 +791,6 @@ hipError_t launch_type(const Cache& c, const Args& a, const Plan& p, hipStream_t
 }  // namespace
 
 size_t attend_ws_bytes(const Cache& c, int32_t heads, int32_t k) {
-  if (c.latent()) return 0;
   const Plan p = plan(c, heads, k);
   if (p.splits == 1) return 0;
   const size_t parts = static_cast<size_t>(c.rows) * heads * p.splits;
@@ -603,18 +801,6 @@ hipError_t launch_attend(const Cache& c, int32_t heads, int32_t k, float scale, 
                          const void* k_pages, const float* k_scale, const void* v_pages,
                          const float* v_scale, const int32_t* table, const int32_t* lengths,
                          const int32_t* idx, void* out, float* lse, void* ws, hipStream_t st) {
-  if (c.latent()) {
-    const dim3 grid(heads, c.rows);
-    const auto* qq = static_cast<const uint16_t*>(q);
-    auto* o = static_cast<uint16_t*>(out);
-    if (c.dtype == kFP8)
-      attend_latent_kernel<576, 512, kFP8, true><<<grid, 256, 0, st>>>(
-          c, heads, k, scale, qq, k_pages, k_scale, v_pages, v_scale, table, lengths, idx, o, lse);
-    else
-      attend_latent_kernel<576, 512, kBF16, true><<<grid, 256, 0, st>>>(
-          c, heads, k, scale, qq, k_pages, k_scale, v_pages, v_scale, table, lengths, idx, o, lse);
-    return hipGetLastError();
-  }
   const Plan p = plan(c, heads, k);
   Args a{};
   a.q = static_cast<const uint16_t*>(q);
@@ -630,6 +816,7 @@ hipError_t launch_attend(const Cache& c, int32_t heads, int32_t k, float scale, 
   const size_t parts = static_cast<size_t>(c.rows) * heads * p.splits;
   a.part_ml = static_cast<float2*>(ws);
   a.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + align_up(parts * sizeof(float2)));
+  a.rows = c.rows;
   a.heads = heads;
   a.share = heads / c.kv_heads;
   a.k = k;
@@ -639,6 +826,7 @@ hipError_t launch_attend(const Cache& c, int32_t heads, int32_t k, float scale, 
   a.kv_heads = c.kv_heads;
   a.scale2 = scale * kLog2e;
   a.div = make_div(c.P);
+  if (c.latent()) return launch_latent(c, a, p, st);
   switch (c.dk) {
     case 64: return launch_type<64>(c, a, p, st);
     case 128: return launch_type<128>(c, a, p, st);
