@@ -16,6 +16,10 @@ typedef __attribute__((ext_vector_type(2))) int i32x2;
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+// The sums are rescaled to a new maximum only when a score exceeds the old one
+// by this much (log2): until then weights go up to 2^8, which loses nothing in
+// fp32 and in the weights' bf16 parts, and O's registers are left alone.
+constexpr float kSlack = 8.f;
 constexpr uint32_t kHidden = 0xFFFFFFFFu;  // the slot of a token that is not visible
 
 // n / P for 0 <= n < 2^31 by a multiplication: with l = ceil(log2 P), m =
@@ -130,6 +134,20 @@ __device__ __forceinline__ float part_factor(float m, float l, float mall) {
   return __builtin_amdgcn_exp2f(m - mall);
 }
 
+// Reductions over the four lane groups of a query head (lanes l % 16 alike).
+__device__ __forceinline__ float groups_max(float x) {
+  auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float groups_sum(float x) {
+  auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
 // log of the sum of exponentials from its log2 maximum and scaled sum.
 __device__ __forceinline__ float final_lse(float m, float l) {
   return (m == -INFINITY ? 0.f : m * kLn2) + __logf(l);
@@ -197,7 +215,7 @@ __global__ __launch_bounds__(256) void attend_kernel(Args a) {
   }
 
   f32x4 acc[RT][NJ];
-  float m[RT], l[RT];  // maximum of the head (all lanes alike), this lane's part of the sum
+  float m[RT], l[RT];  // reference maximum of the head (all lanes alike), this lane's part of the sum
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
     m[r] = -INFINITY;
@@ -307,10 +325,8 @@ __global__ __launch_bounds__(256) void attend_kernel(Args a) {
           x[i] = sl[i] == kHidden ? -INFINITY : y;
           high = fmaxf(high, x[i]);
         }
-        if (__any(high > m[r])) {  // wave-uniform: a new maximum somewhere
-          high = fmaxf(high, __shfl_xor(high, 16, kWave));
-          high = fmaxf(high, __shfl_xor(high, 32, kWave));
-          const float next = fmaxf(m[r], high);
+        if (__any(high > m[r] + kSlack)) {  // wave-uniform
+          const float next = fmaxf(m[r], groups_max(high));
           const float f = next == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m[r] - next);
           m[r] = next;
           l[r] *= f;
@@ -362,8 +378,7 @@ __global__ __launch_bounds__(256) void attend_kernel(Args a) {
   // Join the four waves: common maximum, then a tree through LDS into wave 0.
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
-    l[r] += __shfl_xor(l[r], 16, kWave);
-    l[r] += __shfl_xor(l[r], 32, kWave);
+    l[r] = groups_sum(l[r]);
     if (g == 0) top[wave][r][c] = m[r];
   }
   __syncthreads();
@@ -434,13 +449,16 @@ __global__ __launch_bounds__(256) void attend_kernel(Args a) {
   }
 }
 
-// The splits of one (row, head), joined by one wave in split order.
+// The splits of one (row, head) joined by one workgroup: D / 4 threads hold
+// four dimensions each, and 1024 / D groups of them take every such split; the
+// groups' sums are added in order.
 template <int D>
 __global__ __launch_bounds__(256) void attend_join_kernel(Args a) {
-  constexpr int E = D / 64;
-  const int lane = lane_id();
-  const int head = blockIdx.x * 4 + threadIdx.x / kWave, row = blockIdx.y;
-  if (head >= a.heads) return;
+  constexpr int T = D / 4, GS = 256 / T;
+  __shared__ float4 sums[GS][T];
+  __shared__ float total[GS];
+  const int head = blockIdx.x, row = blockIdx.y;
+  const int d = threadIdx.x % T, grp = threadIdx.x / T;
   int32_t len;
   const int32_t todo = tokens_of(a, row, len);
   const int32_t per = tiles_per_split(todo, a.splits) * kTileTokens;
@@ -448,23 +466,47 @@ __global__ __launch_bounds__(256) void attend_join_kernel(Args a) {
   const int64_t at = static_cast<int64_t>(row) * a.heads + head;
   const float2* ml = a.part_ml + at * a.splits;
   float m = -INFINITY;
-  for (int s = lane; s < n; s += kWave) m = fmaxf(m, ml[s].x);
+  for (int s = lane_id(); s < n; s += kWave) m = fmaxf(m, ml[s].x);
 #pragma unroll
   for (int o = 1; o < kWave; o <<= 1) m = fmaxf(m, __shfl_xor(m, o, kWave));
-  float l = 0.f, o[E] = {};
-  for (int s = 0; s < n; ++s) {
+  const float4* src = reinterpret_cast<const float4*>(a.part_o + at * a.splits * D) + d;
+  float l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int s = grp; s < n; s += GS) {
     const float2 x = ml[s];
+    const float4 y = src[static_cast<int64_t>(s) * T];
     const float f = part_factor(x.x, x.y, m);
     l += x.y * f;
-    const float* src = a.part_o + (at * a.splits + s) * D + lane * E;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] += src[e] * f;
+    o.x += y.x * f;
+    o.y += y.y * f;
+    o.z += y.z * f;
+    o.w += y.w * f;
   }
+  if (n > 1) {  // with one split, group 0 has it all
+    sums[grp][d] = o;
+    if (d == 0) total[grp] = l;
+    __syncthreads();
+    if (grp != 0) return;
+    for (int i = 1; i < min(GS, n); ++i) {
+      const float4 y = sums[i][d];
+      l += total[i];
+      o.x += y.x;
+      o.y += y.y;
+      o.z += y.z;
+      o.w += y.w;
+    }
+  }
+  if (grp != 0) return;
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  if (lane == 0 && a.lse) a.lse[at] = l == 0.f ? -INFINITY : final_lse(m, l);
-#pragma unroll
-  for (int e = 0; e < E; ++e)
-    reinterpret_cast<__bf16*>(a.out)[at * D + lane * E + e] = static_cast<__bf16>(o[e] * inv);
+  if (d == 0 && a.lse) a.lse[at] = l == 0.f ? -INFINITY : final_lse(m, l);
+  bf16x2 y0, y1;
+  y0[0] = static_cast<__bf16>(o.x * inv);
+  y0[1] = static_cast<__bf16>(o.y * inv);
+  y1[0] = static_cast<__bf16>(o.z * inv);
+  y1[1] = static_cast<__bf16>(o.w * inv);
+  *reinterpret_cast<uint2*>(a.out + at * D + 4 * d) =
+      make_uint2(__builtin_bit_cast(uint32_t, y0), __builtin_bit_cast(uint32_t, y1));
 }
 
 // ---------------------------------------------------------------- latent rows
@@ -491,7 +533,8 @@ __global__ __launch_bounds__(512) void attend_latent_kernel(Args a) {
   constexpr int KU = kLatentK * EB / 64;     // key chunks per lane
   constexpr int KS = kLatentK / 32;          // matrix steps of a score
   constexpr int NJ = kLatentV / 16;
-  constexpr int QL = 3;  // query fragments in LDS: in registers they spill
+  constexpr int QL = 2;      // query fragments in LDS: in registers they spill
+  constexpr int kAhead = 4;  // LDS reads under way
   struct Shared {
     union {
       uint4 tile[2][2][32 * CH];    // [buffer][token group]
@@ -606,20 +649,47 @@ __global__ __launch_bounds__(512) void attend_latent_kernel(Args a) {
       }
       const uint8_t* buf = reinterpret_cast<const uint8_t*>(sh.tile[it & 1][grp]);
       const int first = (2 * it + grp) * 32;
+      // Scores.  Fragment f = 2u + h: 16 bytes of token half h; kAhead reads are
+      // under way (the barriers keep the compiler from undoing that).
+      auto key = [&](int f) {
+        const int u = f / 2, h = f % 2;
+        return *reinterpret_cast<const uint4*>(buf + (koff ^ (kFp8 ? 0 : u % 2 * 64)) + 16 * h * CH * 16 +
+                                               (kFp8 ? u : u / 2 * 2) * 64);
+      };
       f32x4 st[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
+      uint4 kb[kAhead];
 #pragma unroll
-      for (int u = 0; u < KU; ++u)
+      for (int f = 0; f < kAhead; ++f) kb[f] = key(f);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint4 x = *reinterpret_cast<const uint4*>(
-              buf + (koff ^ (kFp8 ? 0 : u % 2 * 64)) + 16 * h * CH * 16 + (kFp8 ? u : u / 2 * 2) * 64);
-          if constexpr (kFp8) {
-            st[h] = mfma16_bf16(fp8x8_to_bf16(x.x, x.y), query(2 * u), st[h]);
-            st[h] = mfma16_bf16(fp8x8_to_bf16(x.z, x.w), query(2 * u + 1), st[h]);
-          } else {
-            st[h] = mfma16_bf16(as_bf16x8(x), query(u), st[h]);
-          }
+      for (int f = 0; f < 2 * KU; ++f) {
+        const uint4 x = kb[f % kAhead];
+        if constexpr (kFp8) {
+          st[f % 2] = mfma16_bf16(fp8x8_to_bf16(x.x, x.y), query(f / 2 * 2), st[f % 2]);
+          st[f % 2] = mfma16_bf16(fp8x8_to_bf16(x.z, x.w), query(f / 2 * 2 + 1), st[f % 2]);
+        } else {
+          st[f % 2] = mfma16_bf16(as_bf16x8(x), query(f / 2), st[f % 2]);
         }
+        if (f + kAhead < 2 * KU) kb[f % kAhead] = key(f + kAhead);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      // V^T fragment j: 16 dimensions of this lane group's eight tokens.
+      auto value = [&](int j, uint4& v) {
+        const uint8_t* p = buf + (voff ^ (j % 4 * kVStep)) + j / 4 * (4 * kVStep);
+        if constexpr (kFp8) {
+          const i32x2 y = __builtin_amdgcn_ds_read_tr8_b64_v2i32((__attribute__((address_space(3))) i32x2*)p);
+          v.x = y[0];
+          v.y = y[1];
+        } else {
+          const s16x4 y0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)p);
+          const s16x4 y1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              (__attribute__((address_space(3))) s16x4*)(p + 16 * CH * 16));
+          v = __builtin_bit_cast(uint4, __builtin_shufflevector(y0, y1, 0, 1, 2, 3, 4, 5, 6, 7));
+        }
+      };
+      uint4 vb[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) value(j, vb[j]);
       uint32_t sl[8];
       float ks[8];
 #pragma unroll
@@ -640,10 +710,8 @@ __global__ __launch_bounds__(512) void attend_latent_kernel(Args a) {
         x[i] = sl[i] == kHidden ? -INFINITY : y;
         high = fmaxf(high, x[i]);
       }
-      if (__any(high > m)) {
-        high = fmaxf(high, __shfl_xor(high, 16, kWave));
-        high = fmaxf(high, __shfl_xor(high, 32, kWave));
-        const float next = fmaxf(m, high);
+      if (__any(high > m + kSlack)) {
+        const float next = fmaxf(m, groups_max(high));
         const float f = next == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - next);
         m = next;
         l *= f;
@@ -661,28 +729,21 @@ __global__ __launch_bounds__(512) void attend_latent_kernel(Args a) {
         ph[i] = hi;
         pl[i] = static_cast<__bf16>(w - static_cast<float>(hi));
       }
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
-        const uint8_t* p = buf + (voff ^ (j % 4 * kVStep)) + j / 4 * (4 * kVStep);
-        bf16x8 v;
-        if constexpr (kFp8) {
-          const i32x2 y = __builtin_amdgcn_ds_read_tr8_b64_v2i32((__attribute__((address_space(3))) i32x2*)p);
-          v = fp8x8_to_bf16(y[0], y[1]);
-        } else {
-          const s16x4 y0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)p);
-          const s16x4 y1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (__attribute__((address_space(3))) s16x4*)(p + 16 * CH * 16));
-          v = __builtin_bit_cast(bf16x8, __builtin_shufflevector(y0, y1, 0, 1, 2, 3, 4, 5, 6, 7));
-        }
+        const uint4 y = vb[j % kAhead];
+        const bf16x8 v = kFp8 ? fp8x8_to_bf16(y.x, y.y) : as_bf16x8(y);
         acc[j] = mfma16_bf16(v, ph, acc[j]);
         acc[j] = mfma16_bf16(v, pl, acc[j]);
+        if (j + kAhead < NJ) value(j + kAhead, vb[j % kAhead]);
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
   }
 
   // Join the two token groups: group 1 hands its sums to group 0 through LDS.
-  l += __shfl_xor(l, 16, kWave);
-  l += __shfl_xor(l, 32, kWave);
+  l = groups_sum(l);
   __syncthreads();
   if (grp == 1) {
     if (g == 0) {
@@ -766,7 +827,7 @@ hipError_t launch_dim(const Cache& c, const Args& a, const Plan& p, hipStream_t 
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
-  attend_join_kernel<D><<<dim3((a.heads + 3) / 4, c.rows), 256, 0, st>>>(a);
+  attend_join_kernel<D><<<dim3(a.heads, c.rows), 256, 0, st>>>(a);
   return hipGetLastError();
 }
 
@@ -779,7 +840,7 @@ hipError_t launch_latent(const Cache& c, const Args& a, const Plan& p, hipStream
     attend_latent_kernel<kBF16><<<grid, 512, 0, st>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
-  attend_join_kernel<kLatentV><<<dim3((a.heads + 3) / 4, c.rows), 256, 0, st>>>(a);
+  attend_join_kernel<kLatentV><<<dim3(a.heads, c.rows), 256, 0, st>>>(a);
   return hipGetLastError();
 }
 
