@@ -127,10 +127,26 @@ def _ptr(x):
     return x.data_ptr()
 
 
+_torch_device = _torch_stream = None
+
+
+def _current_device() -> int:
+    """torch's current device; its getters are looked up once (a Stream object for each call costs
+    as much as the call)."""
+    global _torch_device, _torch_stream
+    if _torch_device is None:
+        import torch
+        torch.cuda.init()
+        _torch_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda i: torch.cuda.current_stream(i).cuda_stream)
+        _torch_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    return _torch_device()
+
+
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        device = _current_device()
+        return _torch_stream(device)
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -221,6 +237,28 @@ def misa_hisa_score_topk(shp, h, m, k, q, q_scale, w, pooled, kk, k_scale, heads
 # ------------------------------------------------------------------ serving
 
 
+def _dev(x):
+    """Device address of a contiguous device tensor (or an int address, or None -> NULL)."""
+    if x is None or x.__class__ is int:
+        return x
+    if not (x.is_cuda and x.is_contiguous()):
+        raise ValueError("tensors must be contiguous and on the device")
+    return x.data_ptr()
+
+
+def _call(fn: str, tensor, args, stream):
+    """Calls the entry point on `stream`, by default the current one of `tensor`'s device, which is
+    the current device while the call is made."""
+    f = getattr(_lib, fn)
+    if stream is None and tensor.__class__ is not int and tensor is not None:
+        device = tensor.get_device()
+        if device != _current_device():
+            import torch
+            with torch.cuda.device(device):
+                return _check(f(*args, _stream(None)), fn)
+    _check(f(*args, _stream(stream)), fn)
+
+
 def cache(rows, row_pages, pages, page_tokens, kv_heads, dk, dv, kv_dtype) -> misa_cache:
     return misa_cache(rows, row_pages, pages, page_tokens, kv_heads, dk, dv, kv_dtype)
 
@@ -228,7 +266,7 @@ def cache(rows, row_pages, pages, page_tokens, kv_heads, dk, dv, kv_dtype) -> mi
 def page_buffers(buffers):
     """The `buffers` argument of misa_page_copy, from (data, planes, page_bytes) triples.  It holds
     addresses: the tensors must outlive it."""
-    return (misa_page_buffer * len(buffers))(*(misa_page_buffer(_ptr(d), b, p) for d, p, b in buffers))
+    return (misa_page_buffer * len(buffers))(*(misa_page_buffer(_dev(d), b, p) for d, p, b in buffers))
 
 
 def misa_attend_workspace_bytes(cache: misa_cache, heads: int, k: int) -> int:
@@ -237,34 +275,34 @@ def misa_attend_workspace_bytes(cache: misa_cache, heads: int, k: int) -> int:
 
 def misa_attend(cache, heads, k, scale, q, k_pages, k_scale, v_pages, v_scale, table, lengths, idx,
                 out, lse, ws, stream=None):
-    _check(_lib.misa_attend(ctypes.byref(cache), heads, k, scale, _ptr(q), _ptr(k_pages),
-                            _ptr(k_scale), _ptr(v_pages), _ptr(v_scale), _ptr(table),
-                            _ptr(lengths), _ptr(idx), _ptr(out), _ptr(lse), _ptr(ws),
-                            _nbytes(ws), _stream(stream)), "misa_attend")
+    _call("misa_attend", q, (
+        ctypes.byref(cache), heads, k, scale, _dev(q), _dev(k_pages), _dev(k_scale), _dev(v_pages),
+        _dev(v_scale), _dev(table), _dev(lengths), _dev(idx), _dev(out), _dev(lse), _dev(ws),
+        _nbytes(ws)), stream)
 
 
 def misa_page_write(cache, n, row, pos, k_new, v_new, k_pages, k_scale, v_pages, v_scale, table,
                     stream=None):
-    _check(_lib.misa_page_write(ctypes.byref(cache), n, _ptr(row), _ptr(pos), _ptr(k_new),
-                                _ptr(v_new), _ptr(k_pages), _ptr(k_scale), _ptr(v_pages),
-                                _ptr(v_scale), _ptr(table), _stream(stream)), "misa_page_write")
+    _call("misa_page_write", k_pages, (
+        ctypes.byref(cache), n, _dev(row), _dev(pos), _dev(k_new), _dev(v_new), _dev(k_pages),
+        _dev(k_scale), _dev(v_pages), _dev(v_scale), _dev(table)), stream)
 
 
 def misa_page_extend(cache, n, row, count, table, lengths, refs, ok, stream=None):
-    _check(_lib.misa_page_extend(ctypes.byref(cache), n, _ptr(row), _ptr(count), _ptr(table),
-                                 _ptr(lengths), _ptr(refs), _ptr(ok), _stream(stream)),
-           "misa_page_extend")
+    _call("misa_page_extend", table, (
+        ctypes.byref(cache), n, _dev(row), _dev(count), _dev(table), _dev(lengths), _dev(refs),
+        _dev(ok)), stream)
 
 
 def misa_page_fork(cache, n, parent, child, table, lengths, refs, src, dst, ok, stream=None):
-    _check(_lib.misa_page_fork(ctypes.byref(cache), n, _ptr(parent), _ptr(child), _ptr(table),
-                               _ptr(lengths), _ptr(refs), _ptr(src), _ptr(dst), _ptr(ok),
-                               _stream(stream)), "misa_page_fork")
+    _call("misa_page_fork", table, (
+        ctypes.byref(cache), n, _dev(parent), _dev(child), _dev(table), _dev(lengths), _dev(refs),
+        _dev(src), _dev(dst), _dev(ok)), stream)
 
 
 def misa_page_free(cache, n, row, table, lengths, refs, stream=None):
-    _check(_lib.misa_page_free(ctypes.byref(cache), n, _ptr(row), _ptr(table), _ptr(lengths),
-                               _ptr(refs), _stream(stream)), "misa_page_free")
+    _call("misa_page_free", table, (
+        ctypes.byref(cache), n, _dev(row), _dev(table), _dev(lengths), _dev(refs)), stream)
 
 
 def misa_page_workspace_bytes(cache: misa_cache) -> int:
@@ -272,19 +310,18 @@ def misa_page_workspace_bytes(cache: misa_cache) -> int:
 
 
 def misa_page_compact(cache, table, refs, table_out, refs_out, map, live, src, dst, ws, stream=None):
-    _check(_lib.misa_page_compact(ctypes.byref(cache), _ptr(table), _ptr(refs), _ptr(table_out),
-                                  _ptr(refs_out), _ptr(map), _ptr(live), _ptr(src), _ptr(dst),
-                                  _ptr(ws), _nbytes(ws), _stream(stream)), "misa_page_compact")
+    _call("misa_page_compact", table, (
+        ctypes.byref(cache), _dev(table), _dev(refs), _dev(table_out), _dev(refs_out), _dev(map),
+        _dev(live), _dev(src), _dev(dst), _dev(ws), _nbytes(ws)), stream)
 
 
 def misa_page_copy(buffers, pages, n, src, dst, stream=None):
     """`buffers`: what page_buffers() gives."""
-    _check(_lib.misa_page_copy(buffers, len(buffers), pages, n, _ptr(src), _ptr(dst),
-                               _stream(stream)), "misa_page_copy")
+    _call("misa_page_copy", src, (buffers, len(buffers), pages, n, _dev(src), _dev(dst)), stream)
 
 
 def misa_rms_norm(rows, n, groups, x_dtype, out_dtype, eps, x, residual, weight, sum_out, out,
                   out_scale, stream=None):
-    _check(_lib.misa_rms_norm(rows, n, groups, x_dtype, out_dtype, eps, _ptr(x), _ptr(residual),
-                              _ptr(weight), _ptr(sum_out), _ptr(out), _ptr(out_scale),
-                              _stream(stream)), "misa_rms_norm")
+    _call("misa_rms_norm", x, (
+        rows, n, groups, x_dtype, out_dtype, eps, _dev(x), _dev(residual), _dev(weight),
+        _dev(sum_out), _dev(out), _dev(out_scale)), stream)

@@ -74,6 +74,44 @@ __device__ __forceinline__ int wave_inclusive_sum(int v) {
   return v;
 }
 
+// Lane l's partner at step `o` of an all-reduction over neighbouring lanes (o =
+// 1, 2, 4, ... in order: the values of both halves of 2o lanes are alike by
+// then, so that a mirrored partner is as good as lane l ^ o): register moves
+// instead of LDS permutes.
+template <int O>
+__device__ __forceinline__ float lanes_partner(float x) {
+  const int u = __float_as_int(x);
+  if constexpr (O == 1) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(u, u, 0xB1, 0xF, 0xF, false));  // quad_perm 1 0 3 2
+  } else if constexpr (O == 2) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(u, u, 0x4E, 0xF, 0xF, false));  // quad_perm 2 3 0 1
+  } else if constexpr (O == 4) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(u, u, 0x141, 0xF, 0xF, false));  // row_half_mirror
+  } else if constexpr (O == 8) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(u, u, 0x140, 0xF, 0xF, false));  // row_mirror
+  } else if constexpr (O == 16) {
+    // Swaps the odd rows of one copy with the even rows of the other: one of
+    // the results is x itself, the other its partner.
+    const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    return __int_as_float((threadIdx.x & 16) ? r[0] : r[1]);
+  } else {
+    const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    return __int_as_float((threadIdx.x & 32) ? r[0] : r[1]);
+  }
+}
+
+// Sum (MAX: maximum, NaN left out) over N neighbouring lanes, known to all.
+template <int N, bool MAX>
+__device__ __forceinline__ float lanes_reduce(float x) {
+  if constexpr (N > 1) x = MAX ? fmaxf(x, lanes_partner<1>(x)) : x + lanes_partner<1>(x);
+  if constexpr (N > 2) x = MAX ? fmaxf(x, lanes_partner<2>(x)) : x + lanes_partner<2>(x);
+  if constexpr (N > 4) x = MAX ? fmaxf(x, lanes_partner<4>(x)) : x + lanes_partner<4>(x);
+  if constexpr (N > 8) x = MAX ? fmaxf(x, lanes_partner<8>(x)) : x + lanes_partner<8>(x);
+  if constexpr (N > 16) x = MAX ? fmaxf(x, lanes_partner<16>(x)) : x + lanes_partner<16>(x);
+  if constexpr (N > 32) x = MAX ? fmaxf(x, lanes_partner<32>(x)) : x + lanes_partner<32>(x);
+  return x;
+}
+
 // Block-wide exclusive prefix sum of `v` in thread order; `total` receives the
 // block sum.  `tmp` is LDS scratch of NT/64 ints.  Contains __syncthreads().
 template <int NT>
