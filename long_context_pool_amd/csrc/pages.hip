@@ -12,95 +12,92 @@ namespace {
 
 // ---------------------------------------------------------------- token writes
 
-// One subgroup of LPR lanes per (token, kv head, K or V): D elements, 8 per
-// lane and step, one 16-byte load each; fp8 reduces the largest magnitude over
-// the subgroup first.  Bound by memory traffic.
-template <int D, bool FP8>
+// One subgroup of LPR lanes per (token, kv head), which writes its K and its V
+// (LATENT: K alone): D elements, 8 per lane and step, one 16-byte load each; fp8
+// reduces the largest magnitude over the subgroup first.  Both rows' loads are
+// under way while three dependent loads find the slot.  Bound by memory
+// traffic: @WRITE@.
+template <int D, bool FP8, bool LATENT>
 __global__ __launch_bounds__(256) void page_write_kernel(
-    int64_t items, int32_t per_token, int32_t kv_heads, int32_t rows, int32_t row_pages,
-    int32_t pages, int32_t P, const int32_t* __restrict__ row, const int32_t* __restrict__ pos,
+    uint32_t items, int32_t kv_heads, int32_t rows, int32_t row_pages, int32_t pages, int32_t P,
+    const int32_t* __restrict__ row, const int32_t* __restrict__ pos,
     const uint16_t* __restrict__ k_new, const uint16_t* __restrict__ v_new, void* __restrict__ k_pages,
     float* __restrict__ k_scale, void* __restrict__ v_pages, float* __restrict__ v_scale,
     const int32_t* __restrict__ table) {
   constexpr int kChunks = D / 8;
   constexpr int LPR = kChunks >= 64 ? 64 : kChunks;
   constexpr int NV = (kChunks + LPR - 1) / LPR;
+  constexpr int KV = LATENT ? 1 : 2;
   const int sub = threadIdx.x % LPR;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * (256 / LPR) + threadIdx.x / LPR;
+  const uint32_t item = blockIdx.x * (256 / LPR) + threadIdx.x / LPR;
   if (item >= items) return;  // whole subgroups leave together
-  const int64_t token = item / per_token;
-  const int32_t which = static_cast<int32_t>(item - token * per_token);
-  const bool is_v = which >= kv_heads;
-  const int32_t head = is_v ? which - kv_heads : which;
+  const uint32_t token = item / kv_heads;
+  const int32_t head = static_cast<int32_t>(item - token * kv_heads);
+  uint4 x[KV][NV];
+#pragma unroll
+  for (int w = 0; w < KV; ++w) {
+    const uint16_t* src = (w ? v_new : k_new) + static_cast<int64_t>(item) * D;
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+      const int c = u * LPR + sub;
+      x[w][u] = make_uint4(0, 0, 0, 0);
+      if (c < kChunks) x[w][u] = *reinterpret_cast<const uint4*>(src + c * 8);
+    }
+  }
   const int32_t r = row[token], s = pos[token];
   if (r < 0 || r >= rows || s < 0 || s / P >= row_pages) return;
   const int32_t page = table[static_cast<int64_t>(r) * row_pages + s / P];
   if (page < 0 || page >= pages) return;
-  const uint16_t* src = (is_v ? v_new : k_new) + (token * kv_heads + head) * D;
   const int64_t slot = (static_cast<int64_t>(page) * kv_heads + head) * P + s % P;
-  uint4 x[NV];
 #pragma unroll
-  for (int u = 0; u < NV; ++u) {
-    const int c = u * LPR + sub;
-    x[u] = make_uint4(0, 0, 0, 0);
-    if (c < kChunks) x[u] = *reinterpret_cast<const uint4*>(src + c * 8);
-  }
-  if constexpr (!FP8) {
-    uint16_t* dst = static_cast<uint16_t*>(is_v ? v_pages : k_pages) + slot * D;
+  for (int w = 0; w < KV; ++w) {
+    void* pool = w ? v_pages : k_pages;
+    if constexpr (!FP8) {
+      uint16_t* dst = static_cast<uint16_t*>(pool) + slot * D;
 #pragma unroll
-    for (int u = 0; u < NV; ++u) {
-      const int c = u * LPR + sub;
-      if (c < kChunks) *reinterpret_cast<uint4*>(dst + c * 8) = x[u];
-    }
-  } else {
-    float amax = 0.f;
-#pragma unroll
-    for (int u = 0; u < NV; ++u) {
-      const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        amax = amax_step(amax, __uint_as_float(w[e] << 16));
-        amax = amax_step(amax, __uint_as_float(w[e] & 0xFFFF0000u));
+      for (int u = 0; u < NV; ++u) {
+        const int c = u * LPR + sub;
+        if (c < kChunks) *reinterpret_cast<uint4*>(dst + c * 8) = x[w][u];
       }
-    }
+    } else {
+      float y[NV][8], amax = 0.f;
 #pragma unroll
-    for (int o = 1; o < LPR; o <<= 1) amax = fmaxf(amax, __shfl_xor(amax, o, kWave));
-    float scale, mult;
-    e4m3_scale(amax, scale, mult);
-    uint8_t* dst = static_cast<uint8_t*>(is_v ? v_pages : k_pages) + slot * D;
+      for (int u = 0; u < NV; ++u) {
+        const uint32_t q[4] = {x[w][u].x, x[w][u].y, x[w][u].z, x[w][u].w};
 #pragma unroll
-    for (int u = 0; u < NV; ++u) {
-      const int c = u * LPR + sub;
-      const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-      uint2 code;
-      code.x = e4m3_pack4(__uint_as_float(w[0] << 16), __uint_as_float(w[0] & 0xFFFF0000u),
-                          __uint_as_float(w[1] << 16), __uint_as_float(w[1] & 0xFFFF0000u), mult);
-      code.y = e4m3_pack4(__uint_as_float(w[2] << 16), __uint_as_float(w[2] & 0xFFFF0000u),
-                          __uint_as_float(w[3] << 16), __uint_as_float(w[3] & 0xFFFF0000u), mult);
-      if (c < kChunks) *reinterpret_cast<uint2*>(dst + c * 8) = code;
+        for (int e = 0; e < 4; ++e) {
+          y[u][2 * e] = __uint_as_float(q[e] << 16);
+          y[u][2 * e + 1] = __uint_as_float(q[e] & 0xFFFF0000u);
+          amax = amax_step(amax_step(amax, y[u][2 * e]), y[u][2 * e + 1]);
+        }
+      }
+      float scale, mult;
+      e4m3_scale(lanes_reduce<LPR, true>(amax), scale, mult);
+      uint8_t* dst = static_cast<uint8_t*>(pool) + slot * D;
+#pragma unroll
+      for (int u = 0; u < NV; ++u) {
+        const int c = u * LPR + sub;
+        if (c < kChunks)
+          *reinterpret_cast<uint2*>(dst + c * 8) =
+              make_uint2(e4m3_pack4(y[u][0], y[u][1], y[u][2], y[u][3], mult),
+                         e4m3_pack4(y[u][4], y[u][5], y[u][6], y[u][7], mult));
+      }
+      if (sub == 0) (w ? v_scale : k_scale)[slot] = scale;
     }
-    if (sub == 0) (is_v ? v_scale : k_scale)[slot] = scale;
   }
 }
 
-template <int D>
+template <int D, bool LATENT>
 hipError_t launch_write(const Cache& c, int32_t n, const int32_t* row, const int32_t* pos,
                         const void* k_new, const void* v_new, void* k_pages, float* k_scale,
                         void* v_pages, float* v_scale, const int32_t* table, hipStream_t st) {
   constexpr int LPR = D / 8 >= 64 ? 64 : D / 8;
-  const int32_t per_token = c.kv_heads * (c.latent() ? 1 : 2);
-  const int64_t items = static_cast<int64_t>(n) * per_token;
-  const int64_t blocks = (items + 256 / LPR - 1) / (256 / LPR);
-  const auto* kn = static_cast<const uint16_t*>(k_new);
-  const auto* vn = static_cast<const uint16_t*>(v_new);
-  if (c.dtype == kFP8)
-    page_write_kernel<D, true><<<static_cast<uint32_t>(blocks), 256, 0, st>>>(
-        items, per_token, c.kv_heads, c.rows, c.row_pages, c.pages, c.P, row, pos, kn, vn, k_pages,
-        k_scale, v_pages, v_scale, table);
-  else
-    page_write_kernel<D, false><<<static_cast<uint32_t>(blocks), 256, 0, st>>>(
-        items, per_token, c.kv_heads, c.rows, c.row_pages, c.pages, c.P, row, pos, kn, vn, k_pages,
-        k_scale, v_pages, v_scale, table);
+  const uint32_t items = n * c.kv_heads;  // below 2^31
+  const uint32_t blocks = (items - 1) / (256 / LPR) + 1;
+  const auto f = c.dtype == kFP8 ? page_write_kernel<D, true, LATENT> : page_write_kernel<D, false, LATENT>;
+  f<<<blocks, 256, 0, st>>>(items, c.kv_heads, c.rows, c.row_pages, c.pages, c.P, row, pos,
+                            static_cast<const uint16_t*>(k_new), static_cast<const uint16_t*>(v_new),
+                            k_pages, k_scale, v_pages, v_scale, table);
   return hipGetLastError();
 }
 
@@ -119,38 +116,68 @@ __device__ __forceinline__ int32_t pages_of(int32_t tokens, int32_t P) {
   return tokens / P + (tokens % P != 0);
 }
 
-// Whether an earlier entry of the list in LDS names the same row.
-__device__ __forceinline__ bool listed_before(const int32_t* list, int i) {
-  const int32_t r = list[i];
-  bool hit = false;
-  int j = 0;
-  for (; j + 4 <= i; j += 4) {
-    const int4 x = *reinterpret_cast<const int4*>(list + j);
-    hit |= x.x == r || x.y == r || x.z == r || x.w == r;
-  }
-  for (; j < i; ++j) hit |= list[j] == r;
-  return hit;
+__device__ __forceinline__ int32_t per_thread(int32_t n) { return (n + kListThreads - 1) / kListThreads; }
+
+// The rows of a list and the first entry that names each, in LDS: open
+// addressing over at least twice as many places as entries, so that a search
+// ends.  The first entry is a minimum: the order of the threads does not matter.
+struct Rows {
+  int32_t key[2 * kMaxEntries];
+  int32_t first[2 * kMaxEntries];
+};
+
+__device__ __forceinline__ uint32_t rows_size(int32_t n) {
+  uint32_t size = 64;
+  while (size < 2u * n) size *= 2;  // at most 2 * kMaxEntries
+  return size;
 }
 
+// A barrier must follow.
+__device__ __forceinline__ void rows_clear(Rows& h, uint32_t size) {
+  for (uint32_t i = threadIdx.x; i < size; i += kListThreads) {
+    h.key[i] = kNone;
+    h.first[i] = kMaxEntries;
+  }
+}
+
+// Enters row r >= 0 of entry i; returns its place.  A barrier must follow
+// before first[place] is read.
+__device__ __forceinline__ uint32_t rows_enter(Rows& h, uint32_t size, int32_t r, int32_t i) {
+  uint32_t at = (static_cast<uint32_t>(r) * 2654435761u >> 16) & (size - 1);
+  for (;;) {
+    const int32_t old = atomicCAS(&h.key[at], kNone, r);
+    if (old == kNone || old == r) break;
+    at = (at + 1) & (size - 1);
+  }
+  atomicMin(&h.first[at], i);
+  return at;
+}
+
+// Four entries of refs from p on; entries behind the last page count as used.
+__device__ __forceinline__ int4 refs_at(const int32_t* refs, int32_t pages, int32_t p) {
+  if (p + 4 <= pages) return *reinterpret_cast<const int4*>(refs + p);
+  int4 x = make_int4(1, 1, 1, 1);
+  if (p < pages) x.x = refs[p];
+  if (p + 1 < pages) x.y = refs[p + 1];
+  if (p + 2 < pages) x.z = refs[p + 2];
+  return x;
+}
+
+constexpr int kScanPages = kListThreads * 4;  // pages of a scan's step
+
 // Calls found(rank, page) for the free pages of rank < want, lowest id first,
-// and returns how many there are of those (all threads).  The scan ends with
-// the chunk that holds the last one wanted.
+// and returns how many there are of those (all threads).  `first` is what
+// refs_at gives for this thread's first four pages; the next step's are loaded
+// ahead.  The scan ends with the step that holds the last one wanted.
 template <class F>
-__device__ int scan_free(const int32_t* refs, int32_t pages, int32_t want, int* tmp,
-                         F found) {
-  constexpr int kChunk = kListThreads * 4;
+__device__ int scan_free(const int32_t* refs, int32_t pages, int32_t want, int4 first, int* tmp, F found) {
   int have = 0;
-  for (int32_t c0 = 0; c0 < pages && have < want; c0 += kChunk) {
+  int4 next = first;
+  for (int32_t c0 = 0; c0 < pages && have < want; c0 += kScanPages) {
     const int32_t p = c0 + static_cast<int32_t>(threadIdx.x) * 4;
-    int32_t x[4] = {1, 1, 1, 1};
-    if (p + 4 <= pages) {
-      const int4 v = *reinterpret_cast<const int4*>(refs + p);
-      x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (p + e < pages) x[e] = refs[p + e];
-    }
+    const int4 v = next;
+    next = refs_at(refs, pages, p + kScanPages);
+    const int32_t x[4] = {v.x, v.y, v.z, v.w};
     int mine = 0;
 #pragma unroll
     for (int e = 0; e < 4; ++e) mine += x[e] <= 0;
@@ -168,53 +195,69 @@ __device__ int scan_free(const int32_t* refs, int32_t pages, int32_t want, int* 
 }
 
 // misa_page_extend: one workgroup.  need[i] pages for entry i, offsets by a
-// prefix sum, the free pages counted, then handed out by rank.
+// prefix sum; one scan collects the free pages' ids in LDS, and thread j hands
+// out the j-th.  Lists that need more than LDS holds scan again.
 __global__ __launch_bounds__(kListThreads) void page_extend_kernel(
     int32_t n, int32_t rows, int32_t row_pages, int32_t pages, int32_t P,
     const int32_t* __restrict__ row, const int32_t* __restrict__ count, int32_t* __restrict__ table,
-    int32_t* __restrict__ lengths, int32_t* __restrict__ refs, int32_t* __restrict__ ok) {
-  __shared__ __attribute__((aligned(16))) int32_t list[kMaxEntries];
+    int32_t* __restrict__ lengths, int32_t* refs, int32_t* __restrict__ ok) {
+  __shared__ Rows seen;
+  __shared__ int32_t list[kMaxEntries];
   __shared__ int32_t offset[kMaxEntries];  // pages needed by the entries before this one
+  __shared__ int32_t held[kMaxEntries];    // pages of the entry's row before the call
+  __shared__ int32_t taken[kMaxEntries];
   __shared__ int tmp[kListThreads / kWave];
-  for (int i = threadIdx.x; i < n; i += kListThreads) list[i] = row[i];
+  const int4 first_refs = refs_at(refs, pages, threadIdx.x * 4);
+  const int32_t per = per_thread(n);  // thread t has the entries per * t + e, e < per
+  const uint32_t places = rows_size(n);
+  rows_clear(seen, places);
+  int32_t r[kPerThread], more[kPerThread], len[kPerThread];
+#pragma unroll
+  for (int e = 0; e < kPerThread; ++e) {
+    const int i = threadIdx.x * per + e;
+    const bool inside = e < per && i < n;
+    r[e] = inside ? row[i] : kNone;
+    more[e] = inside ? count[i] : -1;
+    if (r[e] >= rows) r[e] = kNone;
+    if (inside) list[i] = r[e];
+  }
   __syncthreads();
-  int32_t len[kPerThread], need[kPerThread];
+  uint32_t place[kPerThread];
+#pragma unroll
+  for (int e = 0; e < kPerThread; ++e) {
+    len[e] = r[e] >= 0 ? lengths[r[e]] : -1;
+    place[e] = r[e] >= 0 ? rows_enter(seen, places, r[e], threadIdx.x * per + e) : 0;
+  }
+  __syncthreads();
+  int32_t need[kPerThread];
   bool valid[kPerThread];
   int sum = 0;
 #pragma unroll
   for (int e = 0; e < kPerThread; ++e) {
-    const int i = threadIdx.x * kPerThread + e;
-    valid[e] = false;
-    need[e] = 0;
-    len[e] = 0;
-    if (i < n) {
-      const int32_t r = list[i], more = count[i];
-      if (r >= 0 && r < rows && more >= 0 && !listed_before(list, i)) {
-        len[e] = lengths[r];
-        const int64_t to = static_cast<int64_t>(len[e]) + more;
-        if (len[e] >= 0 && to <= static_cast<int64_t>(row_pages) * P) {
-          valid[e] = true;
-          need[e] = pages_of(static_cast<int32_t>(to), P) - pages_of(len[e], P);
-        }
-      }
-    }
-    // At most rows * row_pages pages over distinct rows: below 2^31.
-    sum += need[e];
+    const int64_t to = static_cast<int64_t>(len[e]) + more[e];
+    valid[e] = r[e] >= 0 && seen.first[place[e]] == static_cast<int32_t>(threadIdx.x * per + e) &&
+               more[e] >= 0 && len[e] >= 0 && to <= static_cast<int64_t>(row_pages) * P;
+    need[e] = valid[e] ? pages_of(static_cast<int32_t>(to), P) - pages_of(len[e], P) : 0;
+    sum += need[e];  // at most rows * row_pages over distinct rows: below 2^31
   }
   int total;
   int at = block_exclusive_sum<kListThreads>(sum, tmp, total);
   int32_t first[kPerThread];
 #pragma unroll
   for (int e = 0; e < kPerThread; ++e) {
+    const int i = threadIdx.x * per + e;
     first[e] = at;
-    if (threadIdx.x * kPerThread + e < n) offset[threadIdx.x * kPerThread + e] = at;
+    if (e < per && i < n) {
+      offset[i] = at;
+      held[i] = valid[e] ? pages_of(len[e], P) : 0;
+    }
     at += need[e];
   }
+  const int have = scan_free(refs, pages, total, first_refs, tmp, [&](int rank, int32_t page) {
+    if (rank < kMaxEntries) taken[rank] = page;
+  });
   __syncthreads();
-  const int have = scan_free(refs, pages, total, tmp, [](int, int32_t) {});
-  // The last entry whose pages are all there ends at `served`: ranks below it
-  // are handed out.
-  scan_free(refs, pages, have, tmp, [&](int rank, int32_t page) {
+  auto hand_out = [&](int rank, int32_t page) {
     int lo = 0, hi = n - 1;  // the last entry with offset <= rank
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
@@ -222,65 +265,100 @@ __global__ __launch_bounds__(kListThreads) void page_extend_kernel(
     }
     const int end = lo + 1 < n ? offset[lo + 1] : total;
     if (end > have) return;  // that entry is not served
-    const int32_t r = list[lo];
-    const int32_t at_page = pages_of(lengths[r], P) + (rank - offset[lo]);
-    table[static_cast<int64_t>(r) * row_pages + at_page] = page;
+    table[static_cast<int64_t>(list[lo]) * row_pages + held[lo] + (rank - offset[lo])] = page;
     refs[page] = 1;
-  });
-  __syncthreads();  // the table entries above were placed by the old lengths
+  };
+  if (total <= kMaxEntries)
+    for (int j = threadIdx.x; j < have; j += kListThreads) hand_out(j, taken[j]);
+  else
+    scan_free(refs, pages, have, first_refs, tmp, hand_out);
 #pragma unroll
   for (int e = 0; e < kPerThread; ++e) {
-    const int i = threadIdx.x * kPerThread + e;
-    if (i >= n) continue;
+    const int i = threadIdx.x * per + e;
+    if (e >= per || i >= n) continue;
     const bool good = valid[e] && (need[e] == 0 || first[e] + need[e] <= have);
-    if (good) lengths[list[i]] = len[e] + count[i];
+    if (good) lengths[r[e]] = len[e] + more[e];
     ok[i] = good;
   }
 }
 
-// misa_page_fork, first launch: decide every entry, take the free pages, set
-// the children's lengths.
-__global__ __launch_bounds__(kListThreads) void page_fork_plan_kernel(
+// Enters the parent's whole pages into a child's table row; this thread's part
+// of them is begin, begin + step, ...  refs are integer sums: any order.
+__device__ __forceinline__ void share_pages(int32_t* __restrict__ table, int32_t* refs, int64_t from,
+                                            int64_t to, int32_t whole, int32_t pages, int begin,
+                                            int step) {
+  for (int32_t s = begin; s < whole; s += step) {
+    const int32_t page = table[from + s];
+    table[to + s] = page;
+    if (page >= 0 && page < pages) atomicAdd(refs + page, 1);
+  }
+}
+
+// misa_page_fork, by one workgroup: decide every entry, take the free pages,
+// set the children's lengths and last pages.  APPLY: and share the whole pages,
+// a wave per entry (short lists; longer ones take a second launch for that).
+// A parent of a forked child that is not empty is no child of the call, so its
+// row does not change.
+template <bool APPLY>
+__global__ __launch_bounds__(kListThreads) void page_fork_kernel(
     int32_t n, int32_t rows, int32_t row_pages, int32_t pages, int32_t P,
-    const int32_t* __restrict__ parent, const int32_t* __restrict__ child,
-    const int32_t* __restrict__ table, int32_t* __restrict__ lengths, int32_t* __restrict__ refs,
-    int32_t* __restrict__ src, int32_t* __restrict__ dst, int32_t* __restrict__ ok) {
-  __shared__ __attribute__((aligned(16))) int32_t list[kMaxEntries];
+    const int32_t* __restrict__ parent, const int32_t* __restrict__ child, int32_t* table,
+    int32_t* __restrict__ lengths, int32_t* refs, int32_t* __restrict__ src,
+    int32_t* __restrict__ dst, int32_t* __restrict__ ok) {
+  __shared__ Rows seen;
   __shared__ int32_t taken[kMaxEntries];
+  __shared__ int32_t whole[APPLY ? kMaxEntries : 1];   // pages to share
+  __shared__ int32_t source[APPLY ? kMaxEntries : 1];  // the parents
+  __shared__ int32_t target[APPLY ? kMaxEntries : 1];  // the children
   __shared__ int tmp[kListThreads / kWave];
-  for (int i = threadIdx.x; i < n; i += kListThreads) list[i] = child[i];
-  __syncthreads();
-  int32_t len[kPerThread], from[kPerThread];
+  const int4 first_refs = refs_at(refs, pages, threadIdx.x * 4);
+  const int32_t per = per_thread(n);  // thread t has the entries per * t + e, e < per
+  const uint32_t places = rows_size(n);
+  rows_clear(seen, places);
+  int32_t p[kPerThread], c[kPerThread], len[kPerThread], from[kPerThread];
   bool valid[kPerThread];
+#pragma unroll
+  for (int e = 0; e < kPerThread; ++e) {
+    const int i = threadIdx.x * per + e;
+    const bool inside = e < per && i < n;
+    p[e] = inside ? parent[i] : kNone;
+    c[e] = inside ? child[i] : kNone;
+    if (APPLY && inside) {
+      source[i] = p[e];
+      target[i] = c[e];
+    }
+  }
+  __syncthreads();
+  uint32_t place[kPerThread];
+#pragma unroll
+  for (int e = 0; e < kPerThread; ++e) {
+    const bool named = c[e] >= 0 && c[e] < rows;
+    place[e] = named ? rows_enter(seen, places, c[e], threadIdx.x * per + e) : 0;
+    valid[e] = named && p[e] >= 0 && p[e] < rows && c[e] != p[e];
+    len[e] = valid[e] ? held_tokens(lengths[p[e]], row_pages, P) : 0;
+    if (valid[e]) valid[e] = lengths[c[e]] == 0;
+    from[e] = kNone;
+    if (valid[e] && len[e] % P != 0) {
+      const int32_t last = table[static_cast<int64_t>(p[e]) * row_pages + len[e] / P];
+      if (last >= 0 && last < pages) from[e] = last;
+    }
+  }
+  __syncthreads();
   int sum = 0;
 #pragma unroll
   for (int e = 0; e < kPerThread; ++e) {
-    const int i = threadIdx.x * kPerThread + e;
-    valid[e] = false;
-    len[e] = 0;
-    from[e] = kNone;
-    if (i < n) {
-      const int32_t c = list[i], p = parent[i];
-      if (c >= 0 && c < rows && p >= 0 && p < rows && p != c && lengths[c] == 0 &&
-          !listed_before(list, i)) {
-        valid[e] = true;
-        len[e] = held_tokens(lengths[p], row_pages, P);
-        if (len[e] % P != 0) {
-          const int32_t last = table[static_cast<int64_t>(p) * row_pages + len[e] / P];
-          if (last >= 0 && last < pages) from[e] = last;
-        }
-      }
-    }
+    valid[e] = valid[e] && seen.first[place[e]] == static_cast<int32_t>(threadIdx.x * per + e);
+    if (!valid[e]) from[e] = kNone;
     sum += from[e] != kNone;
   }
   int total;
   int at = block_exclusive_sum<kListThreads>(sum, tmp, total);
-  const int have = scan_free(refs, pages, total, tmp, [&](int rank, int32_t page) { taken[rank] = page; });
-  __syncthreads();  // every read of refs, lengths and taken's writes before
+  const int have = scan_free(refs, pages, total, first_refs, tmp, [&](int rank, int32_t page) { taken[rank] = page; });
+  __syncthreads();  // every read of refs and lengths, and taken's writes, before
 #pragma unroll
   for (int e = 0; e < kPerThread; ++e) {
-    const int i = threadIdx.x * kPerThread + e;
-    if (i >= n) continue;
+    const int i = threadIdx.x * per + e;
+    if (e >= per || i >= n) continue;
     const bool part = from[e] != kNone;
     const bool good = valid[e] && (!part || at < have);
     const int32_t page = part && good ? taken[at] : kNone;
@@ -288,43 +366,47 @@ __global__ __launch_bounds__(kListThreads) void page_fork_plan_kernel(
     src[i] = page != kNone ? from[e] : kNone;
     dst[i] = page;
     ok[i] = good;
-    if (good) lengths[list[i]] = len[e];
+    if (APPLY) whole[i] = good ? len[e] / P : 0;
+    if (good) {
+      lengths[c[e]] = len[e];
+      if (len[e] % P != 0) table[static_cast<int64_t>(c[e]) * row_pages + len[e] / P] = page;
+    }
     at += part;
+  }
+  if constexpr (APPLY) {
+    __syncthreads();
+    for (int i = threadIdx.x / kWave; i < n; i += kListThreads / kWave)
+      if (whole[i] > 0)
+        share_pages(table, refs, static_cast<int64_t>(source[i]) * row_pages,
+                    static_cast<int64_t>(target[i]) * row_pages, whole[i], pages, lane_id(), kWave);
   }
 }
 
-// misa_page_fork, second launch: workgroup (x, i) enters a part of the
-// parent's pages into child i's table row.  A parent of a forked child that is
-// not empty is no child of the call, so its row does not change here.
-__global__ __launch_bounds__(256) void page_fork_apply_kernel(
-    int32_t rows, int32_t row_pages, int32_t pages, int32_t P, const int32_t* __restrict__ parent,
-    const int32_t* __restrict__ child, int32_t* __restrict__ table,
-    const int32_t* __restrict__ lengths, int32_t* __restrict__ refs,
-    const int32_t* __restrict__ dst, const int32_t* __restrict__ ok) {
+// misa_page_fork, second launch of long lists: workgroup (x, i) shares a part
+// of the pages of entry i.
+__global__ __launch_bounds__(256) void page_share_kernel(int32_t row_pages, int32_t pages, int32_t P,
+                                                         const int32_t* __restrict__ parent,
+                                                         const int32_t* __restrict__ child,
+                                                         int32_t* __restrict__ table,
+                                                         const int32_t* __restrict__ lengths,
+                                                         int32_t* refs, const int32_t* __restrict__ ok) {
   const int i = blockIdx.y;
   if (!ok[i]) return;
   const int32_t c = child[i];
-  const int32_t len = lengths[c];
-  const int32_t whole = len / P;
-  const int64_t to = static_cast<int64_t>(c) * row_pages;
-  const int64_t from = static_cast<int64_t>(parent[i]) * row_pages;
-  for (int32_t s = blockIdx.x * 256 + threadIdx.x; s < whole; s += gridDim.x * 256) {
-    const int32_t page = table[from + s];
-    table[to + s] = page;
-    if (page >= 0 && page < pages) atomicAdd(refs + page, 1);  // integer: any order, same sum
-  }
-  if (blockIdx.x == 0 && threadIdx.x == 0 && len % P != 0) table[to + whole] = dst[i];
+  share_pages(table, refs, static_cast<int64_t>(parent[i]) * row_pages,
+              static_cast<int64_t>(c) * row_pages, lengths[c] / P, pages,
+              blockIdx.x * 256 + threadIdx.x, gridDim.x * 256);
 }
 
-// misa_page_free: workgroup (x, i) clears a part of row i.  Lengths are read
-// by every workgroup of the row, so they are cleared by a launch of their own.
+// misa_page_free: workgroup i clears the row of entry i, unless an earlier one
+// names it.
 __global__ __launch_bounds__(256) void page_free_kernel(int32_t rows, int32_t row_pages,
                                                         int32_t pages, int32_t P,
                                                         const int32_t* __restrict__ row,
                                                         int32_t* __restrict__ table,
-                                                        const int32_t* __restrict__ lengths,
+                                                        int32_t* __restrict__ lengths,
                                                         int32_t* __restrict__ refs) {
-  const int i = blockIdx.y;
+  const int i = blockIdx.x;
   const int32_t r = row[i];
   if (r < 0 || r >= rows) return;
   bool before = false;
@@ -332,20 +414,14 @@ __global__ __launch_bounds__(256) void page_free_kernel(int32_t rows, int32_t ro
   if (__syncthreads_or(before)) return;
   const int32_t held = pages_of(held_tokens(lengths[r], row_pages, P), P);
   const int64_t at = static_cast<int64_t>(r) * row_pages;
-  for (int32_t s = blockIdx.x * 256 + threadIdx.x; s < held; s += gridDim.x * 256) {
+#pragma unroll 4
+  for (int32_t s = threadIdx.x; s < held; s += 256) {
     const int32_t page = table[at + s];
     table[at + s] = kNone;
     if (page >= 0 && page < pages) atomicSub(refs + page, 1);
   }
-}
-
-__global__ __launch_bounds__(256) void page_clear_lengths_kernel(int32_t n, int32_t rows,
-                                                                 const int32_t* __restrict__ row,
-                                                                 int32_t* __restrict__ lengths) {
-  const int i = blockIdx.x * 256 + threadIdx.x;
-  if (i >= n) return;
-  const int32_t r = row[i];
-  if (r >= 0 && r < rows) lengths[r] = 0;
+  __syncthreads();  // every thread has read the length
+  if (threadIdx.x == 0) lengths[r] = 0;
 }
 
 // Workgroups per table row: four entries a thread, at most 64 (the kernels loop).
@@ -356,59 +432,42 @@ int32_t row_blocks(const Cache& c) {
 
 // ---------------------------------------------------------------- compaction
 
-constexpr int kCountPages = 4096;  // pages per counting workgroup
+constexpr int kCountPages = 1024;  // pages per workgroup: four per thread
+
+__device__ __forceinline__ int used4(int4 x) { return (x.x > 0) + (x.y > 0) + (x.z > 0) + (x.w > 0); }
+
+// refs_at, with entries behind the last page free.
+__device__ __forceinline__ int4 refs_or_free(const int32_t* refs, int32_t pages, int32_t p) {
+  if (p + 4 <= pages) return *reinterpret_cast<const int4*>(refs + p);
+  int4 x = make_int4(0, 0, 0, 0);
+  if (p < pages) x.x = refs[p];
+  if (p + 1 < pages) x.y = refs[p + 1];
+  if (p + 2 < pages) x.z = refs[p + 2];
+  return x;
+}
 
 __global__ __launch_bounds__(256) void page_count_kernel(int32_t pages,
                                                          const int32_t* __restrict__ refs,
                                                          int32_t* __restrict__ counts) {
   __shared__ int tmp[4];
-  int mine = 0;
-  const int32_t c0 = blockIdx.x * kCountPages;
-  for (int32_t p = c0 + threadIdx.x; p < min(c0 + kCountPages, pages); p += 256)
-    mine += refs[p] > 0;
   int total;
-  block_exclusive_sum<256>(mine, tmp, total);
+  block_exclusive_sum<256>(used4(refs_or_free(refs, pages, blockIdx.x * kCountPages + threadIdx.x * 4)), tmp, total);
   if (threadIdx.x == 0) counts[blockIdx.x] = total;
 }
 
-// Live pages in [0, end): the counts of the whole chunks below and the rest of
-// the last one.  All threads; contains barriers.
-__device__ int live_below(int32_t end, const int32_t* __restrict__ refs,
-                          const int32_t* __restrict__ counts, int* tmp) {
-  int mine = 0;
-  const int32_t whole = end / kCountPages;
-  for (int32_t b = threadIdx.x; b < whole; b += 256) mine += counts[b];
-  for (int32_t p = whole * kCountPages + threadIdx.x; p < end; p += 256) mine += refs[p] > 0;
-  int total;
-  block_exclusive_sum<256>(mine, tmp, total);
-  return total;
-}
-
-// Second launch: the rank of every hole (a free page below `live`) and mover
-// (a live page behind it), by prefix sums over 256 pages per workgroup.  A
-// mover's map entry holds -2 - rank until the last launch.
-__global__ __launch_bounds__(256) void page_place_kernel(int32_t pages, int32_t chunks,
-                                                         const int32_t* __restrict__ refs,
-                                                         const int32_t* __restrict__ counts,
-                                                         int32_t* __restrict__ map,
-                                                         int32_t* __restrict__ live_out,
-                                                         int32_t* __restrict__ src,
-                                                         int32_t* __restrict__ dst) {
-  __shared__ int tmp[4];
-  int mine = 0;
-  for (int b = threadIdx.x; b < chunks; b += 256) mine += counts[b];
-  int live;
-  block_exclusive_sum<256>(mine, tmp, live);
-  const int stay = live_below(live, refs, counts, tmp);  // live pages that do not move
-  const int32_t p0 = blockIdx.x * 256;
-  const int before = live_below(p0, refs, counts, tmp);
-  const int32_t p = p0 + threadIdx.x;
-  const bool inside = p < pages;
-  const bool used = inside && refs[p] > 0;
-  int total;
-  const int rank = before + block_exclusive_sum<256>(used, tmp, total);  // live pages before p
+// What becomes of four pages from p on, of which `x` are the refs: `rank` live
+// pages lie before them, `live` in all, `stay` of them below `live`.  Holes and
+// movers get their ranks; a mover's map entry holds -2 - rank until the tables
+// are done.
+__device__ __forceinline__ void place4(int4 x, int32_t p, int32_t pages, int rank, int live, int stay,
+                                       int32_t* __restrict__ map, int32_t* __restrict__ src,
+                                       int32_t* __restrict__ dst) {
+  const int32_t v[4] = {x.x, x.y, x.z, x.w};
   const int holes = live - stay;
-  if (inside) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e, ++p) {
+    if (p >= pages) break;
+    const bool used = v[e] > 0;
     if (used && p >= live) {
       src[rank - stay] = p;
       map[p] = -2 - (rank - stay);
@@ -420,8 +479,79 @@ __global__ __launch_bounds__(256) void page_place_kernel(int32_t pages, int32_t 
       src[p] = kNone;
       dst[p] = kNone;
     }
+    rank += used;
   }
+}
+
+// Second launch: ranks by prefix sums over the counts and a workgroup's pages.
+__global__ __launch_bounds__(256) void page_place_kernel(int32_t pages, int32_t chunks,
+                                                         const int32_t* __restrict__ refs,
+                                                         const int32_t* __restrict__ counts,
+                                                         int32_t* __restrict__ map,
+                                                         int32_t* __restrict__ live_out,
+                                                         int32_t* __restrict__ src,
+                                                         int32_t* __restrict__ dst) {
+  __shared__ int tmp[4];
+  const int32_t p = blockIdx.x * kCountPages + threadIdx.x * 4;
+  const int4 x = refs_or_free(refs, pages, p);
+  int all = 0, lower = 0;
+  for (int b = threadIdx.x; b < chunks; b += 256) {
+    const int c = counts[b];
+    all += c;
+    lower += b < static_cast<int>(blockIdx.x) ? c : 0;
+  }
+  int live, before, stay, total;
+  block_exclusive_sum<256>(all, tmp, live);
+  // Live pages below `live`: whole chunks, and the part of the one it is in.
+  const int32_t edge = live / kCountPages;
+  const int32_t q = edge * kCountPages + threadIdx.x * 4;
+  const int4 y = q < pages ? refs_or_free(refs, pages, q) : make_int4(0, 0, 0, 0);
+  int mine = 0;
+  for (int b = threadIdx.x; b < edge; b += 256) mine += counts[b];
+  mine += (y.x > 0 && q < live) + (y.y > 0 && q + 1 < live) + (y.z > 0 && q + 2 < live) +
+          (y.w > 0 && q + 3 < live);
+  block_exclusive_sum<256>(lower, tmp, before);
+  block_exclusive_sum<256>(mine, tmp, stay);
+  const int rank = before + block_exclusive_sum<256>(used4(x), tmp, total);
+  place4(x, p, pages, rank, live, stay, map, src, dst);
   if (p == 0) live_out[0] = live;
+}
+
+// A table entry's page afterwards, from the map as place4 leaves it.
+__device__ __forceinline__ int32_t moved_page(int32_t id, int32_t pages, const int32_t* map, const int32_t* dst) {
+  if (id < 0 || id >= pages) return kNone;
+  const int32_t to = map[id];
+  return to < kNone ? dst[-2 - to] : to;
+}
+
+// Small pools and tables: everything in one workgroup and one launch.
+__global__ __launch_bounds__(kListThreads) void page_compact_small_kernel(
+    int32_t pages, int32_t entries, const int32_t* table, const int32_t* refs, int32_t* table_out,
+    int32_t* refs_out, int32_t* map, int32_t* __restrict__ live_out, int32_t* src, int32_t* dst) {
+  __shared__ int tmp[kListThreads / kWave];
+  const int32_t p = threadIdx.x * 4;
+  const int4 x = refs_or_free(refs, pages, p);
+  int live, stay;
+  const int rank = block_exclusive_sum<kListThreads>(used4(x), tmp, live);
+  block_exclusive_sum<kListThreads>((x.x > 0 && p < live) + (x.y > 0 && p + 1 < live) +
+                                        (x.z > 0 && p + 2 < live) + (x.w > 0 && p + 3 < live),
+                                    tmp, stay);
+  place4(x, p, pages, rank, live, stay, map, src, dst);
+  if (p == 0) live_out[0] = live;
+  __syncthreads();
+  const int32_t v[4] = {x.x, x.y, x.z, x.w};
+  for (int i = threadIdx.x; i < entries; i += kListThreads) table_out[i] = moved_page(table[i], pages, map, dst);
+  int32_t to[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) to[e] = p + e < pages ? moved_page(p + e, pages, map, dst) : kNone;
+  __syncthreads();  // every read of map before
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (p + e < pages) {
+      map[p + e] = to[e];
+      if (to[e] != kNone) refs_out[to[e]] = v[e];
+      if (p + e >= live) refs_out[p + e] = 0;
+    }
 }
 
 // Last launch: the movers' map entries, refs and the tables.  Threads that
@@ -448,13 +578,7 @@ __global__ __launch_bounds__(256) void page_finish_kernel(
     }
   }
   if (i < entries) {
-    const int32_t id = table[i];
-    int32_t to = kNone;
-    if (id >= 0 && id < pages) {
-      to = map[id];
-      if (to < kNone) to = dst[-2 - to];
-    }
-    table_out[i] = to;
+    table_out[i] = moved_page(table[i], pages, map, dst);
   }
 }
 
@@ -515,16 +639,16 @@ hipError_t launch_page_write(const Cache& c, int32_t n, const int32_t* row, cons
                              void* v_pages, float* v_scale, const int32_t* table, hipStream_t st) {
   switch (c.dk) {
     case 64:
-      return launch_write<64>(c, n, row, pos, k_new, v_new, k_pages, k_scale, v_pages, v_scale,
+      return launch_write<64, false>(c, n, row, pos, k_new, v_new, k_pages, k_scale, v_pages, v_scale,
                               table, st);
     case 128:
-      return launch_write<128>(c, n, row, pos, k_new, v_new, k_pages, k_scale, v_pages, v_scale,
+      return launch_write<128, false>(c, n, row, pos, k_new, v_new, k_pages, k_scale, v_pages, v_scale,
                                table, st);
     case 256:
-      return launch_write<256>(c, n, row, pos, k_new, v_new, k_pages, k_scale, v_pages, v_scale,
+      return launch_write<256, false>(c, n, row, pos, k_new, v_new, k_pages, k_scale, v_pages, v_scale,
                                table, st);
     default:
-      return launch_write<576>(c, n, row, pos, k_new, v_new, k_pages, k_scale, v_pages, v_scale,
+      return launch_write<576, true>(c, n, row, pos, k_new, v_new, k_pages, k_scale, v_pages, v_scale,
                                table, st);
   }
 }
@@ -540,24 +664,22 @@ hipError_t launch_page_extend(const Cache& c, int32_t n, const int32_t* row, con
 hipError_t launch_page_fork(const Cache& c, int32_t n, const int32_t* parent, const int32_t* child,
                             int32_t* table, int32_t* lengths, int32_t* refs, int32_t* src,
                             int32_t* dst, int32_t* ok, hipStream_t st) {
-  page_fork_plan_kernel<<<1, kListThreads, 0, st>>>(n, c.rows, c.row_pages, c.pages, c.P, parent,
-                                                    child, table, lengths, refs, src, dst, ok);
+  // Up to 16384 table entries one workgroup shares the pages too (@FORK_ONE@);
+  // beyond, a second launch spreads them over the card (@FORK_TWO@).
+  const bool small = static_cast<int64_t>(n) * c.row_pages <= 16384;
+  const auto f = small ? page_fork_kernel<true> : page_fork_kernel<false>;
+  f<<<1, kListThreads, 0, st>>>(n, c.rows, c.row_pages, c.pages, c.P, parent, child, table, lengths,
+                                refs, src, dst, ok);
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  const dim3 grid(row_blocks(c), n);
-  page_fork_apply_kernel<<<grid, 256, 0, st>>>(c.rows, c.row_pages, c.pages, c.P, parent, child,
-                                               table, lengths, refs, dst, ok);
+  if (e != hipSuccess || small) return e;
+  page_share_kernel<<<dim3(row_blocks(c), n), 256, 0, st>>>(c.row_pages, c.pages, c.P, parent, child,
+                                                            table, lengths, refs, ok);
   return hipGetLastError();
 }
 
 hipError_t launch_page_free(const Cache& c, int32_t n, const int32_t* row, int32_t* table,
                             int32_t* lengths, int32_t* refs, hipStream_t st) {
-  const dim3 grid(row_blocks(c), n);
-  page_free_kernel<<<grid, 256, 0, st>>>(c.rows, c.row_pages, c.pages, c.P, row, table, lengths,
-                                         refs);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  page_clear_lengths_kernel<<<(n + 255) / 256, 256, 0, st>>>(n, c.rows, row, lengths);
+  page_free_kernel<<<n, 256, 0, st>>>(c.rows, c.row_pages, c.pages, c.P, row, table, lengths, refs);
   return hipGetLastError();
 }
 
@@ -568,16 +690,22 @@ size_t page_compact_ws_bytes(const Cache& c) {
 hipError_t launch_page_compact(const Cache& c, const int32_t* table, const int32_t* refs,
                                int32_t* table_out, int32_t* refs_out, int32_t* map, int32_t* live,
                                int32_t* src, int32_t* dst, void* ws, hipStream_t st) {
+  const int64_t entries = static_cast<int64_t>(c.rows) * c.row_pages;
+  // One workgroup holds a pool of 4096 pages; with that and up to 16384 table
+  // entries it takes @COMPACT_ONE@ against @COMPACT_THREE@ of the three launches.
+  if (c.pages <= kScanPages && entries <= 16384) {
+    page_compact_small_kernel<<<1, kListThreads, 0, st>>>(c.pages, static_cast<int32_t>(entries), table,
+                                                          refs, table_out, refs_out, map, live, src, dst);
+    return hipGetLastError();
+  }
   const int32_t chunks = (c.pages + kCountPages - 1) / kCountPages;
   auto* counts = static_cast<int32_t*>(ws);
   page_count_kernel<<<chunks, 256, 0, st>>>(c.pages, refs, counts);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  page_place_kernel<<<(c.pages + 255) / 256, 256, 0, st>>>(c.pages, chunks, refs, counts, map, live,
-                                                           src, dst);
+  page_place_kernel<<<chunks, 256, 0, st>>>(c.pages, chunks, refs, counts, map, live, src, dst);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int64_t entries = static_cast<int64_t>(c.rows) * c.row_pages;
   const int64_t most = entries > c.pages ? entries : c.pages;
   page_finish_kernel<<<static_cast<uint32_t>((most + 255) / 256), 256, 0, st>>>(
       c.pages, entries, table, refs, table_out, refs_out, map, live, src, dst);
