@@ -584,7 +584,7 @@ __global__ __launch_bounds__(256) void page_finish_kernel(
 
 // ---------------------------------------------------------------- copies
 
-constexpr int kCopyBytes = 16384;  // bytes of a page that one workgroup copies
+constexpr int kCopyBytes = 32768;  // bytes of a page that one workgroup copies
 
 struct CopyPlan {
   PageBuffers bufs;
@@ -592,11 +592,16 @@ struct CopyPlan {
   int32_t parts[kMaxPageBuffers];  // workgroups per page
 };
 
-template <class V>
+// N dwords per thread and step, marked as not to be kept: pages go by once
+// (20000 pages of 32 KB, four planes, 1.3 GB: 241 us; 259 us with plain loads
+// and stores, 272 us of those in pieces of 16 KB).
+template <int N>
 __device__ __forceinline__ void copy_run(uint8_t* to, const uint8_t* from, int64_t bytes) {
-  constexpr int kStep = 256 * sizeof(V);
-  for (int64_t o = threadIdx.x * sizeof(V); o < bytes; o += kStep)
-    *reinterpret_cast<V*>(to + o) = *reinterpret_cast<const V*>(from + o);
+  typedef __attribute__((ext_vector_type(N))) uint32_t V;
+  constexpr int kStep = 256 * N * 4;
+  for (int64_t o = threadIdx.x * (N * 4); o < bytes; o += kStep)
+    __builtin_nontemporal_store(__builtin_nontemporal_load(reinterpret_cast<const V*>(from + o)),
+                                reinterpret_cast<V*>(to + o));
 }
 
 // Workgroups run over (buffer, pair, plane, part of the page).
@@ -619,9 +624,9 @@ __global__ __launch_bounds__(256) void page_copy_kernel(CopyPlan plan, int32_t p
   uint8_t* to = base + d * buf.page_bytes;
   const uint8_t* from = base + s * buf.page_bytes;
   if (buf.page_bytes % 16 == 0)
-    copy_run<uint4>(to, from, bytes);
+    copy_run<4>(to, from, bytes);
   else
-    copy_run<uint32_t>(to, from, bytes);
+    copy_run<1>(to, from, bytes);
 }
 
 int32_t copy_parts(const PageBuffer& b) {
