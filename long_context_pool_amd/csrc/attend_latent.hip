@@ -21,6 +21,72 @@ __device__ __forceinline__ void landed() { __builtin_amdgcn_s_waitcnt(0x0F70); }
 
 constexpr int kLatentStage = 512;  // tokens whose slots are in LDS at a time
 
+// The end of a workgroup's work, for token group G (both meet in the barriers):
+// the groups' sums are joined a quarter of the dimensions at a time; each group
+// hands one quarter to the other through LDS and writes the other one.
+template <int G, int NJ, int NB>
+__device__ __forceinline__ void hand_over(const Args& a, const f32x4 (&acc)[NJ], uint4 (&even)[2][NB],
+                                          uint4 (&odd)[2][NB], float (&top)[2][4][16],
+                                          float (&sum)[2][4][16], float m, float l, int row, int split,
+                                          int head0, int hw, int c, int g) {
+  constexpr int kPart = NJ / 4;  // products of a quarter
+  static_assert(kPart * 4 * kWave <= 2 * NB, "a quarter fits a buffer");
+  const bool mine = head0 + c < a.heads;
+  const int64_t at = static_cast<int64_t>(row) * a.heads + head0 + c;
+  const int64_t part = at * a.splits + split;
+  float4* give = reinterpret_cast<float4*>(G == 0 ? even : odd) + hw * kWave + lane_id();  // [product][wave][lane]
+  const float4* take = reinterpret_cast<const float4*>(G == 0 ? odd : even) + hw * kWave + lane_id();
+  float f_own = 0.f, f_other = 0.f;
+#pragma unroll
+  for (int pass = 0; pass < 2; ++pass) {
+    if (pass > 0) __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kPart; ++j) {
+      const f32x4 y = acc[(2 * pass + 1 - G) * kPart + j];
+      give[j * 4 * kWave] = make_float4(y[0], y[1], y[2], y[3]);
+    }
+    __syncthreads();
+    if (pass == 0) {
+      const float m1 = top[1 - G][hw][c], l1 = sum[1 - G][hw][c];
+      const float mall = fmaxf(m, m1);
+      f_own = part_factor(m, l, mall);
+      f_other = part_factor(m1, l1, mall);
+      const float lall = l * f_own + l1 * f_other;
+      if (G == 0 && g == 0 && mine) {
+        if (a.splits > 1)
+          a.part_ml[part] = make_float2(mall, lall);
+        else if (a.lse)
+          a.lse[at] = lall == 0.f ? -INFINITY : final_lse(mall, lall);
+      }
+      if (a.splits == 1) {
+        const float inv = lall == 0.f ? 0.f : 1.f / lall;
+        f_own *= inv;
+        f_other *= inv;
+      }
+    }
+    if (!mine) continue;
+#pragma unroll
+    for (int j = 0; j < kPart; ++j) {
+      const int d = 16 * ((2 * pass + G) * kPart + j) + 4 * g;
+      const f32x4 y = acc[(2 * pass + G) * kPart + j];
+      const float4 z = take[j * 4 * kWave];
+      const float4 o = make_float4(y[0] * f_own + z.x * f_other, y[1] * f_own + z.y * f_other,
+                                   y[2] * f_own + z.z * f_other, y[3] * f_own + z.w * f_other);
+      if (a.splits > 1) {
+        *reinterpret_cast<float4*>(a.part_o + part * kLatentV + d) = o;
+      } else {
+        bf16x2 u, v;
+        u[0] = static_cast<__bf16>(o.x);
+        u[1] = static_cast<__bf16>(o.y);
+        v[0] = static_cast<__bf16>(o.z);
+        v[1] = static_cast<__bf16>(o.w);
+        *reinterpret_cast<uint2*>(a.out + at * kLatentV + d) =
+            make_uint2(__builtin_bit_cast(uint32_t, u), __builtin_bit_cast(uint32_t, v));
+      }
+    }
+  }
+}
+
 // One workgroup of eight waves per (split, 64 query heads, row): waves 0-3 and
 // 4-7 are two token groups, and wave w of a group has the query heads 16 (w %
 // 4) .. +15.  A group's tile of 32 cached rows goes to LDS once, by direct
@@ -57,7 +123,7 @@ __global__ __launch_bounds__(512) void attend_latent_kernel(Args a) {
   __shared__ uint4 q_lds[4][QL][kWave];
   __shared__ __attribute__((aligned(16))) uint32_t slots[kLatentStage];
   __shared__ __attribute__((aligned(16))) float scales[kFp8 ? kLatentStage : 4];
-  __shared__ float top[4][16], sum[4][16];
+  __shared__ float top[2][4][16], sum[2][4][16];
 
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int c = lane & 15, g = lane >> 4;
@@ -278,70 +344,16 @@ __global__ __launch_bounds__(512) void attend_latent_kernel(Args a) {
     }
   }
 
-  // Join the two token groups: group 1 hands its sums to group 0 through LDS, a
-  // quarter of the dimensions at a time.
-  constexpr int kPart = NJ / 4;  // products of a quarter
   l = groups_sum(l);
   __syncthreads();
-  if (grp == 1 && g == 0) {
-    top[hw][c] = m;
-    sum[hw][c] = l;
+  if (g == 0) {
+    top[grp][hw][c] = m;
+    sum[grp][hw][c] = l;
   }
-  const int64_t at = static_cast<int64_t>(row) * a.heads + min(head0 + c, a.heads - 1);
-  const int64_t part = at * a.splits + split;
-  const bool mine = grp == 0 && head0 + c < a.heads;
-  float f0 = 0.f, f1 = 0.f;
-#pragma unroll
-  for (int qt = 0; qt < 4; ++qt) {
-    float4* red = reinterpret_cast<float4*>(qt % 2 ? odd : even);  // [product][wave][lane]
-    if (grp == 1) {
-#pragma unroll
-      for (int j = 0; j < kPart; ++j) {
-        const f32x4 y = acc[qt * kPart + j];
-        red[(j * 4 + hw) * kWave + lane] = make_float4(y[0], y[1], y[2], y[3]);
-      }
-    }
-    __syncthreads();
-    if (qt == 0 && grp == 0) {
-      const float m1 = top[hw][c], l1 = sum[hw][c];
-      const float mall = fmaxf(m, m1);
-      f0 = part_factor(m, l, mall);
-      f1 = part_factor(m1, l1, mall);
-      const float lall = l * f0 + l1 * f1;
-      if (g == 0 && mine) {
-        if (a.splits > 1)
-          a.part_ml[part] = make_float2(mall, lall);
-        else if (a.lse)
-          a.lse[at] = lall == 0.f ? -INFINITY : final_lse(mall, lall);
-      }
-      if (a.splits == 1) {
-        const float inv = lall == 0.f ? 0.f : 1.f / lall;
-        f0 *= inv;
-        f1 *= inv;
-      }
-    }
-    if (mine) {
-#pragma unroll
-      for (int j = 0; j < kPart; ++j) {
-        const int d = 16 * (qt * kPart + j) + 4 * g;
-        const f32x4 y = acc[qt * kPart + j];
-        const float4 z = red[(j * 4 + hw) * kWave + lane];
-        const float4 o = make_float4(y[0] * f0 + z.x * f1, y[1] * f0 + z.y * f1, y[2] * f0 + z.z * f1,
-                                     y[3] * f0 + z.w * f1);
-        if (a.splits > 1) {
-          *reinterpret_cast<float4*>(a.part_o + part * kLatentV + d) = o;
-        } else {
-          bf16x2 u, v;
-          u[0] = static_cast<__bf16>(o.x);
-          u[1] = static_cast<__bf16>(o.y);
-          v[0] = static_cast<__bf16>(o.z);
-          v[1] = static_cast<__bf16>(o.w);
-          *reinterpret_cast<uint2*>(a.out + at * kLatentV + d) =
-              make_uint2(__builtin_bit_cast(uint32_t, u), __builtin_bit_cast(uint32_t, v));
-        }
-      }
-    }
-  }
+  if (grp == 0)
+    hand_over<0>(a, acc, even, odd, top, sum, m, l, row, split, head0, hw, c, g);
+  else
+    hand_over<1>(a, acc, even, odd, top, sum, m, l, row, split, head0, hw, c, g);
 }
 
 }  // namespace
