@@ -16,35 +16,45 @@ __device__ __forceinline__ void store_elem(int dt, void* base, int64_t i, float 
     static_cast<__bf16*>(base)[i] = static_cast<__bf16>(x);
 }
 
-// Eight elements at e (a multiple of 8; 16-byte aligned) as fp32.
+// Eight elements at e as fp32: one or two 16-byte loads, which need not be
+// aligned to more than an element (rows of odd length start anywhere).
+struct __attribute__((packed, aligned(2))) Bf16x8 {
+  uint32_t w[4];
+};
+struct __attribute__((packed, aligned(4))) F32x8 {
+  float w[8];
+};
+struct __attribute__((packed, aligned(1))) Codes8 {
+  uint32_t w[2];
+};
+
 template <int XT>
 __device__ __forceinline__ void load8(const void* base, int64_t e, float (&x)[8]) {
   if constexpr (XT == kF32) {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + e);
-    const float4 a = p[0], b = p[1];
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    const F32x8 v = *reinterpret_cast<const F32x8*>(static_cast<const float*>(base) + e);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = v.w[i];
   } else {
-    const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + e);
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+    const Bf16x8 v = *reinterpret_cast<const Bf16x8*>(static_cast<const uint16_t*>(base) + e);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      x[2 * i] = __uint_as_float(v.w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(v.w[i] & 0xFFFF0000u);
     }
   }
 }
 
 __device__ __forceinline__ void store8(int dt, void* base, int64_t e, const float (&x)[8]) {
   if (dt == kF32) {
-    float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + e);
-    p[0] = make_float4(x[0], x[1], x[2], x[3]);
-    p[1] = make_float4(x[4], x[5], x[6], x[7]);
+    F32x8 v;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v.w[i] = x[i];
+    *reinterpret_cast<F32x8*>(static_cast<float*>(base) + e) = v;
   } else {
     bf16x8 y;
 #pragma unroll
     for (int i = 0; i < 8; ++i) y[i] = static_cast<__bf16>(x[i]);
-    *reinterpret_cast<bf16x8*>(static_cast<uint16_t*>(base) + e) = y;
+    *reinterpret_cast<Bf16x8*>(static_cast<uint16_t*>(base) + e) = __builtin_bit_cast(Bf16x8, y);
   }
 }
 
@@ -70,16 +80,19 @@ __device__ __forceinline__ void part_sums(float (&ss)[V], int lanes) {
   if constexpr (O < kWave / 2) part_sums<2 * O>(ss, lanes);
 }
 
-// Parts that are multiples of 8 elements.  T threads per row, V vectors of 8
-// elements in registers per thread: one read of x and residual, one write.
-// Parts of a row (GROUPED) are 2^k <= 64 vectors, neighbouring lanes of a wave,
-// so that their sums are shuffles.  Bound by memory traffic: 8192 rows of 64
-// parts of 128, bf16 -> fp8 (201 MB), @NORM_BIG@; 32 rows of 4096
-// with residual, @NORM_SMALL@.
-template <int XT, int T, int V, bool GROUPED>
-__global__ __launch_bounds__(256) void norm_kernel(int32_t rows, int32_t n, int32_t part_vecs,
-                                                   int32_t out_dtype, float inv_size, float eps,
-                                                   const void* x, const void* residual,
+// T threads per row, V vectors of eight elements in registers per thread: one
+// read of x and residual, one write.  The parts of a row (GROUPED) have 2^k <=
+// 64 places of a vector each, neighbouring lanes of a wave, of which the last
+// may be empty, so that their sums are register moves.  ODD: a row's length is
+// no multiple of eight; its last vector ends with the row, and the elements that
+// the one before already has are left out of sums and stores.  Bound by memory
+// traffic: 8192 rows of 64 parts of 128, bf16 -> fp8 (201 MB), 42 us, 4.8 TB/s;
+// 32 rows of 4096 with residual, 3.8 us, a launch and two loads' latency.
+template <int XT, int T, int V, bool GROUPED, bool ODD>
+__global__ __launch_bounds__(256) void norm_kernel(int32_t rows, int32_t n, int32_t groups,
+                                                   int32_t part_shift, int32_t out_dtype,
+                                                   float inv_size, float eps, const void* x,
+                                                   const void* residual,
                                                    const float* __restrict__ weight, void* sum_out,
                                                    void* __restrict__ out,
                                                    float* __restrict__ out_scale) {
@@ -88,49 +101,78 @@ __global__ __launch_bounds__(256) void norm_kernel(int32_t rows, int32_t n, int3
   const int64_t row = static_cast<int64_t>(blockIdx.x) * (256 / T) + threadIdx.x / T;
   if (row >= rows) return;  // T < 256: whole rows of lanes leave; T = 256: never
   const int64_t base = row * n;
-  const int nv = n / 8;
-  float y[V][8];
-  float ss[V];
+  const int32_t size = n / groups;
+  // Place v * T + t: its element in the row and in its part, and how many of its
+  // elements are left out; false: an empty place.
+  auto place = [&](int v, int& e, int& w, int& skip) {
+    const int i = v * T + t;
+    skip = 0;
+    if constexpr (GROUPED) {
+      const int part = i >> part_shift, at = (i & ((1 << part_shift) - 1)) * 8;
+      e = part * size + at;
+      w = min(at, size - 8);
+      return part < groups && at < size;
+    } else {
+      e = i * 8;
+      const bool inside = e < n;
+      if (ODD && inside) skip = max(e + 8 - n, 0);
+      e -= skip;
+      w = min(e, n - 8);
+      return inside;
+    }
+  };
+  auto store = [&](int dt, void* to, int e, int skip, const float(&z)[8]) {
+    if (!ODD || skip == 0) {
+      store8(dt, to, base + e, z);
+    } else {
+#pragma unroll
+      for (int i = 1; i < 8; ++i)
+        if (i >= skip) store_elem(dt, to, base + e + i, z[i]);
+    }
+  };
+  float y[V][8], ss[V];
+  int e, at, skip;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int i = v * T + t;
-    ss[v] = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[v][e] = 0.f;
-    if (i < nv) load8<XT>(x, base + i * 8, y[v]);
+    for (int i = 0; i < 8; ++i) y[v][i] = 0.f;
+    if (place(v, e, at, skip)) load8<XT>(x, base + e, y[v]);
   }
   if (residual) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int i = v * T + t;
-      if (i < nv) {
+      if (place(v, e, at, skip)) {
         float z[8];
-        load8<XT>(residual, base + i * 8, z);
+        load8<XT>(residual, base + e, z);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[v][e] += z[e];
+        for (int i = 0; i < 8; ++i) y[v][i] += z[i];
       }
     }
   }
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    if (sum_out && v * T + t < nv) store8(XT, sum_out, base + (v * T + t) * 8, y[v]);
+    const bool inside = place(v, e, at, skip);
+    if (sum_out && inside) store(XT, sum_out, e, skip, y[v]);
+    ss[v] = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) ss[v] += y[v][e] * y[v][e];
+    for (int i = 0; i < 8; ++i) {
+      if (ODD && i < skip) y[v][i] = 0.f;
+      ss[v] += y[v][i] * y[v][i];
+    }
   }
-  // Few vectors: the weights are on their way during the reduction.
-  constexpr int WV = V <= 4 ? V : 1;
-  float w[WV][8];
-  auto load_w = [&](int v, float (&to)[8]) {
-    const int i = v * T + t;
-    load8<kF32>(weight, (GROUPED ? i & (part_vecs - 1) : min(i, nv - 1)) * 8, to);
-  };
-  if constexpr (V <= 4) {
+  // Few elements: the weights are on their way during the reduction.
+  constexpr bool kEarly = V <= 4;
+  float w[kEarly ? V : 1][8];
+  if constexpr (kEarly) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) load_w(v, w[v]);
+    for (int v = 0; v < V; ++v) {
+      place(v, e, at, skip);
+      load8<kF32>(weight, at, w[v]);
+    }
   }
   float r[V];
   if constexpr (GROUPED) {
-    part_sums<1>(ss, part_vecs);
+    part_sums<1>(ss, 1 << part_shift);
 #pragma unroll
     for (int v = 0; v < V; ++v) r[v] = __builtin_amdgcn_rsqf(ss[v] * inv_size + eps);
   } else {
@@ -144,35 +186,41 @@ __global__ __launch_bounds__(256) void norm_kernel(int32_t rows, int32_t n, int3
   float amax = 0.f;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int i = v * T + t;
-    if (i < nv) {
-      if constexpr (V > 4) load_w(v, w[0]);
+    const bool inside = place(v, e, at, skip);
+    if constexpr (!kEarly) load8<kF32>(weight, at, w[0]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        y[v][e] = y[v][e] * r[v] * w[V <= 4 ? v : 0][e];
-        amax = amax_step(amax, y[v][e]);
-      }
+    for (int i = 0; i < 8; ++i) {
+      y[v][i] = y[v][i] * r[v] * w[kEarly ? v : 0][i];
+      if (inside && !(ODD && i < skip)) amax = amax_step(amax, y[v][i]);
     }
   }
   if (out_dtype != kFP8) {
 #pragma unroll
     for (int v = 0; v < V; ++v)
-      if (v * T + t < nv) store8(out_dtype, out, base + (v * T + t) * 8, y[v]);
+      if (place(v, e, at, skip)) store(out_dtype, out, e, skip, y[v]);
     return;
   }
   float scale, mult;
   e4m3_scale(row_reduce<T, true>(amax, tmp[1]), scale, mult);
+  auto* codes = static_cast<uint8_t*>(out) + base;
 #pragma unroll
-  for (int v = 0; v < V; ++v)
-    if (v * T + t < nv)
-      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(out) + base + (v * T + t) * 8) =
-          make_uint2(e4m3_pack4(y[v][0], y[v][1], y[v][2], y[v][3], mult),
-                     e4m3_pack4(y[v][4], y[v][5], y[v][6], y[v][7], mult));
+  for (int v = 0; v < V; ++v) {
+    if (!place(v, e, at, skip)) continue;
+    const Codes8 c = {{e4m3_pack4(y[v][0], y[v][1], y[v][2], y[v][3], mult),
+                       e4m3_pack4(y[v][4], y[v][5], y[v][6], y[v][7], mult)}};
+    if (!ODD || skip == 0) {
+      *reinterpret_cast<Codes8*>(codes + e) = c;
+    } else {
+#pragma unroll
+      for (int i = 1; i < 8; ++i)
+        if (i >= skip) codes[e + i] = static_cast<uint8_t>(c.w[i / 4] >> (i % 4 * 8));
+    }
+  }
   if (t == 0) out_scale[row] = scale;
 }
 
 struct NormArgs {
-  int32_t rows, n, groups, x_dtype, out_dtype;
+  int32_t rows, n, groups, part_shift, x_dtype, out_dtype;
   float eps;
   const void *x, *residual;
   const float* weight;
@@ -180,31 +228,37 @@ struct NormArgs {
   float* out_scale;
 };
 
-template <int XT, int T, int V, bool GROUPED>
+template <int XT, int T, int V, bool GROUPED, bool ODD>
 void launch_norm(const NormArgs& a, hipStream_t st) {
-  const int32_t size = a.n / a.groups;
   const int32_t per = 256 / T;
-  norm_kernel<XT, T, V, GROUPED><<<(a.rows - 1) / per + 1, 256, 0, st>>>(
-      a.rows, a.n, size / 8, a.out_dtype, 1.f / static_cast<float>(size), a.eps, a.x, a.residual,
-      a.weight, a.sum_out, a.out, a.out_scale);
+  norm_kernel<XT, T, V, GROUPED, ODD><<<(a.rows - 1) / per + 1, 256, 0, st>>>(
+      a.rows, a.n, a.groups, a.part_shift, a.out_dtype, 1.f / static_cast<float>(a.n / a.groups),
+      a.eps, a.x, a.residual, a.weight, a.sum_out, a.out, a.out_scale);
 }
 
-// Threads per row and vectors per thread, by the row's length: rows up to 128
-// (512) elements share a wave (workgroup), longer ones have a workgroup, whose
-// registers hold up to 32768.
-template <int XT, bool GROUPED>
+// Threads per row and vectors per thread, by the vectors' places in a row: up to
+// 16 (64) a row shares a wave (workgroup), longer ones have a workgroup, whose
+// registers hold up to 4096.
+template <int XT, bool GROUPED, bool ODD>
 void launch_norm_size(const NormArgs& a, hipStream_t st) {
-  const int32_t nv = a.n / 8;
-  if (nv <= 16) launch_norm<XT, 16, 1, GROUPED>(a, st);
-  else if (nv <= 64) launch_norm<XT, 64, 1, GROUPED>(a, st);
-  else if (nv <= 256) launch_norm<XT, 256, 1, GROUPED>(a, st);
-  else if (nv <= 512) launch_norm<XT, 256, 2, GROUPED>(a, st);
-  else if (nv <= 1024) launch_norm<XT, 256, 4, GROUPED>(a, st);
-  else if (nv <= 2048) launch_norm<XT, 256, 8, GROUPED>(a, st);
-  else launch_norm<XT, 256, 16, GROUPED>(a, st);
+  const int32_t places = GROUPED ? a.groups << a.part_shift : (a.n + 7) / 8;
+  if (places <= 16) launch_norm<XT, 16, 1, GROUPED, ODD>(a, st);
+  else if (places <= 64) launch_norm<XT, 64, 1, GROUPED, ODD>(a, st);
+  else if (places <= 256) launch_norm<XT, 256, 1, GROUPED, ODD>(a, st);
+  else if (places <= 512) launch_norm<XT, 256, 2, GROUPED, ODD>(a, st);
+  else if (places <= 1024) launch_norm<XT, 256, 4, GROUPED, ODD>(a, st);
+  else if (places <= 2048) launch_norm<XT, 256, 8, GROUPED, ODD>(a, st);
+  else launch_norm<XT, 256, 16, GROUPED, ODD>(a, st);
 }
 
-// Every other n and groups: one workgroup per row, the row's sums in LDS; wave w
+template <int XT>
+void launch_norm_type(const NormArgs& a, hipStream_t st) {
+  if (a.groups > 1) launch_norm_size<XT, true, false>(a, st);
+  else if (a.n % 8 == 0) launch_norm_size<XT, false, false>(a, st);
+  else launch_norm_size<XT, false, true>(a, st);
+}
+
+// Rows below eight elements and every other division into parts: one workgroup per row, the row's sums in LDS; wave w
 // takes the parts w, w + 4, ... one after the other.
 template <int XT>
 __global__ __launch_bounds__(256) void norm_any_kernel(int32_t n, int32_t size, int32_t out_dtype,
@@ -259,13 +313,16 @@ hipError_t launch_rms_norm(int32_t rows, int32_t n, int32_t groups, int32_t x_dt
                            const float* weight, void* sum_out, void* out, float* out_scale,
                            hipStream_t st) {
   const int32_t size = n / groups;
-  const bool pow2 = (size & (size - 1)) == 0;
-  if (size % 8 == 0 && (groups == 1 || (pow2 && size <= 512))) {
-    const NormArgs a{rows, n, groups, x_dtype, out_dtype, eps, x, residual, weight, sum_out, out, out_scale};
+  int32_t shift = 0;  // 2^shift places of eight elements hold a part
+  while (groups > 1 && (8 << shift) < size) ++shift;
+  const bool in_registers =
+      groups == 1 ? n >= 8 : (size % 8 == 0 && shift <= 6 && (static_cast<int64_t>(groups) << shift) * 8 <= kMaxNorm);
+  if (in_registers) {
+    const NormArgs a{rows, n, groups, shift, x_dtype, out_dtype, eps, x, residual, weight, sum_out, out, out_scale};
     if (x_dtype == kF32)
-      groups == 1 ? launch_norm_size<kF32, false>(a, st) : launch_norm_size<kF32, true>(a, st);
+      launch_norm_type<kF32>(a, st);
     else
-      groups == 1 ? launch_norm_size<kBF16, false>(a, st) : launch_norm_size<kBF16, true>(a, st);
+      launch_norm_type<kBF16>(a, st);
     return hipGetLastError();
   }
   const size_t lds = static_cast<size_t>(n) * sizeof(float);
