@@ -243,6 +243,8 @@ misa_status misa_hisa_score_topk(const misa_shape* shape, int32_t h, int32_t m, 
  * Conventions on top of those above:
  *  - The limits on d, H, h and k above are the indexer's; each entry point
  *    below states its own.
+ *  - Calls that read or change one cache are ordered by the caller (one stream,
+ *    or events); calls on different caches are independent.
  *  - Integer arrays the calls read on the device (tables, lengths, lists) are
  *    checked there: an entry that names nothing (a row outside [0, rows), a
  *    page outside [0, pages), a position beyond the table) is skipped, and
@@ -269,9 +271,8 @@ misa_status misa_hisa_score_topk(const misa_shape* shape, int32_t h, int32_t m, 
  * kv_dtype is MISA_BF16 or MISA_FP8_E4M3.  Limits: rows, row_pages, pages and
  * page_tokens >= 1, page_tokens <= 4096, kv_heads <= 256, rows * row_pages <
  * 2^31, row_pages * page_tokens <= 2^30, rows <= 2^20, pages <= 2^24, pages *
- * kv_heads * page_tokens < 2^32 - 1.  The
- * calls that touch only tables, lengths and refs ignore kv_heads, dk, dv and
- * kv_dtype. */
+ * kv_heads * page_tokens < 2^32 - 1.  The calls that touch only tables, lengths
+ * and refs ignore kv_heads, dk, dv and kv_dtype. */
 typedef struct {
   int32_t rows, row_pages, pages, page_tokens;
   int32_t kv_heads, dk, dv;
@@ -309,7 +310,7 @@ misa_status misa_attend(const misa_cache* cache, int32_t heads, int32_t k, float
  * misa_page_extend keeps it, once per step for every layer.
  *   row, pos  [n]  int32
  *   k_new  [n, kv_heads, dk]  bf16        v_new  [n, kv_heads, dv]  bf16
- * n = 0 is a no-op; n * kv_heads < 2^31. */
+ * n = 0 is a no-op; n * kv_heads <= 2^25. */
 misa_status misa_page_write(const misa_cache* cache, int32_t n, const int32_t* row,
                             const int32_t* pos, const void* k_new, const void* v_new,
                             void* k_pages, float* k_scale, void* v_pages, float* v_scale,
@@ -391,9 +392,10 @@ misa_status misa_page_copy(const misa_page_buffer* buffers, int32_t n_buffers, i
  *   sum_out      [rows, n]  x_dtype, y, written if non-NULL (may be x or residual)
  *   out          [rows, n]  out_dtype (any misa_dtype), written
  *   out_scale    [rows]     fp32, written (fp8 only, else ignored)
- * fp32 throughout: y^2 must stay in fp32's range.  rows >= 0 (0: no-op), 1 <=
- * n <= 32768, groups divides n, eps >= 0; an all-zero part with eps = 0 gives
- * NaN. */
+ * out must not overlap the inputs or sum_out.  fp32 throughout: a part's mean
+ * square plus eps must be in fp32's normal range (an all-zero part with eps = 0
+ * gives NaN).  0 <= rows < 2^24 (0: no-op), 1 <= n <= 32768, groups divides n,
+ * eps >= 0. */
 misa_status misa_rms_norm(int32_t rows, int32_t n, int32_t groups, int32_t x_dtype,
                           int32_t out_dtype, float eps, const void* x, const void* residual,
                           const float* weight, void* sum_out, void* out, float* out_scale,

@@ -247,15 +247,15 @@ def _dev(x):
 
 
 def _call(fn: str, tensor, args, stream):
-    """Calls the entry point on `stream`, by default the current one of `tensor`'s device, which is
-    the current device while the call is made."""
+    """Calls the entry point with the device of `tensor` as the current one, on `stream` (by default
+    that device's current one)."""
     f = getattr(_lib, fn)
-    if stream is None and tensor.__class__ is not int and tensor is not None:
+    if tensor is not None and tensor.__class__ is not int:
         device = tensor.get_device()
         if device != _current_device():
             import torch
             with torch.cuda.device(device):
-                return _check(f(*args, _stream(None)), fn)
+                return _check(f(*args, _stream(stream)), fn)
     _check(f(*args, _stream(stream)), fn)
 
 

@@ -110,7 +110,7 @@ misa_status misa_page_write(const misa_cache* cache, int32_t n, const int32_t* r
   Cache c;
   MISA_TRY(check_cache(cache, c));
   if (n < 0) return MISA_ERR_INVALID_ARG;
-  if (static_cast<int64_t>(n) * c.kv_heads >= (int64_t{1} << 31)) return MISA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(n) * c.kv_heads > (int64_t{1} << 25)) return MISA_ERR_UNSUPPORTED;
   MISA_TRY(check_pools(c, k_pages, k_scale, v_pages, v_scale));
   MISA_TRY(check_out(table, true));
   if (n == 0) return MISA_OK;
@@ -225,7 +225,8 @@ misa_status misa_rms_norm(int32_t rows, int32_t n, int32_t groups, int32_t x_dty
       out_dtype > MISA_FP8_E4M3)
     return MISA_ERR_INVALID_ARG;
   if (!(eps >= 0.f) || !std::isfinite(eps)) return MISA_ERR_INVALID_ARG;
-  if (x_dtype == MISA_FP8_E4M3 || n > misa::kMaxNorm) return MISA_ERR_UNSUPPORTED;
+  if (x_dtype == MISA_FP8_E4M3 || n > misa::kMaxNorm || rows >= (1 << 24))
+    return MISA_ERR_UNSUPPORTED;
   if (rows == 0) return MISA_OK;
   MISA_TRY(check_out(x, true));
   MISA_TRY(check_out(residual, false));

@@ -21,8 +21,8 @@ constexpr float kSlack = 8.f;
 constexpr uint32_t kHidden = 0xFFFFFFFFu;  // the slot of a token that is not visible
 
 // n / P for 0 <= n < 2^31 by a multiplication: with l = ceil(log2 P), m =
-// floor(2^(31+l) / P) + 1 exceeds 2^(31+l) / P by less than 2^l / P * P, so
-// n * m >> (31+l) is the quotient.
+// floor(2^(31+l) / P) + 1 is at most 1 above 2^(31+l) / P, so n * m / 2^(31+l)
+// exceeds n / P by less than n / 2^(31+l) < 2^-l <= 1 / P: the same quotient.
 struct Div {
   uint32_t m, shift, P;
 };

@@ -144,13 +144,22 @@ def test_norm_refuses(misa):
                    dict(eps=math.nan), dict(x=None), dict(w=None), dict(out=None), dict(scale=None), dict(x=FAKE + 8),
                    dict(res=FAKE + 2), dict(s=FAKE + 4)):
         assert call(**change) == -1, change
-    assert call(xt=2) == -2 and call(n=32769) == -2
+    assert call(xt=2) == -2 and call(n=32769) == -2 and call(rows=1 << 24) == -2
     assert call(rows=0, x=None, w=None, out=None, scale=None) == 0
 
 
 def test_binding_raises(misa):
     with pytest.raises(misa.MisaError, match="misa_page_free"):
         misa.misa_page_free(misa.cache(4, 8, 40, 16, 0, 0, 0, 0), -1, FAKE, FAKE, FAKE, FAKE, stream=0)
+
+
+def test_binding_refuses_host_and_strided_tensors(misa):
+    c = misa.cache(4, 8, 40, 16, 0, 0, 0, 0)
+    host = torch.zeros(32, dtype=torch.int32)
+    with pytest.raises(ValueError, match="contiguous and on the device"):
+        misa.misa_page_free(c, 1, host, FAKE, FAKE, FAKE, stream=0)
+    with pytest.raises(ValueError, match="contiguous and on the device"):
+        misa.page_buffers([(host, 1, 4)])
 
 
 # ------------------------------------------------------------------ inputs
@@ -338,6 +347,16 @@ def test_attend_splits_long_rows(misa):
         got, lse = _check_attend(misa, *case)
         again, _ = _run_attend(misa, *case, want_lse=False)
         assert torch.equal(got.view(torch.int16), again.view(torch.int16))
+
+
+@gpu
+@pytest.mark.parametrize("dk,dv,dtype", [(64, 64, 1), (64, 64, 2), (128, 128, 1), (128, 128, 2), (256, 256, 1), (256, 256, 2)])
+def test_attend_large_caches(misa, dk, dv, dtype):
+    """Caches of more than 64 MB, read with loads that are not kept; a row of a few tokens beside a long one."""
+    n = (70 << 20) // (2 * (dk + dv) * (2 if dtype == 1 else 1))
+    case = _attend_case(misa, dk, dv, 1, 2, 64, [n, 77], dtype, seed=8)
+    _log(f"[gpu] attend large dk {dk} dtype {dtype} n {n}")
+    _check_attend(misa, *case)
 
 
 @gpu
@@ -588,6 +607,91 @@ def test_page_copy(misa, page_bytes):
         assert torch.equal(x.cpu()[:-64], w.flatten()) and torch.all(x[-64:] == 9)
 
 
+@gpu
+def test_page_copy_long_lists(misa):
+    """More pieces than workgroups of a grid: pairs far down the list, the others skipped."""
+    pages, n = 50, 200000
+    data = torch.randint(0, 256, (2, pages, 64), dtype=torch.uint8)
+    src = torch.full((n,), -1, dtype=torch.int32)
+    dst = src.clone()
+    want = data.clone()
+    for i, (a, b) in enumerate([(3, 4), (10, 0), (49, 20)]):
+        src[n - 1 - 70000 * i], dst[n - 1 - 70000 * i] = a, b
+        want[:, b] = data[:, a]
+    dev = data.cuda()
+    _log("[gpu] copy long list")
+    misa.misa_page_copy(misa.page_buffers([(dev, 2, 64)]), pages, n, src.cuda(), dst.cuda())
+    assert torch.equal(dev.cpu(), want)
+
+
+@gpu
+def test_captured_bookkeeping(misa):
+    """Free, fork, copy, extend and compact in one graph, replayed with eager work between, each replay against the
+    reference."""
+    rng = np.random.default_rng(12)
+    book = _book(misa, 24, 12, 300, 4)
+    dev = Device(misa, book)
+    first = list(range(12)), rng.integers(0, 40, 12).tolist()
+    assert dev.extend(*first) == book.extend(*first)
+    n = 8
+    rows, parent, child, grow, count = (dev.ints([0] * n) for _ in range(5))
+    src, dst, ok, more = (dev.ints([0] * n) for _ in range(4))
+    pmap, live = dev.ints([0] * 300), dev.ints([0])
+    msrc, mdst = dev.ints([0] * 150), dev.ints([0] * 150)
+    ws = torch.empty(misa.misa_page_workspace_bytes(book.c), dtype=torch.uint8, device="cuda")
+    data = torch.arange(300, dtype=torch.int32, device="cuda").view(300, 1).repeat(1, 4)
+    bufs = misa.page_buffers([(data, 1, 16)])
+
+    def step():
+        c = book.c
+        misa.misa_page_free(c, n, rows, dev.table, dev.lengths, dev.refs)
+        misa.misa_page_fork(c, n, parent, child, dev.table, dev.lengths, dev.refs, src, dst, ok)
+        misa.misa_page_copy(bufs, 300, n, src, dst)
+        misa.misa_page_extend(c, n, grow, count, dev.table, dev.lengths, dev.refs, more)
+        misa.misa_page_compact(c, dev.table, dev.refs, dev.table, dev.refs, pmap, live, msrc, mdst, ws)
+        misa.misa_page_copy(bufs, 300, 150, msrc, mdst)
+
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    state = [x.clone() for x in (dev.table, dev.lengths, dev.refs)]
+    with torch.cuda.stream(side):
+        step()  # all entries name row 0: a first run before the capture
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        step()
+    for x, y in zip((dev.table, dev.lengths, dev.refs), state):
+        x.copy_(y)
+    pool = np.arange(300)[:, None].repeat(4, 1)
+    data.copy_(torch.from_numpy(pool.astype(np.int32)))
+    for turn in range(5):
+        values = [rng.integers(-1, 25, n), rng.integers(-1, 25, n), rng.integers(-1, 25, n), rng.integers(-1, 25, n),
+                  rng.integers(0, 12, n)]
+        for x, y in zip((rows, parent, child, grow, count), values):
+            x.copy_(torch.from_numpy(y.astype(np.int32)))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        r, p, h, g, k = (v.tolist() for v in values)
+        book.free(r)
+        fsrc, fdst, fok = book.fork(p, h)
+        for a, b in zip(fsrc, fdst):
+            if a >= 0:
+                pool[b] = pool[a]
+        fmore = book.extend(g, k)
+        wmap, wlive, csrc, cdst = book.compact()
+        moved = pool.copy()
+        for a, b in zip(csrc, cdst):
+            if a >= 0:
+                moved[b] = pool[a]
+        pool = moved
+        assert (src.tolist(), dst.tolist(), ok.tolist(), more.tolist()) == (fsrc, fdst, fok, fmore), turn
+        assert (pmap.tolist(), live.tolist()) == (wmap, [wlive]), turn
+        dev.same(book)
+        assert (data.cpu().numpy() == pool).all()
+        assert int(torch.ones(1000, device="cuda").sum()) == 1000  # eager work between replays
+
+
 # ------------------------------------------------------------------ the norm
 
 
@@ -626,6 +730,8 @@ def _check_norm(misa, rows, n, groups, xt, ot, eps, x, residual, weight, in_plac
 @pytest.mark.parametrize("rows,n,groups", [
     (1, 1, 1), (3, 17, 1), (5, 128, 1), (2, 130, 2), (7, 1000, 1), (2, 4096, 1), (3, 8192, 64), (2, 896, 8), (1, 32768, 1),
     (2, 32768, 256), (9, 512, 4), (3, 2048, 8), (4, 12, 12), (130, 64, 1), (2, 16384, 1), (2, 5120, 40), (1, 20000, 1),
+    (5, 7, 1), (300, 8, 1), (33, 9, 1), (70, 127, 1), (9, 513, 1), (3, 4095, 1), (2, 8191, 1), (2, 16383, 1), (2, 32767, 1),
+    (7, 1002, 1), (3, 24, 3), (2, 1120, 2), (2, 8000, 8), (40, 96, 12), (2, 30000, 2),
 ])
 def test_norm(misa, rows, n, groups, xt, ot):
     gen = torch.Generator().manual_seed(n)
