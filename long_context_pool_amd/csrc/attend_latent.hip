@@ -19,7 +19,7 @@ __device__ __forceinline__ void barrier() {
 // This wave's direct loads to LDS have landed.
 __device__ __forceinline__ void landed() { __builtin_amdgcn_s_waitcnt(0x0F70); }
 
-constexpr int kLatentStage = 512;  // tokens whose slots are in LDS at a time
+constexpr int kLatentStage = 512;  // tokens whose slots are in LDS at a time: one per thread
 
 // The end of a workgroup's work, for token group G (both meet in the barriers):
 // the groups' sums are joined a quarter of the dimensions at a time; each group
@@ -141,19 +141,12 @@ __global__ __launch_bounds__(512) void attend_latent_kernel(Args a) {
   if (t0 >= t1 && split > 0) return;
 
   bf16x8 qf[KS - QL];
-  {
-    const int h = head0 + c < a.heads ? head0 + c : 0;
-    const uint16_t* src = a.q + (static_cast<int64_t>(row) * a.heads + h) * kLatentK;
-#pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      const int d0 = kFp8 ? 64 * (s / 2) + 16 * g + 8 * (s % 2) : 32 * s + 8 * g;
-      const uint4 x = *reinterpret_cast<const uint4*>(src + d0);
-      if (s < KS - QL)
-        qf[s] = as_bf16x8(x);
-      else if (grp == 0)
-        q_lds[hw][s - (KS - QL)][lane] = x;
-    }
-  }
+  auto keep_query = [&](int s, uint4 x) {
+    if (s < KS - QL)
+      qf[s] = as_bf16x8(x);
+    else if (grp == 0)
+      q_lds[hw][s - (KS - QL)][lane] = x;
+  };
   auto query = [&](int s) {
     return s < KS - QL ? qf[s < KS - QL ? s : 0] : as_bf16x8(q_lds[hw][s < KS - QL ? 0 : s - (KS - QL)][lane]);
   };
@@ -212,6 +205,38 @@ __global__ __launch_bounds__(512) void attend_latent_kernel(Args a) {
   } else {
     const int vr = 4 * g + c / 4;
     voff = vr * kRow + ((c / 2 % 2) ^ swz(vr)) * 16 + c % 2 * 8;
+  }
+
+  // The queries.  Beside a bf16 cache they have the shape of two tiles of 32 rows,
+  // one for each group to load, into the buffer that the first pair leaves free;
+  // a wave's fragments are those of a key.
+  if constexpr (!kFp8) {
+    const int h = min(chunk * kLatentHeads + grp * 32 + r, a.heads - 1);
+    const uint8_t* src = reinterpret_cast<const uint8_t*>(a.q) +
+                         (static_cast<int64_t>(row) * a.heads + h) * (kLatentK * 2) + (lane % CB ^ swz(r)) * 16;
+#pragma unroll
+    for (int n = 0; n < NI; ++n) issue(n, src, odd);
+  } else {
+    const int h = min(head0 + c, a.heads - 1);
+    const uint16_t* src = a.q + (static_cast<int64_t>(row) * a.heads + h) * kLatentK;
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+      keep_query(s, *reinterpret_cast<const uint4*>(src + 64 * (s / 2) + 16 * g + 8 * (s % 2)));
+  }
+  auto fill = [&](int32_t base) {  // slots (and scales) of the stage at `base`: one per thread
+    const int32_t i = threadIdx.x, count = min(kLatentStage, t1 - base);
+    const uint32_t s = i < count ? slot_of(a, row, 0, len, base + i) : kHidden;
+    slots[i] = s;
+    if constexpr (kFp8) scales[i] = s == kHidden ? 0.f : a.k_scale[s];
+  };
+  fill(t0);
+  if constexpr (!kFp8) {
+    landed();
+    __syncthreads();
+    const uint8_t* buf = reinterpret_cast<const uint8_t*>(odd[hw / 2]) + 16 * (hw % 2) * kRow;
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+      keep_query(s, *reinterpret_cast<const uint4*>(buf + (koff ^ (s % 2 * 64)) + s / 2 * kBlock));
   }
 
   bool hidden = false;
@@ -325,13 +350,10 @@ __global__ __launch_bounds__(512) void attend_latent_kernel(Args a) {
   };
 
   for (int32_t base = t0; base < t1; base += kLatentStage) {
-    const int32_t count = min(kLatentStage, t1 - base);
-    const int32_t pairs = (count + 63) / 64;
-    if (base != t0) __syncthreads();
-    for (int32_t i = threadIdx.x; i < pairs * 64; i += 512) {
-      const uint32_t s = i < count ? slot_of(a, row, 0, len, base + i) : kHidden;
-      slots[i] = s;
-      if constexpr (kFp8) scales[i] = s == kHidden ? 0.f : a.k_scale[s];
+    const int32_t pairs = (min(kLatentStage, t1 - base) + 63) / 64;
+    if (base != t0) {
+      __syncthreads();
+      fill(base);
     }
     __syncthreads();
     const uint8_t* src;
