@@ -357,13 +357,32 @@ int group_heads(const Cache& c, int32_t share) {
 
 // Workgroups that a CU holds at a time, by the kernels' registers.
 int resident(const Cache& c, int32_t share) {
-  if (c.latent()) return 1;
   const int one = c.dk == 64 ? 4 : c.dk == 128 ? 3 : 2;
   return group_heads(c, share) == 32 ? one - 1 : one;
 }
 
 constexpr int kCus = 256;
 constexpr int kMaxSplits = 128;
+constexpr int kWholeTokens = 512;
+
+// Splits of a latent row.  A workgroup (one per CU) takes about 3.1 us for a
+// pair of tiles; a join costs about 4 us and, for each split, the way of its
+// sums to memory and back, 4 KB a head at 4.5 TB/s.  32 rows of 128 heads: 256
+// listed tokens 19.4 us whole, 25.1 us in two splits; 2048 88 us whole, 60 us in
+// two, 46 us in four.
+int32_t latent_splits(int64_t groups, int64_t tokens, int64_t heads, int64_t limit) {
+  int32_t best = 1;
+  double least = 0;
+  for (int32_t s = 1; s <= limit; ++s) {
+    const int64_t pairs = (tokens + s * 64 - 1) / (s * 64), rounds = (groups * s + kCus - 1) / kCus;
+    const double us = 3.1 * pairs * rounds + (s > 1 ? 4.0 + s * heads * (4096 / 4.5e6) : 0.0);
+    if (s == 1 || us < least) {
+      best = s;
+      least = us;
+    }
+  }
+  return best;
+}
 
 struct Plan {
   int32_t chunks, splits;
@@ -382,15 +401,21 @@ Plan plan(const Cache& c, int32_t heads, int32_t k) {
   p.chunks = (share + per - 1) / per;
   const int64_t groups = static_cast<int64_t>(c.rows) * c.kv_heads * p.chunks;
   const int64_t most = k > 0 ? k : static_cast<int64_t>(c.row_pages) * c.P;
-  // One round of workgroups over the card: more of them only add to the join
-  // and to the last round's tail (8 rows of up to 131072 fp8 tokens: 768
-  // workgroups 322 us, 1024 340 us, 512 342 us; 32 rows x 2048 listed tokens:
-  // 768 58.4 us, 1536 63.2 us).
-  int64_t s = kCus * resident(c, share) / groups;
-  s = std::min<int64_t>(s, (most + kMinSplitTokens - 1) / kMinSplitTokens);
+  const int64_t limit = std::min<int64_t>((most + kMinSplitTokens - 1) / kMinSplitTokens, kMaxSplits);
+  if (c.latent()) {
+    p.splits = latent_splits(groups, most, static_cast<int64_t>(c.rows) * heads, limit);
+  } else {
+    // One round of workgroups over the card: more of them only add to the join
+    // and to the last round's tail (8 rows of up to 131072 fp8 tokens: 768
+    // workgroups 322 us, 1024 340 us, 512 342 us; 32 rows x 2048 listed tokens:
+    // 768 58.4 us, 1536 63.2 us).  Up to 512 tokens the join costs more than the
+    // four tiles that a wave has then (one row of 200 tokens: 6.6 us whole, 9.1
+    // us in two splits; 500: 8.9 us either way; 1000: 13.6 us and 9.2 us).
+    const int64_t s = most <= kWholeTokens ? 1 : kCus * resident(c, share) / groups;
+    p.splits = static_cast<int32_t>(std::max<int64_t>(1, std::min(s, limit)));
+  }
   const int64_t row_bytes = static_cast<int64_t>(c.dk + c.dv) * (c.dtype == kFP8 ? 1 : 2);
   p.once = p.chunks == 1 && c.rows * most * c.kv_heads * row_bytes >= kOnceBytes;
-  p.splits = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(s, kMaxSplits)));
   return p;
 }
 
