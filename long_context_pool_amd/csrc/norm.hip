@@ -80,16 +80,18 @@ __device__ __forceinline__ void part_sums(float (&ss)[V], int lanes) {
   if constexpr (O < kWave / 2) part_sums<2 * O>(ss, lanes);
 }
 
+constexpr int kEarlyWeights = 4;
+
 // T threads per row, V vectors of eight elements in registers per thread: one
 // read of x and residual, one write.  The parts of a row (GROUPED) have 2^k <=
 // 64 places of a vector each, neighbouring lanes of a wave, of which the last
 // may be empty, so that their sums are register moves.  ODD: a row's length is
 // no multiple of eight; its last vector ends with the row, and the elements that
 // the one before already has are left out of sums and stores.  Bound by memory
-// traffic: 8192 rows of 64 parts of 128, bf16 -> fp8 (201 MB), 42 us, 4.8 TB/s;
+// traffic: 8192 rows of 64 parts of 128, bf16 -> fp8 (201 MB), 40.6 us, 5.0 TB/s;
 // 32 rows of 4096 with residual, 3.8 us, a launch and two loads' latency.
 template <int XT, int T, int V, bool GROUPED, bool ODD>
-__global__ __launch_bounds__(256) void norm_kernel(int32_t rows, int32_t n, int32_t groups,
+__global__ __launch_bounds__(256) void norm_kernel(int32_t rows, int32_t n, int32_t size,
                                                    int32_t part_shift, int32_t out_dtype,
                                                    float inv_size, float eps, const void* x,
                                                    const void* residual,
@@ -101,7 +103,6 @@ __global__ __launch_bounds__(256) void norm_kernel(int32_t rows, int32_t n, int3
   const int64_t row = static_cast<int64_t>(blockIdx.x) * (256 / T) + threadIdx.x / T;
   if (row >= rows) return;  // T < 256: whole rows of lanes leave; T = 256: never
   const int64_t base = row * n;
-  const int32_t size = n / groups;
   // Place v * T + t: its element in the row and in its part, and how many of its
   // elements are left out; false: an empty place.
   auto place = [&](int v, int& e, int& w, int& skip) {
@@ -111,7 +112,7 @@ __global__ __launch_bounds__(256) void norm_kernel(int32_t rows, int32_t n, int3
       const int part = i >> part_shift, at = (i & ((1 << part_shift) - 1)) * 8;
       e = part * size + at;
       w = min(at, size - 8);
-      return part < groups && at < size;
+      return e < n && at < size;
     } else {
       e = i * 8;
       const bool inside = e < n;
@@ -160,12 +161,14 @@ __global__ __launch_bounds__(256) void norm_kernel(int32_t rows, int32_t n, int3
       ss[v] += y[v][i] * y[v][i];
     }
   }
-  // Few elements: the weights are on their way during the reduction.
-  constexpr bool kEarly = V <= 4;
-  float w[kEarly ? V : 1][8];
+  // Weights on their way during the reduction: of parts, one vector for all of a
+  // thread's places (T is a multiple of a part's); else where they are few.
+  constexpr bool kEarly = GROUPED || V <= kEarlyWeights;
+  constexpr int WV = GROUPED || !kEarly ? 1 : V;
+  float w[WV][8];
   if constexpr (kEarly) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
+    for (int v = 0; v < WV; ++v) {
       place(v, e, at, skip);
       load8<kF32>(weight, at, w[v]);
     }
@@ -183,22 +186,33 @@ __global__ __launch_bounds__(256) void norm_kernel(int32_t rows, int32_t n, int3
 #pragma unroll
     for (int v = 0; v < V; ++v) r[v] = f;
   }
-  float amax = 0.f;
+  // z = y w now; r, the same for a part, comes in with the last product.
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const bool inside = place(v, e, at, skip);
-    if constexpr (!kEarly) load8<kF32>(weight, at, w[0]);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      y[v][i] = y[v][i] * r[v] * w[kEarly ? v : 0][i];
-      if (inside && !(ODD && i < skip)) amax = amax_step(amax, y[v][i]);
+    if constexpr (!kEarly) {
+      place(v, e, at, skip);
+      load8<kF32>(weight, at, w[0]);
     }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[v][i] *= w[v < WV ? v : 0][i];
   }
   if (out_dtype != kFP8) {
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (place(v, e, at, skip)) store(out_dtype, out, e, skip, y[v]);
+    for (int v = 0; v < V; ++v) {
+      if (!place(v, e, at, skip)) continue;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[v][i] *= r[v];
+      store(out_dtype, out, e, skip, y[v]);
+    }
     return;
+  }
+  float amax = 0.f;  // empty places and left-out elements hold zeros, or NaN if their part does
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = amax_step(top, y[v][i]);
+    amax = fmaxf(amax, top * r[v]);
   }
   float scale, mult;
   e4m3_scale(row_reduce<T, true>(amax, tmp[1]), scale, mult);
@@ -206,8 +220,9 @@ __global__ __launch_bounds__(256) void norm_kernel(int32_t rows, int32_t n, int3
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     if (!place(v, e, at, skip)) continue;
-    const Codes8 c = {{e4m3_pack4(y[v][0], y[v][1], y[v][2], y[v][3], mult),
-                       e4m3_pack4(y[v][4], y[v][5], y[v][6], y[v][7], mult)}};
+    const float f = r[v] * mult;
+    const Codes8 c = {{e4m3_pack4(y[v][0], y[v][1], y[v][2], y[v][3], f),
+                       e4m3_pack4(y[v][4], y[v][5], y[v][6], y[v][7], f)}};
     if (!ODD || skip == 0) {
       *reinterpret_cast<Codes8*>(codes + e) = c;
     } else {
@@ -232,7 +247,7 @@ template <int XT, int T, int V, bool GROUPED, bool ODD>
 void launch_norm(const NormArgs& a, hipStream_t st) {
   const int32_t per = 256 / T;
   norm_kernel<XT, T, V, GROUPED, ODD><<<(a.rows - 1) / per + 1, 256, 0, st>>>(
-      a.rows, a.n, a.groups, a.part_shift, a.out_dtype, 1.f / static_cast<float>(a.n / a.groups),
+      a.rows, a.n, a.n / a.groups, a.part_shift, a.out_dtype, 1.f / static_cast<float>(a.n / a.groups),
       a.eps, a.x, a.residual, a.weight, a.sum_out, a.out, a.out_scale);
 }
 

@@ -15,17 +15,12 @@ __device__ __forceinline__ void e4m3_scale(float amax, float& scale, float& mult
   mult = some ? kE4M3Max / amax : 1.f;
 }
 
-// x * mult clamped to +-448 (the product may round past it), NaN kept.
-__device__ __forceinline__ float e4m3_prepare(float x, float mult) {
-  const float y = x * mult;
-  const float c = __builtin_amdgcn_fmed3f(y, -kE4M3Max, kE4M3Max);
-  return y == y ? c : y;
-}
-
-// Four codes in one dword (hardware conversion, round to nearest even).
+// Four codes of x * mult in one dword (hardware conversion, round to nearest
+// even).  |x| is at most the amax that gave mult, so that a product exceeds 448 by
+// a few roundings at most, and everything below 464 becomes 448: no clamp.
 __device__ __forceinline__ uint32_t e4m3_pack4(float a, float b, float c, float d, float mult) {
-  int r = __builtin_amdgcn_cvt_pk_fp8_f32(e4m3_prepare(a, mult), e4m3_prepare(b, mult), 0, false);
-  r = __builtin_amdgcn_cvt_pk_fp8_f32(e4m3_prepare(c, mult), e4m3_prepare(d, mult), r, true);
+  int r = __builtin_amdgcn_cvt_pk_fp8_f32(a * mult, b * mult, 0, false);
+  r = __builtin_amdgcn_cvt_pk_fp8_f32(c * mult, d * mult, r, true);
   return static_cast<uint32_t>(r);
 }
 
