@@ -80,7 +80,11 @@ __device__ __forceinline__ void part_sums(float (&ss)[V], int lanes) {
   if constexpr (O < kWave / 2) part_sums<2 * O>(ss, lanes);
 }
 
+// Vectors of a thread up to which the weights are loaded before the row's sum is
+// known: with more they cost the registers of a second workgroup on the CU.
 constexpr int kEarlyWeights = 4;
+// 1 / rms beyond which it is multiplied in first.
+constexpr float kFarRoot = 0x1p16f;
 
 // T threads per row, V vectors of eight elements in registers per thread: one
 // read of x and residual, one write.  The parts of a row (GROUPED) have 2^k <=
@@ -186,7 +190,19 @@ __global__ __launch_bounds__(256) void norm_kernel(int32_t rows, int32_t n, int3
 #pragma unroll
     for (int v = 0; v < V; ++v) r[v] = f;
   }
-  // z = y w now; r, the same for a part, comes in with the last product.
+  // z = y w now; r, the same for a part, comes in with the last product.  A large
+  // (small) r comes first: y w of the smallest (largest) values could leave fp32's
+  // range while y r w does not, and so could r times the codes' multiplier.
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const bool first = r[v] > kFarRoot || r[v] < 1.f / kFarRoot;
+    if (__any(first)) {
+      const float f = first ? r[v] : 1.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[v][i] *= f;
+      r[v] = first ? 1.f : r[v];
+    }
+  }
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     if constexpr (!kEarly) {
@@ -273,8 +289,9 @@ void launch_norm_type(const NormArgs& a, hipStream_t st) {
   else launch_norm_size<XT, false, true>(a, st);
 }
 
-// Rows below eight elements and every other division into parts: one workgroup per row, the row's sums in LDS; wave w
-// takes the parts w, w + 4, ... one after the other.
+// Rows below eight elements and every other division into parts: one workgroup
+// per row, the row's sums in LDS; wave w takes the parts w, w + 4, ... one after
+// the other.  Bound by its passes over LDS and the reductions between them.
 template <int XT>
 __global__ __launch_bounds__(256) void norm_any_kernel(int32_t n, int32_t size, int32_t out_dtype,
                                                        float eps, const void* x,

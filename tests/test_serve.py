@@ -130,6 +130,9 @@ def test_copy_refuses(misa):
         assert call(**change) == -1, change
     assert call(n_buffers=9) == -2
     assert call(page_bytes=1 << 31, planes=65536, n=4096) == -2  # more workgroups than a grid holds
+    assert call(page_bytes=1 << 31, planes=65536, pages=1 << 24, n=0) == -2  # offsets beyond 64 bits
+    assert call(page_bytes=1 << 31, planes=1 << 15, pages=1 << 17, n=0) == -2
+    assert call(page_bytes=1 << 31, planes=1 << 14, pages=1 << 17, n=0) == 0
     assert lib.misa_page_copy(None, 1, 10, 3, FAKE, FAKE, None) == -1
     assert call(n=0, src=None, dst=None) == 0
 
@@ -756,6 +759,20 @@ def test_norm_zero_and_tiny_rows(misa):
     scale = torch.empty(4, device="cuda")
     misa.misa_rms_norm(1, 1024, 1, 0, 2, 1e-6, x.cuda(), None, torch.ones(1024, device="cuda"), None, out, scale)
     assert torch.all(out.float() == 0) and scale[0] == 1
+
+
+@gpu
+@pytest.mark.parametrize("n,groups", [(64, 1), (1024, 8), (1001, 1), (4096, 1), (12, 4)])
+@pytest.mark.parametrize("ot", [torch.float32, torch.bfloat16, torch.float8_e4m3fn], ids=["f32", "bf16", "fp8"])
+def test_norm_far_values(misa, n, groups, ot):
+    """Small values with small weights, large ones with large weights: their products leave fp32's range, the result
+    does not.  Ordinary rows beside the far ones."""
+    gen = torch.Generator().manual_seed(n)
+    for value, by in ((1e-16, 1e-25), (1e16, 1e24), (1e-16, 1.0), (1e16, 1e-20)):
+        x = torch.randn(5, n, generator=gen)
+        x[::2] *= value
+        x[3] *= math.sqrt(value)
+        _check_norm(misa, 5, n, groups, torch.float32, ot, 0.0, x, None, by * torch.randn(n // groups, generator=gen))
 
 
 @gpu
