@@ -369,8 +369,8 @@ misa_status misa_page_compact(const misa_cache* cache, const int32_t* table, con
  * bytes each, [planes, pages, page_bytes]. */
 typedef struct {
   void* data;
-  int64_t page_bytes; /* a positive multiple of 4 */
-  int32_t planes;
+  int64_t page_bytes; /* a positive multiple of 4, at most 2^31 */
+  int32_t planes;     /* 1 .. 65536 */
 } misa_page_buffer;
 
 /* Copy page src[i] onto page dst[i], i < n, in every plane of n_buffers (1 ..

@@ -205,8 +205,10 @@ misa_status misa_page_copy(const misa_page_buffer* buffers, int32_t n_buffers, i
     const misa_page_buffer& x = buffers[i];
     MISA_TRY(check_out(x.data, true));
     if (x.page_bytes < 4 || x.page_bytes % 4 != 0 || x.planes < 1) return MISA_ERR_INVALID_ARG;
-    // Byte offsets inside a buffer stay below 2^62.
-    if (x.page_bytes > (int64_t{1} << 32) / 2 || x.planes > 65536) return MISA_ERR_UNSUPPORTED;
+    if (x.page_bytes > (int64_t{1} << 31) || x.planes > 65536) return MISA_ERR_UNSUPPORTED;
+    // Byte offsets inside a buffer stay below 2^62 (pages * planes is at most 2^40).
+    if (x.page_bytes > (int64_t{1} << 62) / (static_cast<int64_t>(pages) * x.planes))
+      return MISA_ERR_UNSUPPORTED;
     b.b[i] = {static_cast<uint8_t*>(x.data), x.page_bytes, x.planes};
   }
   if (n == 0) return MISA_OK;

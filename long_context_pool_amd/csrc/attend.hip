@@ -369,8 +369,10 @@ constexpr int kWholeTokens = 512;
 // pair of tiles; a join costs about 4 us and, for each split, the way of its
 // sums to memory and back, 4 KB a head at 4.5 TB/s.  32 rows of 128 heads: 256
 // listed tokens 19.4 us whole, 25.1 us in two splits; 2048 88 us whole, 60 us in
-// two, 46 us in four.
+// two, 46 us in four.  With sixteen rounds of workgroups and more, a split could
+// save at most a part of the last one.
 int32_t latent_splits(int64_t groups, int64_t tokens, int64_t heads, int64_t limit) {
+  if (groups >= 16 * kCus) return 1;
   int32_t best = 1;
   double least = 0;
   for (int32_t s = 1; s <= limit; ++s) {
