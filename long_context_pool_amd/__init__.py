@@ -6,6 +6,10 @@ their addresses and sizes to ``libmisa.so`` and raises :class:`MisaError` on a
 non-OK status.  All computation happens in the library's HIP kernels; there is
 no CPU fallback -- importing this package fails if the library is not built.
 
+The serving calls at the end (attention over a paged cache, the cache's pages,
+the norm) take contiguous device tensors only and run on their device, on its
+current stream unless one is given.
+
 MISA (Mixture of Indexer Sparse Attention) is the drop-in replacement for the
 DeepSeek Sparse Attention token indexer described on the MISA summary page
 ("MISA: Mixture of Indexer Sparse Attention for Long-Context LLM Inference").
@@ -143,9 +147,11 @@ def _current_device() -> int:
     return _torch_device()
 
 
-def _stream(stream):
+def _stream(stream, device=None):
+    """`device`: the current one, where the caller has looked it up."""
     if stream is None:
-        device = _current_device()
+        if device is None:
+            device = _current_device()
         return _torch_stream(device)
     if isinstance(stream, int):
         return stream
@@ -250,13 +256,14 @@ def _call(fn: str, tensor, args, stream):
     """Calls the entry point with the device of `tensor` as the current one, on `stream` (by default
     that device's current one)."""
     f = getattr(_lib, fn)
+    device = None
     if tensor is not None and tensor.__class__ is not int:
         device = tensor.get_device()
         if device != _current_device():
             import torch
             with torch.cuda.device(device):
                 return _check(f(*args, _stream(stream)), fn)
-    _check(f(*args, _stream(stream)), fn)
+    _check(f(*args, _stream(stream, device)), fn)
 
 
 def cache(rows, row_pages, pages, page_tokens, kv_heads, dk, dv, kv_dtype) -> misa_cache:
