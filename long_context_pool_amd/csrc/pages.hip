@@ -2,6 +2,8 @@
 // fork, free, compact) and page copies.  Layouts are those of misa_cache in
 // include/misa.h.  Every id read from device memory (rows, pages, positions)
 // is range-checked before it becomes an address.
+#include <algorithm>
+
 #include "common.hpp"
 #include "launch.hpp"
 #include "quant.hpp"
@@ -439,6 +441,10 @@ int32_t row_blocks(const Cache& c) {
 // ---------------------------------------------------------------- compaction
 
 constexpr int kCountPages = 1024;  // pages per workgroup: four per thread
+// Up to so many, that every workgroup counts all pages is cheaper than a launch
+// that counts them once (with the copies: 2500 pages 13.8 us against 16.2, 6000
+// pages 15.4 against 16.7; 20000 pages would take 1.0 us more).
+constexpr int kOwnChunks = 8;
 constexpr int kSmallPages = 2048;  // pages and table entries of a compaction by one workgroup
 
 __device__ __forceinline__ int used4(int4 x) { return (x.x > 0) + (x.y > 0) + (x.z > 0) + (x.w > 0); }
@@ -490,22 +496,48 @@ __device__ __forceinline__ void place4(int4 x, int32_t p, int32_t pages, int ran
   }
 }
 
+// Live pages of a wave's 256 pages of a chunk.
+__device__ __forceinline__ int wave_used(int4 x) {
+  return __popcll(__ballot(x.x > 0)) + __popcll(__ballot(x.y > 0)) + __popcll(__ballot(x.z > 0)) +
+         __popcll(__ballot(x.w > 0));
+}
+
 // Second launch: ranks by prefix sums over the counts and a workgroup's pages.
+// OWN: the first one; every workgroup counts the whole pool by itself, a count per
+// chunk and wave.
+template <bool OWN>
 __global__ __launch_bounds__(256) void page_place_kernel(int32_t pages, int32_t chunks,
                                                          const int32_t* __restrict__ refs,
-                                                         const int32_t* __restrict__ counts,
+                                                         const int32_t* __restrict__ counts_in,
                                                          int32_t* __restrict__ map,
                                                          int32_t* __restrict__ live_out,
                                                          int32_t* __restrict__ src,
                                                          int32_t* __restrict__ dst) {
+  constexpr int kEach = OWN ? 4 : 1;  // counts of a chunk
   __shared__ int tmp[4];
+  __shared__ int own[OWN ? kOwnChunks * 4 : 1];
   const int32_t p = blockIdx.x * kCountPages + threadIdx.x * 4;
   const int4 x = refs_or_free(refs, pages, p);
+  if constexpr (OWN) {
+    const int wave = threadIdx.x / kWave, whole = pages / kCountPages;
+    const int4* from = reinterpret_cast<const int4*>(refs) + threadIdx.x;
+#pragma unroll 8
+    for (int b = 0; b < whole; ++b) {
+      const int n = wave_used(from[b * 256]);
+      if (lane_id() == 0) own[4 * b + wave] = n;
+    }
+    if (whole < chunks) {
+      const int n = wave_used(refs_or_free(refs, pages, whole * kCountPages + threadIdx.x * 4));
+      if (lane_id() == 0) own[4 * whole + wave] = n;
+    }
+    __syncthreads();
+  }
+  const int32_t* counts = OWN ? own : counts_in;
   int all = 0, lower = 0;
-  for (int b = threadIdx.x; b < chunks; b += 256) {
+  for (int b = threadIdx.x; b < chunks * kEach; b += 256) {
     const int c = counts[b];
     all += c;
-    lower += b < static_cast<int>(blockIdx.x) ? c : 0;
+    lower += b / kEach < static_cast<int>(blockIdx.x) ? c : 0;
   }
   int live, before, stay, total;
   block_exclusive_sum<256>(all, tmp, live);
@@ -514,7 +546,7 @@ __global__ __launch_bounds__(256) void page_place_kernel(int32_t pages, int32_t 
   const int32_t q = edge * kCountPages + threadIdx.x * 4;
   const int4 y = q < pages ? refs_or_free(refs, pages, q) : make_int4(0, 0, 0, 0);
   int mine = 0;
-  for (int b = threadIdx.x; b < edge; b += 256) mine += counts[b];
+  for (int b = threadIdx.x; b < edge * kEach; b += 256) mine += counts[b];
   mine += (y.x > 0 && q < live) + (y.y > 0 && q + 1 < live) + (y.z > 0 && q + 2 < live) +
           (y.w > 0 && q + 3 < live);
   block_exclusive_sum<256>(lower, tmp, before);
@@ -592,7 +624,12 @@ __global__ __launch_bounds__(256) void page_finish_kernel(
 
 // ---------------------------------------------------------------- copies
 
-constexpr int kCopyBytes = 32768;  // bytes of a page in a piece, which one workgroup copies
+constexpr int kCopyBytes = 32768;  // bytes of a page in a piece
+// Pages up to this size have a wave each, larger ones a workgroup per piece (a
+// pool of 20000 pages compacted, pages of 1 KB: 18.0 us so, 29.0 us with
+// workgroups; of 4 KB 28.2 and 32.0; of 8 KB 43.8 and 42.3.  A pool of 1000 pages
+// of 8 KB: 13.8 and 11.2 us).
+constexpr int64_t kWavePage = 4096;
 
 struct CopyPlan {
   PageBuffers bufs;
@@ -600,19 +637,20 @@ struct CopyPlan {
   int32_t parts[kMaxPageBuffers];  // pieces per page
 };
 
-// N dwords per thread and step, marked as not to be kept: pages go by once
-// (20000 pages of 32 KB, four planes, 1.3 GB: 241 us; 259 us with plain loads
+// N dwords per thread and step, T threads on a piece, marked as not to be kept:
+// pages go by once (20000 pages of 32 KB, four planes, 1.3 GB: 241 us; 259 us with plain loads
 // and stores, 272 us of those in pieces of 16 KB).
-template <int N>
+template <int T, int N>
 __device__ __forceinline__ void copy_run(uint8_t* to, const uint8_t* from, int64_t bytes) {
   typedef __attribute__((ext_vector_type(N))) uint32_t V;
-  constexpr int kStep = 256 * N * 4;
-  for (int64_t o = threadIdx.x * (N * 4); o < bytes; o += kStep)
+  constexpr int kStep = T * N * 4;
+  for (int64_t o = threadIdx.x % T * (N * 4); o < bytes; o += kStep)
     __builtin_nontemporal_store(__builtin_nontemporal_load(reinterpret_cast<const V*>(from + o)),
                                 reinterpret_cast<V*>(to + o));
 }
 
 // Piece `w` of the work over (buffer, pair, plane, part of the page).
+template <int T>
 __device__ __forceinline__ void copy_piece(const CopyPlan& plan, int64_t w, int32_t pages,
                                            const int32_t* __restrict__ src,
                                            const int32_t* __restrict__ dst) {
@@ -632,15 +670,20 @@ __device__ __forceinline__ void copy_piece(const CopyPlan& plan, int64_t w, int3
   uint8_t* to = base + d * buf.page_bytes;
   const uint8_t* from = base + s * buf.page_bytes;
   if (buf.page_bytes % 16 == 0)
-    copy_run<4>(to, from, bytes);
+    copy_run<T, 4>(to, from, bytes);
   else
-    copy_run<1>(to, from, bytes);
+    copy_run<T, 1>(to, from, bytes);
 }
 
+// A workgroup (T = 256) or a wave of it (T = 64) per piece.
+template <int T>
 __global__ __launch_bounds__(256) void page_copy_kernel(CopyPlan plan, int64_t pieces, int32_t pages,
                                                         const int32_t* __restrict__ src,
                                                         const int32_t* __restrict__ dst) {
-  for (int64_t w = blockIdx.x; w < pieces; w += gridDim.x) copy_piece(plan, w, pages, src, dst);
+  constexpr int kPieces = 256 / T;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / T);
+  for (int64_t w = static_cast<int64_t>(blockIdx.x) * kPieces + wave; w < pieces; w += static_cast<int64_t>(gridDim.x) * kPieces)
+    copy_piece<T>(plan, w, pages, src, dst);
 }
 
 int32_t copy_parts(const PageBuffer& b) {
@@ -723,10 +766,15 @@ hipError_t launch_page_compact(const Cache& c, const int32_t* table, const int32
   }
   const int32_t chunks = (c.pages + kCountPages - 1) / kCountPages;
   auto* counts = static_cast<int32_t*>(ws);
-  page_count_kernel<<<chunks, 256, 0, st>>>(c.pages, refs, counts);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  page_place_kernel<<<chunks, 256, 0, st>>>(c.pages, chunks, refs, counts, map, live, src, dst);
+  hipError_t e;
+  if (chunks <= kOwnChunks) {
+    page_place_kernel<true><<<chunks, 256, 0, st>>>(c.pages, chunks, refs, counts, map, live, src, dst);
+  } else {
+    page_count_kernel<<<chunks, 256, 0, st>>>(c.pages, refs, counts);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    page_place_kernel<false><<<chunks, 256, 0, st>>>(c.pages, chunks, refs, counts, map, live, src, dst);
+  }
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int64_t most = entries > c.pages ? entries : c.pages;
@@ -751,9 +799,14 @@ hipError_t launch_page_copy(const PageBuffers& b, int32_t pages, int32_t n, cons
     plan.parts[i] = copy_parts(b.b[i]);
     pieces += copy_blocks(b.b[i], n);
   }
+  int64_t largest = 0;
+  for (int32_t i = 0; i < b.n; ++i) largest = std::max(largest, b.b[i].page_bytes);
   // A grid's threads stay below 2^32: workgroups beyond 65536 loop.
-  const uint32_t grid = static_cast<uint32_t>(pieces < 65536 ? pieces : 65536);
-  page_copy_kernel<<<grid, 256, 0, st>>>(plan, pieces, pages, src, dst);
+  const bool waves = largest <= kWavePage;
+  const int64_t blocks = waves ? (pieces + 3) / 4 : pieces;
+  const uint32_t grid = static_cast<uint32_t>(std::min<int64_t>(blocks, 65536));
+  const auto f = waves ? page_copy_kernel<kWave> : page_copy_kernel<256>;
+  f<<<grid, 256, 0, st>>>(plan, pieces, pages, src, dst);
   return hipGetLastError();
 }
 
