@@ -108,7 +108,7 @@ __global__ __launch_bounds__(256) void attend_kernel(Args a) {
   const int nheads = min(16 * RT, a.share - chunk * 16 * RT);
   int32_t len;
   const int32_t todo = tokens_of(a, row, len);
-  const int32_t per = tiles_per_split(todo, a.splits) * kTileTokens;
+  const int32_t per = tiles_per_split(a, todo) * kTileTokens;
   const int32_t t0 = split * per, t1 = min(t0 + per, todo);
   if (t0 >= t1 && split > 0) return;  // nothing here; the join does not look at it
 
@@ -354,7 +354,9 @@ __global__ __launch_bounds__(256) void attend_kernel(Args a) {
   }
 }
 
-constexpr int kMinSplitTokens = 128;  // a split gives each wave a tile
+// Tiles that a workgroup works on at a time: a wave's each, or a token group's; a
+// split has at least those.
+int32_t tiles_at_once(const Cache& c) { return c.latent() ? 2 : 4; }
 
 // Query heads of a workgroup: a matrix tile of 16, or two where a kv head has
 // more and the registers hold them.
@@ -373,19 +375,19 @@ constexpr int kCus = 256;
 constexpr int kMaxSplits = 128;
 constexpr int kWholeTokens = 512;
 
-// Splits of a latent row.  A workgroup (one per CU) takes about 3.1 us for a
-// pair of tiles; a join costs about 4 us and, for each split, the way of its
-// sums to memory and back, 4 KB a head at 4.5 TB/s.  32 rows of 128 heads: 256
-// listed tokens 19.4 us whole, 25.1 us in two splits; 2048 88 us whole, 60 us in
-// two, 46 us in four.  With sixteen rounds of workgroups and more, a split could
-// save at most a part of the last one.
+// Splits of a latent row.  A workgroup (one per CU) takes 2.8 us for a pair of
+// tiles; a join costs about 6 us and, for each split, the way of its sums to
+// memory and back, 4 KB a head at 5.1 TB/s.  24 rows of 128 heads: 384 listed
+// tokens 23.0 us whole, 27.8 us in two splits; 4096 169, 101, 74, 64, 73 and 80 us
+// in 1, 2, 3, 4, 8 and 16.  With sixteen rounds of workgroups and more, a split
+// could save at most a part of the last one.
 int32_t latent_splits(int64_t groups, int64_t tokens, int64_t heads, int64_t limit) {
   if (groups >= 16 * kCus) return 1;
   int32_t best = 1;
   double least = 0;
   for (int32_t s = 1; s <= limit; ++s) {
     const int64_t pairs = (tokens + s * 64 - 1) / (s * 64), rounds = (groups * s + kCus - 1) / kCus;
-    const double us = 3.1 * pairs * rounds + (s > 1 ? 4.0 + s * heads * (4096 / 4.5e6) : 0.0);
+    const double us = 2.8 * pairs * rounds + (s > 1 ? 6.0 + s * heads * (4096 / 5.1e6) : 0.0);
     if (s == 1 || us < least) {
       best = s;
       least = us;
@@ -411,7 +413,8 @@ Plan plan(const Cache& c, int32_t heads, int32_t k) {
   p.chunks = (share + per - 1) / per;
   const int64_t groups = static_cast<int64_t>(c.rows) * c.kv_heads * p.chunks;
   const int64_t most = k > 0 ? k : static_cast<int64_t>(c.row_pages) * c.P;
-  const int64_t limit = std::min<int64_t>((most + kMinSplitTokens - 1) / kMinSplitTokens, kMaxSplits);
+  const int64_t least = tiles_at_once(c) * kTileTokens;
+  const int64_t limit = std::min<int64_t>((most + least - 1) / least, kMaxSplits);
   if (c.latent()) {
     p.splits = latent_splits(groups, most, static_cast<int64_t>(c.rows) * heads, limit);
   } else {
@@ -496,6 +499,7 @@ hipError_t launch_attend(const Cache& c, int32_t heads, int32_t k, float scale, 
   a.share = heads / c.kv_heads;
   a.k = k;
   a.splits = p.splits;
+  a.tiles = tiles_at_once(c);
   a.row_pages = c.row_pages;
   a.pages = c.pages;
   a.kv_heads = c.kv_heads;

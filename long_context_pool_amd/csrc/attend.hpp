@@ -51,6 +51,7 @@ struct Args {
   float* part_o;   // [rows, heads, splits, dv] unnormalised sums of a split
   float2* part_ml;  // [rows, heads, splits] maximum (log2) and sum
   int32_t rows, heads, share, k, splits, row_pages, pages, kv_heads;
+  int32_t tiles;  // that a workgroup works on at a time, a power of two
   float scale2;  // scale * log2(e): softmax by powers of two
   Div div;
 };
@@ -79,12 +80,13 @@ __device__ __forceinline__ void unit_chunk(int chunks, int& unit, int& chunk) {
   unit = b / (8 * chunks) * 8 + b % 8;
 }
 
-// How the tiles of a row are divided: every split takes `per` tiles, a
-// multiple of the workgroup's four waves.
+// How the tiles of a row are divided: every split takes the same number, a
+// multiple of those that its workgroup works on at a time (four waves, or a
+// latent kernel's two token groups).
 constexpr int kTileTokens = 32;
-__device__ __forceinline__ int32_t tiles_per_split(int32_t todo, int32_t splits) {
+__device__ __forceinline__ int32_t tiles_per_split(const Args& a, int32_t todo) {
   const int32_t tiles = (todo + kTileTokens - 1) / kTileTokens;
-  return (((tiles + splits - 1) / splits) + 3) & ~3;
+  return (((tiles + a.splits - 1) / a.splits) + a.tiles - 1) & ~(a.tiles - 1);
 }
 
 constexpr int kStage = 2048;  // tokens whose slots (and scales) are in LDS at a time
@@ -142,7 +144,7 @@ __global__ __launch_bounds__(256) void attend_join_kernel(Args a) {
   const int d = threadIdx.x % T, grp = threadIdx.x / T;
   int32_t len;
   const int32_t todo = tokens_of(a, row, len);
-  const int32_t per = tiles_per_split(todo, a.splits) * kTileTokens;
+  const int32_t per = tiles_per_split(a, todo) * kTileTokens;
   const int32_t n = todo > 0 ? (todo + per - 1) / per : 1;  // split 0 always writes
   const int64_t at = static_cast<int64_t>(row) * a.heads + head;
   const float2* ml = a.part_ml + at * a.splits;

@@ -144,7 +144,7 @@ __global__ __launch_bounds__(512) void attend_latent_kernel(Args a) {
   const int head0 = chunk * kLatentHeads + hw * 16;
   int32_t len;
   const int32_t todo = tokens_of(a, row, len);
-  const int32_t per = tiles_per_split(todo, a.splits) * kTileTokens;
+  const int32_t per = tiles_per_split(a, todo) * kTileTokens;
   const int32_t t0 = split * per, t1 = min(t0 + per, todo);
   if (t0 >= t1 && split > 0) return;
 

@@ -564,7 +564,7 @@ __device__ __forceinline__ int32_t moved_page(int32_t id, int32_t pages, const i
 }
 
 // Small pools and tables: everything in one workgroup and one launch (1000 pages
-// 4.7 us; the three launches below take about that each, by latency).
+// 4.7 us; the launches of larger pools take about that each, by latency).
 __global__ __launch_bounds__(kListThreads) void page_compact_small_kernel(
     int32_t pages, int32_t entries, const int32_t* table, const int32_t* refs, int32_t* table_out,
     int32_t* refs_out, int32_t* map, int32_t* __restrict__ live_out, int32_t* src, int32_t* dst) {
@@ -756,8 +756,8 @@ hipError_t launch_page_compact(const Cache& c, const int32_t* table, const int32
                                int32_t* src, int32_t* dst, void* ws, hipStream_t st) {
   const int64_t entries = static_cast<int64_t>(c.rows) * c.row_pages;
   // Small pools and tables in one workgroup: with its copies, a pool of 1000
-  // pages takes 11.1 us so, 16.1 us in three launches; one of 4000 pages with
-  // 3000 table entries would take 24.1 us, against 22.8 us.
+  // pages takes 12.2 us so, 15.1 us in two launches; one of 4000 pages with
+  // 3000 table entries would take 24.2 us, against 22.5 us.
   static_assert(kSmallPages <= kScanPages, "four pages a thread");
   if (c.pages <= kSmallPages && entries <= kSmallPages) {
     page_compact_small_kernel<<<1, kListThreads, 0, st>>>(c.pages, static_cast<int32_t>(entries), table,
