@@ -373,7 +373,6 @@ int resident(const Cache& c, int32_t share) {
 
 constexpr int kCus = 256;
 constexpr int kMaxSplits = 128;
-constexpr int kWholeTokens = 512;
 
 // Splits of a latent row.  A workgroup (one per CU) takes 2.8 us for a pair of
 // tiles; a join costs about 6 us and, for each split, the way of its sums to
@@ -390,6 +389,38 @@ int32_t latent_splits(int64_t groups, int64_t tokens, int64_t heads, int64_t lim
     const double us = 2.8 * pairs * rounds + (s > 1 ? 6.0 + s * heads * (4096 / 5.1e6) : 0.0);
     if (s == 1 || us < least) {
       best = s;
+      least = us;
+    }
+  }
+  return best;
+}
+
+// Splits of a dense row: at most those that fill the card in one round, since more
+// only add to the join and to the last round's tail (8 rows of up to 131072 fp8
+// tokens: 768 workgroups 322 us, 1024 340 us, 512 342 us), and fewer where their
+// join costs more than the steps that it saves.  A wave's step, one tile of K and
+// of V, takes 0.55 us and for each workgroup on its CU the four waves' share of
+// memory and instructions; a join 5.8 us and the sums' way through memory.  Fitted
+// to 730 cases with caches from memory, of which the choice is 4% from the best
+// one, as many splits as fill the card 9%: 32 rows of 600 tokens, 64 heads on 8,
+// 16.0 us whole, 21.4 us in three; 16 rows of 1000 with 256 heads 21.4 and 24.1 us; one
+// row of 2000, 32 heads on 8, 9.4 us in sixteen, 25 us whole.
+int32_t dense_splits(const Cache& c, int32_t heads, int32_t share, int64_t groups, int64_t tokens,
+                     int64_t limit) {
+  const int32_t held = resident(c, share);
+  const int64_t most = std::min<int64_t>(kCus * held / groups, limit);
+  const int32_t all = static_cast<int32_t>((tokens + kTileTokens - 1) / kTileTokens);
+  const int32_t tile_bytes = kTileTokens * (c.dk + c.dv) * (c.dtype == kFP8 ? 1 : 2);
+  const double each = tile_bytes * 8.5e-5 + group_heads(c, share) * c.dk * 1e-4;
+  const double sums = 3.3e-6 * c.rows * heads * c.dk;
+  int32_t best = 1;
+  double least = 0;
+  for (int32_t s = static_cast<int32_t>(most); s >= 1; s = s > 1 ? std::max(1, s * 3 / 4) : 0) {
+    const int32_t per = ((all + s - 1) / s + 3) & ~3, parts = (all + per - 1) / per;
+    const int32_t on_cu = static_cast<int32_t>((groups * parts + kCus - 1) / kCus);
+    const double us = per / 4 * (0.55 + on_cu * each) + (parts > 1 ? 5.8 + parts * sums : 0.0);
+    if (least == 0 || us < least) {
+      best = parts;
       least = us;
     }
   }
@@ -418,14 +449,7 @@ Plan plan(const Cache& c, int32_t heads, int32_t k) {
   if (c.latent()) {
     p.splits = latent_splits(groups, most, static_cast<int64_t>(c.rows) * heads, limit);
   } else {
-    // One round of workgroups over the card: more of them only add to the join
-    // and to the last round's tail (8 rows of up to 131072 fp8 tokens: 768
-    // workgroups 322 us, 1024 340 us, 512 342 us; 32 rows x 2048 listed tokens:
-    // 768 58.4 us, 1536 63.2 us).  Up to 512 tokens the join costs more than the
-    // four tiles that a wave has then (one row of 200 tokens: 6.6 us whole, 9.1
-    // us in two splits; 500: 8.9 us either way; 1000: 13.6 us and 9.2 us).
-    const int64_t s = most <= kWholeTokens ? 1 : kCus * resident(c, share) / groups;
-    p.splits = static_cast<int32_t>(std::max<int64_t>(1, std::min(s, limit)));
+    p.splits = dense_splits(c, heads, share, groups, most, limit);
   }
   const int64_t row_bytes = static_cast<int64_t>(c.dk + c.dv) * (c.dtype == kFP8 ? 1 : 2);
   p.once = p.chunks == 1 && c.rows * most * c.kv_heads * row_bytes >= kOnceBytes;
