@@ -64,10 +64,10 @@ __device__ __forceinline__ int value_dim(int c, int j) {
 // one reader, and the next tile's loads are under way while one is worked on.
 //
 // Bound by memory: 8 rows of up to 131072 fp8 tokens of 8 heads of 128 (1.73 GB)
-// 296 us, 5.8 TB/s; 32 rows x 2048 listed bf16 tokens (261 MB, pieces of 256
-// bytes) 49 us, 5.3 TB/s, and the join 4.7 us.  One row of 2000 tokens (8 MB)
+// 292 us, 5.9 TB/s; 32 rows x 2048 listed bf16 tokens (261 MB, pieces of 256
+// bytes) 51 us, 5.1 TB/s.  One row of 2000 tokens (8 MB)
 // 6.2 us: a launch, three dependent loads to a slot, one tile's loads and the
-// joins of waves.
+// join of the waves' sums.
 //
 // ONCE: the cache is read once (one chunk of query heads) and is large, so its
 // loads are marked as not to be kept (the 8 rows above: 322 us with plain loads;
@@ -359,7 +359,9 @@ __global__ __launch_bounds__(256) void attend_kernel(Args a) {
 int32_t tiles_at_once(const Cache& c) { return c.latent() ? 2 : 4; }
 
 // Query heads of a workgroup: a matrix tile of 16, or two where a kv head has
-// more and the registers hold them.
+// more and the registers hold them (8 rows of 8000 bf16 tokens of 8 heads of 128,
+// 256 query heads: 49.7 us with 32, 58.2 with 16; heads of 64 31.3 and 30.3, fp8
+// 24.8 and 25.8).
 int group_heads(const Cache& c, int32_t share) {
   if (c.latent()) return kLatentHeads;
   return share > 16 && c.dk <= 128 ? 32 : 16;
@@ -403,8 +405,8 @@ int32_t latent_splits(int64_t groups, int64_t tokens, int64_t heads, int64_t lim
 // memory and instructions; a join 5.8 us and the sums' way through memory.  Fitted
 // to 730 cases with caches from memory, of which the choice is 4% from the best
 // one, as many splits as fill the card 9%: 32 rows of 600 tokens, 64 heads on 8,
-// 16.0 us whole, 21.4 us in three; 16 rows of 1000 with 256 heads 21.4 and 24.1 us; one
-// row of 2000, 32 heads on 8, 9.4 us in sixteen, 25 us whole.
+// 16.0 us whole, 21.4 us in three; 16 rows of 1000 with 256 heads 21.4 and 24.1
+// us; one row of 2000, 64 heads on 8, 9.7 us in sixteen, 24.8 us whole.
 int32_t dense_splits(const Cache& c, int32_t heads, int32_t share, int64_t groups, int64_t tokens,
                      int64_t limit) {
   const int32_t held = resident(c, share);

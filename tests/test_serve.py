@@ -735,6 +735,7 @@ def _check_norm(misa, rows, n, groups, xt, ot, eps, x, residual, weight, in_plac
     (2, 32768, 256), (9, 512, 4), (3, 2048, 8), (4, 12, 12), (130, 64, 1), (2, 16384, 1), (2, 5120, 40), (1, 20000, 1),
     (5, 7, 1), (300, 8, 1), (33, 9, 1), (70, 127, 1), (9, 513, 1), (3, 4095, 1), (2, 8191, 1), (2, 16383, 1), (2, 32767, 1),
     (7, 1002, 1), (3, 24, 3), (2, 1120, 2), (2, 8000, 8), (40, 96, 12), (2, 30000, 2),
+    (19, 200, 1), (9, 256, 2), (6, 251, 1), (5, 1024, 1), (5, 1017, 1), (3, 2048, 16), (5, 1999, 1), (3, 6000, 1), (2, 6143, 1), (3, 6144, 48),
 ])
 def test_norm(misa, rows, n, groups, xt, ot):
     gen = torch.Generator().manual_seed(n)
