@@ -638,13 +638,25 @@ struct CopyPlan {
 };
 
 // N dwords per thread and step, T threads on a piece, marked as not to be kept:
-// pages go by once (20000 pages of 32 KB, four planes, 1.3 GB: 241 us; 259 us with plain loads
-// and stores, 272 us of those in pieces of 16 KB).
+// pages go by once.  Four steps' loads are under way before the first store, which
+// might otherwise be to what the next load reads (20000 pages of 32 KB, four
+// planes, 1.3 GB: 230 us with the bookkeeping; 243 us with one load at a time, 261
+// us with plain loads and stores, 274 us of those in pieces of 16 KB).
 template <int T, int N>
 __device__ __forceinline__ void copy_run(uint8_t* to, const uint8_t* from, int64_t bytes) {
   typedef __attribute__((ext_vector_type(N))) uint32_t V;
-  constexpr int kStep = T * N * 4;
-  for (int64_t o = threadIdx.x % T * (N * 4); o < bytes; o += kStep)
+  constexpr int kStep = T * N * 4, kBatch = 4;
+  int64_t o = threadIdx.x % T * (N * 4);
+  for (; o + (kBatch - 1) * kStep < bytes; o += kBatch * kStep) {
+    V x[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      x[i] = __builtin_nontemporal_load(reinterpret_cast<const V*>(from + o + i * kStep));
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      __builtin_nontemporal_store(x[i], reinterpret_cast<V*>(to + o + i * kStep));
+  }
+  for (; o < bytes; o += kStep)
     __builtin_nontemporal_store(__builtin_nontemporal_load(reinterpret_cast<const V*>(from + o)),
                                 reinterpret_cast<V*>(to + o));
 }

@@ -590,7 +590,7 @@ def test_compact_pools(misa, pages, live):
 
 
 @gpu
-@pytest.mark.parametrize("page_bytes", [4, 12, 64, 1000, 16384, 16400, 70000])
+@pytest.mark.parametrize("page_bytes", [4, 12, 64, 1000, 2004, 4096, 5004, 16384, 16400, 40012, 70000])
 def test_page_copy(misa, page_bytes):
     """Pages land in every plane of every buffer; bad pairs are skipped, the rest stays."""
     gen = torch.Generator().manual_seed(page_bytes)
