@@ -24,9 +24,30 @@ struct __attribute__((packed, aligned(2))) Bf16x8 {
 struct __attribute__((packed, aligned(4))) F32x8 {
   float w[8];
 };
-struct __attribute__((packed, aligned(1))) Codes8 {
-  uint32_t w[2];
-};
+
+// bf16 and 8-bit outputs from this size on leave the L2s (32 MB) before anyone
+// reads them; they are marked as not to be kept there, which leaves more of the
+// inputs: 8192 x 64 x 128 to fp8 35.5 us, 40.3 without; 12000 rows of 4096 in bf16
+// 31.4 and 39.4; 2000 rows of 8192 to fp8 11.5 and 11.3.  fp32 sums so marked
+// would cost (12000 rows of 4096 144 us against 123).
+constexpr int64_t kOnceStores = int64_t{16} << 20;
+
+// N dwords to an address that is a multiple of A; `once`: marked as not to be kept.
+template <int N, int A>
+__device__ __forceinline__ void store_words(void* to, const uint32_t (&w)[N], bool once) {
+  typedef __attribute__((ext_vector_type(N))) uint32_t V;
+  typedef V __attribute__((aligned(A))) U;
+  V x;
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] = w[i];
+  if (once) {
+    asm volatile("");  // on both sides, or the branches are merged into a plain store
+    __builtin_nontemporal_store(x, static_cast<U*>(to));
+    asm volatile("");
+  } else {
+    *static_cast<U*>(to) = x;
+  }
+}
 
 template <int XT>
 __device__ __forceinline__ void load8(const void* base, int64_t e, float (&x)[8]) {
@@ -44,8 +65,8 @@ __device__ __forceinline__ void load8(const void* base, int64_t e, float (&x)[8]
   }
 }
 
-__device__ __forceinline__ void store8(int dt, void* base, int64_t e, const float (&x)[8]) {
-  if (dt == kF32) {
+__device__ __forceinline__ void store8(int dt, void* base, int64_t e, const float (&x)[8], bool once) {
+  if (dt == kF32) {  // always kept: each of its two stores leaves out every other 16 bytes of a line
     F32x8 v;
 #pragma unroll
     for (int i = 0; i < 8; ++i) v.w[i] = x[i];
@@ -54,7 +75,8 @@ __device__ __forceinline__ void store8(int dt, void* base, int64_t e, const floa
     bf16x8 y;
 #pragma unroll
     for (int i = 0; i < 8; ++i) y[i] = static_cast<__bf16>(x[i]);
-    *reinterpret_cast<Bf16x8*>(static_cast<uint16_t*>(base) + e) = __builtin_bit_cast(Bf16x8, y);
+    const uint4 v = __builtin_bit_cast(uint4, y);
+    store_words<4, 2>(static_cast<uint16_t*>(base) + e, {v.x, v.y, v.z, v.w}, once);
   }
 }
 
@@ -92,13 +114,13 @@ constexpr float kFarRoot = 0x1p16f;
 // may be empty, so that their sums are register moves.  ODD: a row's length is
 // no multiple of eight; its last vector ends with the row, and the elements that
 // the one before already has are left out of sums and stores.  Bound by memory
-// traffic: 8192 rows of 64 parts of 128, bf16 -> fp8 (201 MB), 40.6 us, 5.0 TB/s;
+// traffic: 8192 rows of 64 parts of 128, bf16 -> fp8 (201 MB), 35.5 us, 5.7 TB/s;
 // 32 rows of 4096 with residual, 3.8 us, a launch and two loads' latency.
 template <int XT, int T, int V, bool GROUPED, bool ODD>
 __global__ __launch_bounds__(256) void norm_kernel(int32_t rows, int32_t n, int32_t size,
                                                    int32_t part_shift, int32_t out_dtype,
-                                                   float inv_size, float eps, const void* x,
-                                                   const void* residual,
+                                                   float inv_size, float eps, bool once,
+                                                   const void* x, const void* residual,
                                                    const float* __restrict__ weight, void* sum_out,
                                                    void* __restrict__ out,
                                                    float* __restrict__ out_scale) {
@@ -128,7 +150,7 @@ __global__ __launch_bounds__(256) void norm_kernel(int32_t rows, int32_t n, int3
   };
   auto store = [&](int dt, void* to, int e, int skip, const float(&z)[8]) {
     if (!ODD || skip == 0) {
-      store8(dt, to, base + e, z);
+      store8(dt, to, base + e, z, once);
     } else {
 #pragma unroll
       for (int i = 1; i < 8; ++i)
@@ -237,14 +259,14 @@ __global__ __launch_bounds__(256) void norm_kernel(int32_t rows, int32_t n, int3
   for (int v = 0; v < V; ++v) {
     if (!place(v, e, at, skip)) continue;
     const float f = r[v] * mult;
-    const Codes8 c = {{e4m3_pack4(y[v][0], y[v][1], y[v][2], y[v][3], f),
-                       e4m3_pack4(y[v][4], y[v][5], y[v][6], y[v][7], f)}};
+    const uint32_t c[2] = {e4m3_pack4(y[v][0], y[v][1], y[v][2], y[v][3], f),
+                           e4m3_pack4(y[v][4], y[v][5], y[v][6], y[v][7], f)};
     if (!ODD || skip == 0) {
-      *reinterpret_cast<Codes8*>(codes + e) = c;
+      store_words<2, 1>(codes + e, c, once);
     } else {
 #pragma unroll
       for (int i = 1; i < 8; ++i)
-        if (i >= skip) codes[e + i] = static_cast<uint8_t>(c.w[i / 4] >> (i % 4 * 8));
+        if (i >= skip) codes[e + i] = static_cast<uint8_t>(c[i / 4] >> (i % 4 * 8));
     }
   }
   if (t == 0) out_scale[row] = scale;
@@ -262,9 +284,10 @@ struct NormArgs {
 template <int XT, int T, int V, bool GROUPED, bool ODD>
 void launch_norm(const NormArgs& a, hipStream_t st) {
   const int32_t per = 256 / T;
+  const bool once = static_cast<int64_t>(a.rows) * a.n * (a.out_dtype == kF32 ? 4 : a.out_dtype == kBF16 ? 2 : 1) >= kOnceStores;
   norm_kernel<XT, T, V, GROUPED, ODD><<<(a.rows - 1) / per + 1, 256, 0, st>>>(
       a.rows, a.n, a.n / a.groups, a.part_shift, a.out_dtype, 1.f / static_cast<float>(a.n / a.groups),
-      a.eps, a.x, a.residual, a.weight, a.sum_out, a.out, a.out_scale);
+      a.eps, once, a.x, a.residual, a.weight, a.sum_out, a.out, a.out_scale);
 }
 
 // Threads per row and vectors per thread, by the vectors' places in a row: the
