@@ -576,7 +576,7 @@ def test_bookkeeping_long_lists(misa):
 
 @gpu
 @pytest.mark.parametrize("live", ["none", "all", "low", "high", "odd"])
-@pytest.mark.parametrize("pages", [1, 2, 255, 257, 5000, 20481, 65536, 70001])
+@pytest.mark.parametrize("pages", [1, 2, 255, 257, 5000, 8192, 8193, 20481, 65536, 70001])
 def test_compact_pools(misa, pages, live):
     book = _book(misa, 3, 7, pages, 4)
     at = np.arange(pages)
