@@ -57,9 +57,11 @@ __device__ __forceinline__ int value_dim(int c, int j) {
 //         holds the tokens 4g .. 4g+3 of both 16-token halves, and V's rows
 //         are loaded in that order.  Eight rows of V make eight columns of V^T
 //         by byte permutes in registers.
-// A weight goes into the product as two bf16 parts (its rounding and the rest,
-// 2^-17 together), or the result would be off by a second bf16 rounding; the
-// cached values are exact in bf16.  Maximum, sums and O stay in fp32 registers.
+// A weight goes into the product as two bf16 parts (2^-16 together), or the result
+// would be off by a second bf16 rounding; the cached values are exact in bf16.
+// Neither part of a positive weight is zero or negative, so that an infinite value
+// stays an infinity of its sign: the first is the weight's predecessor cut off,
+// the second the rest.  Maximum, sums and O stay in fp32 registers.
 // No tile goes through LDS: a cached row has few query heads, each of its bytes
 // one reader, and the next tile's loads are under way while one is worked on.
 //
@@ -244,9 +246,9 @@ __global__ __launch_bounds__(256) void attend_kernel(Args a) {
           const float p = __builtin_amdgcn_exp2f(x[i] - mb);
           l[r] += p;
           const float w = kFp8 ? p * vs[i] : p;
-          const __bf16 hi = static_cast<__bf16>(w);
-          ph[r][i] = hi;
-          pl[r][i] = static_cast<__bf16>(w - static_cast<float>(hi));
+          const uint32_t hi = __builtin_elementwise_sub_sat(__float_as_uint(w), 1u) & 0xFFFF0000u;
+          ph[r][i] = __builtin_bit_cast(__bf16, static_cast<uint16_t>(hi >> 16));
+          pl[r][i] = static_cast<__bf16>(w - __uint_as_float(hi));
         }
       }
       if (__any(hidden)) {  // hidden slots may hold anything: 0 * NaN must not reach O

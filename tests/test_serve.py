@@ -341,6 +341,28 @@ def test_attend_extreme_scores(misa, fp8):
 
 
 @gpu
+@pytest.mark.parametrize("dk", [64, 128, 256])
+@pytest.mark.parametrize("share,k", [(4, 0), (4, 60), (20, 0), (40, 60)])
+def test_attend_infinite_values(misa, dk, share, k):
+    """Infinite values of visible tokens give infinities of their sign in their dimension alone, both signs NaN."""
+    case = _attend_case(misa, dk, dk, 2, 2 * share, 16, [3000, 75], 1, k=k, seed=dk + share)
+    c, heads, k, scale, q, pools, table, lengths, idx = case
+    s, t = (int(x) for x in idx[0, :2]) if k else (5, 2100)
+    for token, dim, value in ((s, 0, math.inf), (t, 1, -math.inf), (s, 2, math.inf), (t, 2, math.inf), (s, 3, math.inf),
+                              (t, 3, -math.inf), (t, dk - 1, math.inf)):
+        pools[1][table[0, token // 16], 1, token % 16, dim] = value
+    _log(f"[gpu] attend infinite values dk {dk} share {share} k {k}")
+    got, lse = _run_attend(misa, *case)
+    want, want_lse, tol, lse_tol = ref.attend(c, heads, k, scale, q, pools[0], pools[2], pools[1], pools[3], table, lengths, idx)
+    far = ~torch.isfinite(want)
+    assert far.sum() == 5 * share
+    assert torch.equal(torch.nan_to_num(got.double()[far], nan=7.0, posinf=8.0, neginf=9.0),
+                       torch.nan_to_num(want[far], nan=7.0, posinf=8.0, neginf=9.0))
+    assert torch.all((got.double() - want).abs()[~far] <= tol[~far])
+    assert torch.all((lse.double() - want_lse).abs() <= lse_tol)
+
+
+@gpu
 def test_attend_splits_long_rows(misa):
     """One long row beside short ones: the split row joined, without lse too, twice the same bits."""
     for dk, dv, dtype, k in ((128, 128, 2, 0), (128, 128, 1, 3000), (576, 512, 1, 0)):
