@@ -107,6 +107,19 @@ __device__ __forceinline__ void part_sums(float (&ss)[V], int lanes) {
 constexpr int kEarlyWeights = 4;
 // 1 / rms beyond which it is multiplied in first.
 constexpr float kFarRoot = 0x1p16f;
+// A sum of squares may leave fp32's range where their mean (of at most 2^15) does
+// not: an infinite one is formed again from elements divided by this.
+constexpr float kFarSquares = 0x1p16f;
+
+__device__ __forceinline__ float far_squares(const float (&y)[8]) {
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float x = y[i] * (1.f / kFarSquares);
+    s += x * x;
+  }
+  return s;
+}
 
 // T threads per row, V vectors of eight elements in registers per thread: one
 // read of x and residual, one write.  The parts of a row (GROUPED) have 2^k <=
@@ -124,7 +137,7 @@ __global__ __launch_bounds__(256) void norm_kernel(int32_t rows, int32_t n, int3
                                                    const float* __restrict__ weight, void* sum_out,
                                                    void* __restrict__ out,
                                                    float* __restrict__ out_scale) {
-  __shared__ float tmp[2][4];
+  __shared__ float tmp[3][4];
   const int t = threadIdx.x % T;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * (256 / T) + threadIdx.x / T;
   if (row >= rows) return;  // T < 256: whole rows of lanes leave; T = 256: never
@@ -202,13 +215,37 @@ __global__ __launch_bounds__(256) void norm_kernel(int32_t rows, int32_t n, int3
   float r[V];
   if constexpr (GROUPED) {
     part_sums<1>(ss, 1 << part_shift);
+    bool over = false;
 #pragma unroll
-    for (int v = 0; v < V; ++v) r[v] = __builtin_amdgcn_rsqf(ss[v] * inv_size + eps);
+    for (int v = 0; v < V; ++v) {
+      r[v] = ss[v] * inv_size;
+      over |= ss[v] == INFINITY;
+    }
+    if (__any(over)) {  // wave-uniform, like the parts
+      float far[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) far[v] = far_squares(y[v]);
+      part_sums<1>(far, 1 << part_shift);
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        if (ss[v] == INFINITY) r[v] = far[v] * inv_size * (kFarSquares * kFarSquares);
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) r[v] = __builtin_amdgcn_rsqf(r[v] + eps);
   } else {
     float s = 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) s += ss[v];
-    const float f = __builtin_amdgcn_rsqf(row_reduce<T, false>(s, tmp[0]) * inv_size + eps);
+    s = row_reduce<T, false>(s, tmp[0]);
+    float mean = s * inv_size;
+    if (__any(s == INFINITY)) {  // uniform over a workgroup with one row
+      float far = 0.f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) far += far_squares(y[v]);
+      far = row_reduce<T, false>(far, tmp[2]);
+      if (s == INFINITY) mean = far * inv_size * (kFarSquares * kFarSquares);
+    }
+    const float f = __builtin_amdgcn_rsqf(mean + eps);
 #pragma unroll
     for (int v = 0; v < V; ++v) r[v] = f;
   }
@@ -345,7 +382,18 @@ __global__ __launch_bounds__(256) void norm_any_kernel(int32_t n, int32_t size, 
     }
 #pragma unroll
     for (int o = 1; o < kWave; o <<= 1) ss += __shfl_xor(ss, o, kWave);
-    const float r = 1.f / sqrtf(ss / static_cast<float>(size) + eps);
+    float mean = ss / static_cast<float>(size);
+    if (ss == INFINITY) {  // every lane alike
+      ss = 0.f;
+      for (int32_t e = lane; e < size; e += kWave) {
+        const float y = z[p0 + e] * (1.f / kFarSquares);
+        ss += y * y;
+      }
+#pragma unroll
+      for (int o = 1; o < kWave; o <<= 1) ss += __shfl_xor(ss, o, kWave);
+      mean = ss / static_cast<float>(size) * (kFarSquares * kFarSquares);
+    }
+    const float r = 1.f / sqrtf(mean + eps);
     for (int32_t e = lane; e < size; e += kWave) {
       const float v = z[p0 + e] * r * weight[e];
       z[p0 + e] = v;
