@@ -252,7 +252,8 @@ misa_status misa_hisa_score_topk(const misa_shape* shape, int32_t h, int32_t m, 
  *  - 8-bit codes are OCP e4m3fn, value = code * scale, rounded to nearest even
  *    from x * (448 / amax); scale = amax / 448, with amax the largest magnitude
  *    of the values that share the scale (NaN left out), and scale = 1 when
- *    amax < 2^-100 (zeros).  A NaN becomes a NaN code; an infinity makes its
+ *    amax < 2^-100 (zeros).  misa_page_write rounds that product as if it were
+ *    exact, misa_rms_norm (whose x is an fp32 result) its fp32 value.  A NaN becomes a NaN code; an infinity makes its
  *    scale infinite and itself a NaN code.
  */
 

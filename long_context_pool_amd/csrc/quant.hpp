@@ -15,6 +15,14 @@ __device__ __forceinline__ void e4m3_scale(float amax, float& scale, float& mult
   mult = some ? kE4M3Max / amax : 1.f;
 }
 
+// What 448 / amax has beyond its fp32 rounding `mult`.  x * mult alone is off by up
+// to a step of fp32, and bf16 values whose exact quotient lies midway between two
+// codes (about one of 1000 does) would not always go to the even one.
+__device__ __forceinline__ float e4m3_rest(float amax, float mult) {
+  const bool some = amax >= 0x1p-100f && amax < INFINITY;
+  return some ? __builtin_fmaf(-mult, amax, kE4M3Max) * mult * (1.f / kE4M3Max) : 0.f;
+}
+
 // Four codes of x * mult in one dword (hardware conversion, round to nearest
 // even).  |x| is at most the amax that gave mult, so that a product exceeds 448 by
 // a few roundings at most, and everything below 464 becomes 448: no clamp.
