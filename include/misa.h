@@ -253,8 +253,9 @@ misa_status misa_hisa_score_topk(const misa_shape* shape, int32_t h, int32_t m, 
  *    from x * (448 / amax); scale = amax / 448, with amax the largest magnitude
  *    of the values that share the scale (NaN left out), and scale = 1 when
  *    amax < 2^-100 (zeros).  misa_page_write rounds that product as if it were
- *    exact, misa_rms_norm (whose x is an fp32 result) its fp32 value.  A NaN becomes a NaN code; an infinity makes its
- *    scale infinite and itself a NaN code.
+ *    exact, misa_rms_norm (whose x is an fp32 result) its fp32 value.  A NaN
+ *    becomes a NaN code; an infinity makes its scale infinite and itself a NaN
+ *    code.
  */
 
 /* A paged cache.  Sequence r of `rows` owns row r of the page table: token s
@@ -292,8 +293,12 @@ typedef struct {
  *   q    [rows, heads, dk]  bf16      out [rows, heads, dv]  bf16, written
  *   idx  [rows, k]  int32 (k > 0; k = 0: NULL)
  *   lse  [rows, heads]  fp32, written if non-NULL
- * Scores, softmax and sums are fp32.  Limits: heads a multiple of kv_heads,
- * heads <= 1024, rows <= 65535, 0 <= k <= 2^20.  ws must hold
+ * Scores, softmax and sums are fp32: q . k and a score times log2(e) must be in
+ * its range, and cached values below 2^90 in magnitude, or infinite (weights of
+ * up to 2^8 are summed before the division by their sum).  A weight goes into
+ * its products as two bf16 parts, which hold it to 2^-16.  Limits: heads a
+ * multiple of kv_heads, heads <= 1024, rows <= 65535, 0 <= k <= 2^20, |scale| <=
+ * 2^127.  ws must hold
  * misa_attend_workspace_bytes(cache, heads, k) bytes (0: invalid arguments or
  * no workspace needed); it carries nothing from one call to the next. */
 size_t misa_attend_workspace_bytes(const misa_cache* cache, int32_t heads, int32_t k);

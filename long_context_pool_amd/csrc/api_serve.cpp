@@ -90,6 +90,7 @@ misa_status misa_attend(const misa_cache* cache, int32_t heads, int32_t k, float
   Cache c;
   MISA_TRY(check_attend(cache, heads, k, c));
   if (!std::isfinite(scale)) return MISA_ERR_INVALID_ARG;
+  if (!std::isfinite(scale * misa::kLog2e)) return MISA_ERR_UNSUPPORTED;
   MISA_TRY(check_pools(c, k_pages, k_scale, v_pages, v_scale));
   MISA_TRY(check_out(q, true));
   MISA_TRY(check_out(table, true));

@@ -12,7 +12,6 @@ typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
 typedef __attribute__((ext_vector_type(4))) short s16x4;
 typedef __attribute__((ext_vector_type(2))) int i32x2;
 
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 // The sums are rescaled to a new maximum only when a score exceeds the old one
 // by this much (log2): until then weights go up to 2^8, which loses nothing in

@@ -125,6 +125,7 @@ struct Cache {
   bool latent() const { return dk == 576 && dv == 512; }
 };
 
+constexpr float kLog2e = 1.4426950408889634f;  // scores are scaled to powers of two by scale * log2(e)
 // Attention of one new token per row.  k > 0: over the listed tokens only.
 size_t attend_ws_bytes(const Cache& c, int32_t heads, int32_t k);
 hipError_t launch_attend(const Cache& c, int32_t heads, int32_t k, float scale, const void* q,

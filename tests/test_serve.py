@@ -64,6 +64,13 @@ def test_attend_refuses_arguments(misa, change, expect):
     assert _attend(misa, misa.cache(4, 8, 40, 16, 2, 128, 128, misa.MISA_BF16), **change) == expect
 
 
+def test_attend_refuses_far_scales(misa):
+    """Scales whose product with log2(e) leaves fp32's range."""
+    c = misa.cache(4, 8, 40, 16, 2, 128, 128, misa.MISA_BF16)
+    assert _attend(misa, c, scale=3e38) == -2 and _attend(misa, c, scale=-3e38) == -2
+    assert _attend(misa, c, scale=2.0 ** 127, q=None) == -1  # the next check
+
+
 def test_attend_refuses_missing_scales_latent_values_and_short_workspaces(misa):
     fp8 = misa.cache(4, 8, 40, 16, 2, 128, 128, misa.MISA_FP8_E4M3)
     assert _attend(misa, fp8, ks=None, vs=FAKE) == -1
