@@ -7,8 +7,10 @@ non-OK status.  All computation happens in the library's HIP kernels; there is
 no CPU fallback -- importing this package fails if the library is not built.
 
 The serving calls at the end (attention over a paged cache, the cache's pages,
-the norm) take contiguous device tensors only and run on their device, on its
-current stream unless one is given.
+the norm) take contiguous tensors only, all on one device, and run there, on its
+current stream unless one is given.  The integers that they read (tables, lengths,
+lists) must be int32 tensors; other types and all sizes are the caller's to keep,
+as in C.
 
 MISA (Mixture of Indexer Sparse Attention) is the drop-in replacement for the
 DeepSeek Sparse Attention token indexer described on the MISA summary page
@@ -243,27 +245,65 @@ def misa_hisa_score_topk(shp, h, m, k, q, q_scale, w, pooled, kk, k_scale, heads
 # ------------------------------------------------------------------ serving
 
 
-def _dev(x):
-    """Device address of a contiguous device tensor (or an int address, or None -> NULL)."""
+_int32 = None
+
+
+def _device(x):
+    """The device of a call's main tensor; None for an address."""
+    if x is None or x.__class__ is int:
+        return None
+    device = x.get_device()
+    if device < 0:
+        raise ValueError("tensors must be contiguous and on the device")
+    return device
+
+
+def _dev(x, device):
+    """Device address of a contiguous tensor on `device`, any one if None (or an int address, or
+    None -> NULL)."""
     if x is None or x.__class__ is int:
         return x
-    if not (x.is_cuda and x.is_contiguous()):
-        raise ValueError("tensors must be contiguous and on the device")
+    on = x.get_device()
+    if (on != device and (device is not None or on < 0)) or not x.is_contiguous():
+        raise ValueError("tensors must be contiguous and on the device, all on one")
     return x.data_ptr()
 
 
-def _call(fn: str, tensor, args, stream):
-    """Calls the entry point with the device of `tensor` as the current one, on `stream` (by default
-    that device's current one)."""
-    f = getattr(_lib, fn)
-    device = None
-    if tensor is not None and tensor.__class__ is not int:
-        device = tensor.get_device()
-        if device != _current_device():
-            import torch
-            with torch.cuda.device(device):
-                return _check(f(*args, _stream(stream)), fn)
-    _check(f(*args, _stream(stream, device)), fn)
+def _ints(x, device):
+    """_dev for the integers a call reads: torch's own are 64-bit, and would be read as twice as
+    many of 32."""
+    if x is None or x.__class__ is int:
+        return x
+    if x.dtype is not _int32:
+        _int32_only(x)
+    on = x.get_device()
+    if (on != device and (device is not None or on < 0)) or not x.is_contiguous():
+        return _dev(x, device)
+    return x.data_ptr()
+
+
+def _int32_only(x):
+    """torch.int32, looked up once; refuses x of another type."""
+    global _int32
+    import torch
+    _int32 = torch.int32
+    if x.dtype is not _int32:
+        raise ValueError(f"integers must be torch.int32, not {x.dtype}")
+
+
+def _call(f, device, args, stream):
+    """Calls the entry point with `device` as the current one, on `stream` (by default that device's
+    current one)."""
+    if device is not None and device != (_torch_device or _current_device)():
+        import torch
+        with torch.cuda.device(device):
+            status = f(*args, _stream(stream))
+    elif stream is None:
+        status = f(*args, _stream(None) if device is None else _torch_stream(device))
+    else:
+        status = f(*args, _stream(stream))
+    if status:
+        raise MisaError(status, f.__name__)
 
 
 def cache(rows, row_pages, pages, page_tokens, kv_heads, dk, dv, kv_dtype) -> misa_cache:
@@ -273,7 +313,9 @@ def cache(rows, row_pages, pages, page_tokens, kv_heads, dk, dv, kv_dtype) -> mi
 def page_buffers(buffers):
     """The `buffers` argument of misa_page_copy, from (data, planes, page_bytes) triples.  It holds
     addresses: the tensors must outlive it."""
-    return (misa_page_buffer * len(buffers))(*(misa_page_buffer(_dev(d), b, p) for d, p, b in buffers))
+    on = _device(buffers[0][0]) if buffers else None
+    return (misa_page_buffer * len(buffers))(
+        *(misa_page_buffer(_dev(d, on), b, p) for d, p, b in buffers))
 
 
 def misa_attend_workspace_bytes(cache: misa_cache, heads: int, k: int) -> int:
@@ -282,34 +324,45 @@ def misa_attend_workspace_bytes(cache: misa_cache, heads: int, k: int) -> int:
 
 def misa_attend(cache, heads, k, scale, q, k_pages, k_scale, v_pages, v_scale, table, lengths, idx,
                 out, lse, ws, stream=None):
-    _call("misa_attend", q, (
-        ctypes.byref(cache), heads, k, scale, _dev(q), _dev(k_pages), _dev(k_scale), _dev(v_pages),
-        _dev(v_scale), _dev(table), _dev(lengths), _dev(idx), _dev(out), _dev(lse), _dev(ws),
-        _nbytes(ws)), stream)
+    on = _device(q)
+    _call(_lib.misa_attend, on, (
+        ctypes.byref(cache), heads, k, scale, _dev(q, on), _dev(k_pages, on),
+        _dev(k_scale, on), _dev(v_pages, on), _dev(v_scale, on),
+        _ints(table, on), _ints(lengths, on), _ints(idx, on),
+        _dev(out, on), _dev(lse, on), _dev(ws, on), _nbytes(ws)), stream)
 
 
 def misa_page_write(cache, n, row, pos, k_new, v_new, k_pages, k_scale, v_pages, v_scale, table,
                     stream=None):
-    _call("misa_page_write", k_pages, (
-        ctypes.byref(cache), n, _dev(row), _dev(pos), _dev(k_new), _dev(v_new), _dev(k_pages),
-        _dev(k_scale), _dev(v_pages), _dev(v_scale), _dev(table)), stream)
+    on = _device(k_pages)
+    _call(_lib.misa_page_write, on, (
+        ctypes.byref(cache), n, _ints(row, on), _ints(pos, on),
+        _dev(k_new, on), _dev(v_new, on), _dev(k_pages, on),
+        _dev(k_scale, on), _dev(v_pages, on), _dev(v_scale, on),
+        _ints(table, on)), stream)
 
 
 def misa_page_extend(cache, n, row, count, table, lengths, refs, ok, stream=None):
-    _call("misa_page_extend", table, (
-        ctypes.byref(cache), n, _dev(row), _dev(count), _dev(table), _dev(lengths), _dev(refs),
-        _dev(ok)), stream)
+    on = _device(table)
+    _call(_lib.misa_page_extend, on, (
+        ctypes.byref(cache), n, _ints(row, on), _ints(count, on),
+        _ints(table, on), _ints(lengths, on), _ints(refs, on),
+        _dev(ok, on)), stream)
 
 
 def misa_page_fork(cache, n, parent, child, table, lengths, refs, src, dst, ok, stream=None):
-    _call("misa_page_fork", table, (
-        ctypes.byref(cache), n, _dev(parent), _dev(child), _dev(table), _dev(lengths), _dev(refs),
-        _dev(src), _dev(dst), _dev(ok)), stream)
+    on = _device(table)
+    _call(_lib.misa_page_fork, on, (
+        ctypes.byref(cache), n, _ints(parent, on), _ints(child, on),
+        _ints(table, on), _ints(lengths, on), _ints(refs, on),
+        _dev(src, on), _dev(dst, on), _dev(ok, on)), stream)
 
 
 def misa_page_free(cache, n, row, table, lengths, refs, stream=None):
-    _call("misa_page_free", table, (
-        ctypes.byref(cache), n, _dev(row), _dev(table), _dev(lengths), _dev(refs)), stream)
+    on = _device(table)
+    _call(_lib.misa_page_free, on, (
+        ctypes.byref(cache), n, _ints(row, on), _ints(table, on),
+        _ints(lengths, on), _ints(refs, on)), stream)
 
 
 def misa_page_workspace_bytes(cache: misa_cache) -> int:
@@ -317,18 +370,25 @@ def misa_page_workspace_bytes(cache: misa_cache) -> int:
 
 
 def misa_page_compact(cache, table, refs, table_out, refs_out, map, live, src, dst, ws, stream=None):
-    _call("misa_page_compact", table, (
-        ctypes.byref(cache), _dev(table), _dev(refs), _dev(table_out), _dev(refs_out), _dev(map),
-        _dev(live), _dev(src), _dev(dst), _dev(ws), _nbytes(ws)), stream)
+    on = _device(table)
+    _call(_lib.misa_page_compact, on, (
+        ctypes.byref(cache), _ints(table, on), _ints(refs, on),
+        _dev(table_out, on), _dev(refs_out, on), _dev(map, on),
+        _dev(live, on), _dev(src, on), _dev(dst, on),
+        _dev(ws, on), _nbytes(ws)), stream)
 
 
 def misa_page_copy(buffers, pages, n, src, dst, stream=None):
     """`buffers`: what page_buffers() gives."""
-    _call("misa_page_copy", src, (buffers, len(buffers), pages, n, _dev(src), _dev(dst)), stream)
+    on = _device(src)
+    _call(_lib.misa_page_copy, on, (
+        buffers, len(buffers), pages, n, _dev(src, on), _dev(dst, on)), stream)
 
 
 def misa_rms_norm(rows, n, groups, x_dtype, out_dtype, eps, x, residual, weight, sum_out, out,
                   out_scale, stream=None):
-    _call("misa_rms_norm", x, (
-        rows, n, groups, x_dtype, out_dtype, eps, _dev(x), _dev(residual), _dev(weight),
-        _dev(sum_out), _dev(out), _dev(out_scale)), stream)
+    on = _device(x)
+    _call(_lib.misa_rms_norm, on, (
+        rows, n, groups, x_dtype, out_dtype, eps, _dev(x, on), _dev(residual, on),
+        _dev(weight, on), _dev(sum_out, on), _dev(out, on),
+        _dev(out_scale, on)), stream)

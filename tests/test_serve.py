@@ -172,6 +172,56 @@ def test_binding_refuses_host_and_strided_tensors(misa):
         misa.page_buffers([(host, 1, 4)])
 
 
+class Elsewhere:
+    """What the binding asks of a tensor, on a device that need not be there."""
+
+    def __init__(self, dtype, device):
+        self.dtype, self.device = dtype, device
+
+    def get_device(self):
+        return self.device
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return FAKE
+
+    def numel(self):
+        return 1
+
+    element_size = numel
+
+
+def test_binding_refuses_wide_integers(misa):
+    """A list of 64-bit integers would be read as twice as many."""
+    c = misa.cache(4, 8, 40, 16, 2, 128, 128, misa.MISA_BF16)
+    wide = Elsewhere(torch.int64, 0)
+    calls = {
+        "misa_attend": ([c, 8, 4, 0.1] + [FAKE] * 10 + [None], (9, 10, 11)),  # table, lengths, idx
+        "misa_page_write": ([c, 1] + [FAKE] * 9, (2, 3, 10)),
+        "misa_page_extend": ([c, 1] + [FAKE] * 6, (2, 3, 4, 5, 6)),
+        "misa_page_fork": ([c, 1] + [FAKE] * 8, (2, 3, 4, 5, 6)),
+        "misa_page_free": ([c, 1] + [FAKE] * 4, (2, 3, 4, 5)),
+        "misa_page_compact": ([c] + [FAKE] * 8 + [None], (1, 2)),
+    }
+    for name, (args, places) in calls.items():
+        for i in places:
+            with pytest.raises(ValueError, match="must be torch.int32, not torch.int64"):
+                getattr(misa, name)(*[wide if j == i else x for j, x in enumerate(args)], stream=0)
+
+
+def test_binding_refuses_tensors_apart(misa):
+    c = misa.cache(4, 8, 40, 16, 0, 0, 0, 0)
+    here, there = Elsewhere(torch.int32, 0), Elsewhere(torch.int32, 1)
+    with pytest.raises(ValueError, match="on the device"):
+        misa.misa_page_free(c, 1, there, here, here, here, stream=0)
+    with pytest.raises(ValueError, match="on the device"):
+        misa.misa_page_free(c, 1, FAKE, Elsewhere(torch.int32, -1), FAKE, FAKE, stream=0)
+    with pytest.raises(ValueError, match="on the device"):
+        misa.page_buffers([(here, 1, 4), (there, 1, 4)])
+
+
 # ------------------------------------------------------------------ inputs
 
 
