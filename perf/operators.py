@@ -227,6 +227,7 @@ def prepare(case, seed):
         _plain_beam(s)  # the children hold the pages of a step before
         s["parent"] = torch.randint(n, (n,), generator=g, device="cuda").int()
         if own:
+            s["src"], s["dst"] = s["src"].int(), s["dst"].int()  # the plain step left 64-bit ids
             _cache(s, 2 * n, width, pages, case["d"], case["d"])
         return s
     # attention and writes: a pool with a tenth of spare pages
