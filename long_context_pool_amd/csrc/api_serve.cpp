@@ -18,8 +18,6 @@ using misa::check_out;
 using misa::check_ws;
 using misa::from_hip;
 
-constexpr int32_t kMaxList = 4096;  // entries of an extend / fork / free list (LDS)
-
 // The page table's half of a cache: sizes only.
 misa_status check_table(const misa_cache* c, Cache& out) {
   if (!c) return MISA_ERR_INVALID_ARG;
@@ -62,7 +60,7 @@ misa_status check_pools(const Cache& c, const void* k_pages, const float* k_scal
 
 misa_status check_list(int32_t n) {
   if (n < 0) return MISA_ERR_INVALID_ARG;
-  return n > kMaxList ? MISA_ERR_UNSUPPORTED : MISA_OK;
+  return n > misa::kMaxList ? MISA_ERR_UNSUPPORTED : MISA_OK;
 }
 
 misa_status check_attend(const misa_cache* cache, int32_t heads, int32_t k, Cache& c) {

@@ -137,6 +137,7 @@ hipError_t launch_page_write(const Cache& c, int32_t n, const int32_t* row, cons
                              const void* k_new, const void* v_new, void* k_pages, float* k_scale,
                              void* v_pages, float* v_scale, const int32_t* table, hipStream_t st);
 
+constexpr int32_t kMaxList = 4096;  // entries of an extend, fork or free list (in LDS)
 hipError_t launch_page_extend(const Cache& c, int32_t n, const int32_t* row, const int32_t* count,
                               int32_t* table, int32_t* lengths, int32_t* refs, int32_t* ok,
                               hipStream_t st);

@@ -110,8 +110,8 @@ hipError_t launch_write(const Cache& c, int32_t n, const int32_t* row, const int
 // ---------------------------------------------------------------- page bookkeeping
 
 constexpr int kListThreads = 1024;  // one workgroup plans a list
-constexpr int kMaxEntries = 4096;   // entries of a list; 4 per thread
-constexpr int kPerThread = kMaxEntries / kListThreads;
+constexpr int kPerThread = kMaxList / kListThreads;
+static_assert(kPerThread * kListThreads == kMaxList, "every entry of the longest list has a thread");
 constexpr int32_t kNone = -1;
 
 // Pages a row of `len` tokens holds, and its length as the table can hold it.
@@ -128,13 +128,13 @@ __device__ __forceinline__ int32_t per_thread(int32_t n) { return (n + kListThre
 // addressing over at least twice as many places as entries, so that a search
 // ends.  The first entry is a minimum: the order of the threads does not matter.
 struct Rows {
-  int32_t key[2 * kMaxEntries];
-  int32_t first[2 * kMaxEntries];
+  int32_t key[2 * kMaxList];
+  int32_t first[2 * kMaxList];
 };
 
 __device__ __forceinline__ uint32_t rows_size(int32_t n) {
   uint32_t size = 64;
-  while (size < 2u * n) size *= 2;  // at most 2 * kMaxEntries
+  while (size < 2u * n) size *= 2;  // at most 2 * kMaxList
   return size;
 }
 
@@ -142,7 +142,7 @@ __device__ __forceinline__ uint32_t rows_size(int32_t n) {
 __device__ __forceinline__ void rows_clear(Rows& h, uint32_t size) {
   for (uint32_t i = threadIdx.x; i < size; i += kListThreads) {
     h.key[i] = kNone;
-    h.first[i] = kMaxEntries;
+    h.first[i] = kMaxList;
   }
 }
 
@@ -210,10 +210,10 @@ __global__ __launch_bounds__(kListThreads) void page_extend_kernel(
     const int32_t* __restrict__ row, const int32_t* __restrict__ count, int32_t* __restrict__ table,
     int32_t* __restrict__ lengths, int32_t* refs, int32_t* __restrict__ ok) {
   __shared__ Rows seen;
-  __shared__ int32_t list[kMaxEntries];
-  __shared__ int32_t offset[kMaxEntries];  // pages needed by the entries before this one
-  __shared__ int32_t held[kMaxEntries];    // pages of the entry's row before the call
-  __shared__ int32_t taken[kMaxEntries];
+  __shared__ int32_t list[kMaxList];
+  __shared__ int32_t offset[kMaxList];  // pages needed by the entries before this one
+  __shared__ int32_t held[kMaxList];    // pages of the entry's row before the call
+  __shared__ int32_t taken[kMaxList];
   __shared__ int tmp[kListThreads / kWave];
   const int4 first_refs = refs_at(refs, pages, threadIdx.x * 4);
   const int32_t per = per_thread(n);  // thread t has the entries per * t + e, e < per
@@ -262,7 +262,7 @@ __global__ __launch_bounds__(kListThreads) void page_extend_kernel(
     at += need[e];
   }
   const int have = scan_free(refs, pages, total, first_refs, tmp, [&](int rank, int32_t page) {
-    if (rank < kMaxEntries) taken[rank] = page;
+    if (rank < kMaxList) taken[rank] = page;
   });
   __syncthreads();
   auto hand_out = [&](int rank, int32_t page) {
@@ -276,7 +276,7 @@ __global__ __launch_bounds__(kListThreads) void page_extend_kernel(
     table[static_cast<int64_t>(list[lo]) * row_pages + held[lo] + (rank - offset[lo])] = page;
     refs[page] = 1;
   };
-  if (total <= kMaxEntries)
+  if (total <= kMaxList)
     for (int j = threadIdx.x; j < have; j += kListThreads) hand_out(j, taken[j]);
   else
     scan_free(refs, pages, have, first_refs, tmp, hand_out);
@@ -316,10 +316,10 @@ __global__ __launch_bounds__(kListThreads) void page_fork_kernel(
     int32_t* __restrict__ lengths, int32_t* refs, int32_t* __restrict__ src,
     int32_t* __restrict__ dst, int32_t* __restrict__ ok) {
   __shared__ Rows seen;
-  __shared__ int32_t taken[kMaxEntries];
-  __shared__ int32_t whole[APPLY ? kMaxEntries : 1];   // pages to share
-  __shared__ int32_t source[APPLY ? kMaxEntries : 1];  // the parents
-  __shared__ int32_t target[APPLY ? kMaxEntries : 1];  // the children
+  __shared__ int32_t taken[kMaxList];
+  __shared__ int32_t whole[APPLY ? kMaxList : 1];   // pages to share
+  __shared__ int32_t source[APPLY ? kMaxList : 1];  // the parents
+  __shared__ int32_t target[APPLY ? kMaxList : 1];  // the children
   __shared__ int tmp[kListThreads / kWave];
   const int4 first_refs = refs_at(refs, pages, threadIdx.x * 4);
   const int32_t per = per_thread(n);  // thread t has the entries per * t + e, e < per
