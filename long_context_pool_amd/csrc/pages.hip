@@ -597,11 +597,12 @@ __global__ __launch_bounds__(kListThreads) void page_compact_small_kernel(
     }
 }
 
-// Last launch: the movers' map entries, refs and the tables.  Threads that
-// meet an entry of `map` before or after it is resolved find the same page.
+// Last launch: the movers' map entries, refs and the tables, which may be the same
+// arrays before and after.  Threads that meet an entry of `map` before or after it
+// is resolved find the same page.
 __global__ __launch_bounds__(256) void page_finish_kernel(
-    int32_t pages, int64_t entries, const int32_t* __restrict__ table, const int32_t* refs,
-    int32_t* __restrict__ table_out, int32_t* refs_out, int32_t* map,
+    int32_t pages, int64_t entries, const int32_t* table, const int32_t* refs,
+    int32_t* table_out, int32_t* refs_out, int32_t* map,
     const int32_t* __restrict__ live_out, const int32_t* __restrict__ src,
     const int32_t* __restrict__ dst) {
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
