@@ -559,10 +559,12 @@ __global__ __launch_bounds__(256) void page_place_kernel(int32_t pages, int32_t 
   if (p == 0) live_out[0] = live;
 }
 
-// A table entry's page afterwards, from the map as place4 leaves it.
+// A table entry's page afterwards, from the map as place4 leaves it.  The map's entry
+// is loaded once (an atomic load of a wave's scope is an ordinary one): another
+// thread may resolve it meanwhile.
 __device__ __forceinline__ int32_t moved_page(int32_t id, int32_t pages, const int32_t* map, const int32_t* dst) {
   if (id < 0 || id >= pages) return kNone;
-  const int32_t to = map[id];
+  const int32_t to = __hip_atomic_load(map + id, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WAVEFRONT);
   return to < kNone ? dst[-2 - to] : to;
 }
 
