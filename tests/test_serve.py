@@ -442,6 +442,35 @@ def test_attend_large_caches(misa, dk, dv, dtype):
 
 
 @gpu
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+@pytest.mark.parametrize("dk,share", [(64, 4), (64, 20), (64, 40), (128, 4), (128, 20), (128, 40), (256, 4), (256, 20)])
+def test_attend_dense_stages(misa, dk, share, fp8):
+    """Whole rows of several stages of 2048 tokens, hidden tokens at their edges: one and two tiles of query heads with
+    loads that are not kept, and two chunks of heads with loads that are."""
+    lengths = [0] * 1024
+    lengths[0], lengths[5], lengths[900], lengths[1023] = 5000, 2049, 4097, 77
+    holes = [(0, 127, -1), (0, 128, -1), (0, 256, -1), (5, 128, -1), (900, 0, -1)]
+    case = _attend_case(misa, dk, dk, 1, share, 16, lengths, 2 if fp8 else 1, seed=share, row_pages=313, holes=holes)
+    _log(f"[gpu] dense stages {dk} share {share} fp8 {fp8}")
+    _check_attend(misa, *case)
+
+
+@gpu
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+@pytest.mark.parametrize("heads", [64, 65, 128])
+def test_attend_latent_stages(misa, heads, fp8):
+    """Splits of several stages of 512 tokens, whose slots are filled again while buffers change hands; hidden tokens at
+    a stage's edges; one chunk of 64 query heads, a second one of a single head, two whole ones.  Many rows by the
+    table, few with tokens, so that a row has few splits."""
+    lengths = [0] * 64
+    lengths[3], lengths[17], lengths[40], lengths[63] = 8191, 2049, 513, 1100
+    holes = [(3, 31, -1), (3, 32, -1), (3, 64, -1), (3, 300, -1), (17, 33, -1), (17, 128, -1), (40, 32, -1), (63, 0, -1)]
+    case = _attend_case(misa, 576, 512, 1, heads, 16, lengths, 2 if fp8 else 1, seed=heads, row_pages=512, holes=holes)
+    _log(f"[gpu] latent stages {heads} fp8 {fp8}")
+    _check_attend(misa, *case)
+
+
+@gpu
 def test_attend_far_offsets(misa):
     """Pools beyond 2^32 bytes and 2^31 elements: the rows live in the last pages."""
     P, kv, d = 64, 8, 128
@@ -848,6 +877,22 @@ def test_norm(misa, rows, n, groups, xt, ot):
     for residual in (None, (2 * torch.randn(rows, n, generator=gen)).to(xt)):
         _check_norm(misa, rows, n, groups, xt, ot, 1e-6, x, residual, weight)
     _check_norm(misa, rows, n, groups, xt, ot, 1e-6, x, residual, weight, in_place=True)
+
+
+@gpu
+@pytest.mark.parametrize("ot,rows,n,groups", [
+    (torch.float8_e4m3fn, 4095, 4096, 1), (torch.float8_e4m3fn, 4096, 4096, 1), (torch.float8_e4m3fn, 4098, 4095, 1),
+    (torch.float8_e4m3fn, 2049, 8192, 64), (torch.float8_e4m3fn, 70000, 251, 1), (torch.float8_e4m3fn, 130000, 130, 2),
+    (torch.bfloat16, 2047, 4096, 1), (torch.bfloat16, 2048, 4096, 1), (torch.bfloat16, 2050, 4095, 1),
+    (torch.bfloat16, 1025, 8192, 64), (torch.bfloat16, 35000, 251, 1),
+])
+def test_norm_large_outputs(misa, ot, rows, n, groups):
+    """Outputs from just below to above 16 MB, from which on they are stored past the caches; rows of odd length, whose
+    stores are aligned to an element only."""
+    gen = torch.Generator().manual_seed(n)
+    x = torch.randn(rows, n, generator=gen).bfloat16()
+    _log(f"[gpu] norm large {rows} x {n} / {groups} {ot}")
+    _check_norm(misa, rows, n, groups, torch.bfloat16, ot, 1e-6, x, None, torch.randn(n // groups, generator=gen))
 
 
 @gpu
