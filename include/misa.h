@@ -400,7 +400,8 @@ misa_status misa_page_copy(const misa_page_buffer* buffers, int32_t n_buffers, i
  *   out_scale    [rows]     fp32, written (fp8 only, else ignored)
  * out must not overlap the inputs or sum_out.  fp32 throughout: a part's mean
  * square plus eps must be in fp32's normal range (an all-zero part with eps = 0
- * gives NaN).  0 <= rows < 2^24 (0: no-op), 1 <= n <= 32768, groups divides n,
+ * gives NaN), and results between 2^-110 and 2^112 in magnitude, or zero, have its
+ * full precision.  0 <= rows < 2^24 (0: no-op), 1 <= n <= 32768, groups divides n,
  * eps >= 0. */
 misa_status misa_rms_norm(int32_t rows, int32_t n, int32_t groups, int32_t x_dtype,
                           int32_t out_dtype, float eps, const void* x, const void* residual,

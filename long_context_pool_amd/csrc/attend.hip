@@ -66,13 +66,13 @@ __device__ __forceinline__ int value_dim(int c, int j) {
 // one reader, and the next tile's loads are under way while one is worked on.
 //
 // Bound by memory: 8 rows of up to 131072 fp8 tokens of 8 heads of 128 (1.73 GB)
-// 292 us, 5.9 TB/s; 32 rows x 2048 listed bf16 tokens (261 MB, pieces of 256
-// bytes) 51 us, 5.1 TB/s.  One row of 2000 tokens (8 MB)
-// 6.2 us: a launch, three dependent loads to a slot, one tile's loads and the
-// join of the waves' sums.
+// 292 to 309 us on several boxes, 5.6 to 5.9 TB/s; 32 rows x 2048 listed bf16 tokens
+// (261 MB, pieces of 256 bytes) 51 us, 5.1 TB/s.  One row of 2000 tokens (8 MB) 6.2
+// us: a launch, three dependent loads to a slot, one tile's loads and the join of
+// the waves' sums.
 //
 // ONCE: the cache is read once (one chunk of query heads) and is large, so its
-// loads are marked as not to be kept (the 8 rows above: 322 us with plain loads;
+// loads are marked as not to be kept (the 8 rows above: 298 us, 322 with plain loads;
 // with two chunks that share a row through L2 it is the other way round, 564 us
 // against 505 us).
 template <int D, int DT, int RT, bool ONCE>
@@ -381,9 +381,10 @@ constexpr int kMaxSplits = 128;
 // Splits of a latent row.  A workgroup (one per CU) takes 2.8 us for a pair of
 // tiles; a join costs about 6 us and, for each split, the way of its sums to
 // memory and back, 4 KB a head at 5.1 TB/s.  24 rows of 128 heads: 384 listed
-// tokens 23.0 us whole, 27.8 us in two splits; 4096 169, 101, 74, 64, 73 and 80 us
+// tokens 23.7 us whole, 25.0 us in two splits; 4096 171, 102, 75, 63, 78 and 89 us
 // in 1, 2, 3, 4, 8 and 16.  With sixteen rounds of workgroups and more, a split
-// could save at most a part of the last one.
+// could save at most a part of the last one.  An fp8 pair takes a tenth more; in
+// seven cases of it, 1 to 200 rows, the choice is at most 7% from the best count.
 int32_t latent_splits(int64_t groups, int64_t tokens, int64_t heads, int64_t limit) {
   if (groups >= 16 * kCus) return 1;
   int32_t best = 1;
@@ -401,14 +402,16 @@ int32_t latent_splits(int64_t groups, int64_t tokens, int64_t heads, int64_t lim
 
 // Splits of a dense row: at most those that fill the card in one round, since more
 // only add to the join and to the last round's tail (8 rows of up to 131072 fp8
-// tokens: 768 workgroups 322 us, 1024 340 us, 512 342 us), and fewer where their
-// join costs more than the steps that it saves.  A wave's step, one tile of K and
-// of V, takes 0.55 us and for each workgroup on its CU the four waves' share of
-// memory and instructions; a join 5.8 us and the sums' way through memory.  Fitted
-// to 730 cases with caches from memory, of which the choice is 4% from the best
-// one, as many splits as fill the card 9%: 32 rows of 600 tokens, 64 heads on 8,
-// 16.0 us whole, 21.4 us in three; 16 rows of 1000 with 256 heads 21.4 and 24.1
-// us; one row of 2000, 64 heads on 8, 9.7 us in sixteen, 24.8 us whole.
+// tokens: 768 workgroups 322 us, 1024 340 us, 512 342 us; all with plain loads), and
+// fewer where their join costs more than the steps that it saves.  A wave's step,
+// one tile of K and of V, takes 0.55 us and for each workgroup on its CU the four
+// waves' share of memory and instructions; a join 5.8 us and the sums' way through
+// memory.  Fitted to 730 cases with caches from memory, of which the choice is 4%
+// from the best one, as many splits as fill the card 9%: 32 rows of 600 tokens, 64
+// heads on 8, 16.0 us whole, 21.4 us in three; 16 rows of 1000 with 256 heads 21.4
+// and 24.1 us; one row of 2000, 64 heads on 8, 9.7 us in sixteen, 24.8 us whole.
+// Groups beyond half of one round stay whole: 8 fp8 heads, rows of 32768 tokens, 48
+// rows in two splits 539 us, 49 rows whole 632 us.
 int32_t dense_splits(const Cache& c, int32_t heads, int32_t share, int64_t groups, int64_t tokens,
                      int64_t limit) {
   const int32_t held = resident(c, share);

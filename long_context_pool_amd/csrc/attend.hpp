@@ -132,8 +132,8 @@ __device__ __forceinline__ float final_lse(float m, float l) {
 // four dimensions each, and 1024 / D groups of them take every such split; the
 // groups' sums are added in order.  A launch of its own: a workgroup that waits
 // for its peers' sums would need an arrival count that is known to start at zero.
-// 32 heads of one row, 16 splits: 3.8 us, a launch and two dependent loads; 32
-// rows of 128 heads of 512 in 4 splits (34 MB) 9.1 us, 3.7 TB/s.
+// 32 heads of one row, 16 splits: 3.5 us, a launch and two dependent loads; 32
+// rows of 128 heads of 512 in 4 splits (34 MB) 8.6 us, 3.9 TB/s.
 template <int D>
 __global__ __launch_bounds__(256) void attend_join_kernel(Args a) {
   constexpr int T = D / 4, GS = 256 / T;

@@ -96,7 +96,7 @@ __device__ __forceinline__ void hand_over(const Args& a, const f32x4 (&acc)[NJ],
 // weight's first part is its rounding (2^-17 together): a cached infinity makes its
 // own token's scores infinite or NaN, so that it never meets a weight above zero.
 //
-// 32 rows of 128 heads over 2048 listed bf16 tokens, in 4 splits: 39.8 us and the
+// 32 rows of 128 heads over 2048 listed bf16 tokens, in 4 splits: 39 us and the
 // join.  Of that a pair of tiles takes 2.77 us (eight of them), for 1.1 us of LDS
 // cycles and 1.33 us of matrix cycles: with two waves a SIMD and all but a few of
 // their 256 registers taken (O 128, queries 60), six reads are under way, too few

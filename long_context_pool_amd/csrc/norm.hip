@@ -128,7 +128,7 @@ __device__ __forceinline__ float far_squares(const float (&y)[8]) {
 // no multiple of eight; its last vector ends with the row, and the elements that
 // the one before already has are left out of sums and stores.  Bound by memory
 // traffic: 8192 rows of 64 parts of 128, bf16 -> fp8 (201 MB), 35.5 us, 5.7 TB/s;
-// 32 rows of 4096 with residual, 3.8 us, a launch and two loads' latency.
+// 32 rows of 4096 with residual, 3.6 us, a launch and two loads' latency.
 template <int XT, int T, int V, bool GROUPED, bool ODD>
 __global__ __launch_bounds__(256) void norm_kernel(int32_t rows, int32_t n, int32_t size,
                                                    int32_t part_shift, int32_t out_dtype,

@@ -18,8 +18,8 @@ namespace {
 // (LATENT: K alone): D elements, 8 per lane and step, one 16-byte load each; fp8
 // reduces the largest magnitude over the subgroup first.  Both rows' loads are
 // under way while three dependent loads find the slot.  Bound by memory
-// traffic: 8192 tokens of 8 heads of 128 to fp8 (47 MB) 12.1 us, 3.9 TB/s; 32
-// tokens in bf16 2.8 us, a launch and four dependent loads.
+// traffic: 8192 tokens of 8 heads of 128 to fp8 (47 MB) 12.2 us, 3.9 TB/s; 32
+// tokens in bf16 3.0 us, a launch and four dependent loads.
 template <int D, bool FP8, bool LATENT>
 __global__ __launch_bounds__(256) void page_write_kernel(
     uint32_t items, int32_t kv_heads, int32_t rows, int32_t row_pages, int32_t pages, int32_t P,
@@ -204,7 +204,7 @@ __device__ int scan_free(const int32_t* refs, int32_t pages, int32_t want, int4 
 // prefix sum; one scan collects the free pages' ids in LDS, and thread j hands
 // out the j-th.  Lists that need more than LDS holds scan again.  Bound by the
 // latency of its chain (entries, lengths, refs, tables): 8 rows of a pool of 900
-// pages 3.1 us, 128 rows of one of 14000 4.9 us.
+// pages 3.8 us, 128 rows of one of 14000 5.1 us.
 __global__ __launch_bounds__(kListThreads) void page_extend_kernel(
     int32_t n, int32_t rows, int32_t row_pages, int32_t pages, int32_t P,
     const int32_t* __restrict__ row, const int32_t* __restrict__ count, int32_t* __restrict__ table,
@@ -307,7 +307,7 @@ __device__ __forceinline__ void share_pages(int32_t* __restrict__ table, int32_t
 // a wave per entry (short lists; longer ones take a second launch for that).
 // A parent of a forked child that is not empty is no child of the call, so its
 // row does not change.  Bound by latency like extend: 8 children 6.2 us, sharing
-// up to 125 pages each included; 128 children 5.2 us, and 2.5 us for the second
+// up to 125 pages each included; 128 children 5.4 us, and 3.3 us for the second
 // launch.
 template <bool APPLY>
 __global__ __launch_bounds__(kListThreads) void page_fork_kernel(
