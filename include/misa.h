@@ -408,6 +408,154 @@ misa_status misa_rms_norm(int32_t rows, int32_t n, int32_t groups, int32_t x_dty
                           const float* weight, void* sum_out, void* out, float* out_scale,
                           hipStream_t stream);
 
+/* ------------------------------------------------------------ rotary positions */
+
+typedef enum {
+  MISA_ROPE_HALF = 0,       /* pair i: elements i and i + rot/2 of the rotated part */
+  MISA_ROPE_INTERLEAVED = 1 /* pair i: elements 2i and 2i + 1                       */
+} misa_rope_pairs;
+
+/* What misa_rope turns: heads of d elements, of which first .. first + rot - 1
+ * are rotated in rot / 2 pairs; the others pass.  x_stride and out_stride are
+ * elements from one token to the next, so that the heads may be a part of a
+ * wider row (the queries and keys of a fused projection).  amplitude multiplies
+ * the rotated part. */
+typedef struct {
+  int32_t heads, d, first, rot;
+  int32_t pairs;             /* a misa_rope_pairs */
+  int32_t x_dtype, out_dtype;
+  float amplitude;
+  int64_t x_stride, out_stride;
+} misa_rope_spec;
+
+/* Rotary positions.  Pair i of a head of token t, (a, b), becomes
+ *   amplitude * (a cos - b sin, a sin + b cos)  of the angle pos[t] * freq[i].
+ * The angle is a product in 64 bits, reduced to one turn there: 2^-50 of itself,
+ * at any position.
+ *   x     [n, heads, d], x_stride apart    MISA_F32 or MISA_BF16
+ *   pos   [n]        int32, any sign
+ *   freq  [rot / 2]  fp64, radians a position (misa_rope_frequencies)
+ *   out   [n, heads, d], out_stride apart  MISA_F32, MISA_BF16 or MISA_FP8_E4M3,
+ *         written; may be x itself (same type and stride)
+ *   out_scale  [n]   fp32, written (fp8 only, else ignored): one scale per token
+ *         over its heads, as misa_*'s q_scale and k_scale
+ * 0 <= n < 2^24 (0: no-op); 1 <= heads, heads * d <= 32768; rot even, 0 < rot <=
+ * 1024, first + rot <= d; strides of at least heads * d (out_stride of an fp8 out
+ * exactly that) and below 2^31; rotated values in fp32's normal range. */
+misa_status misa_rope(const misa_rope_spec* spec, int32_t n, const void* x, const int32_t* pos,
+                      const double* freq, void* out, float* out_scale, hipStream_t stream);
+
+typedef enum {
+  MISA_ROPE_PLAIN = 0,  /* f_i = base^(-2i / rot)                                */
+  MISA_ROPE_LINEAR = 1, /* f_i / factor: positions drawn together                */
+  MISA_ROPE_PARTS = 2   /* by parts: slow pairs as LINEAR, fast ones as PLAIN    */
+} misa_rope_kind;
+
+/* Frequencies for contexts longer than the trained one.  MISA_ROPE_PARTS ("YaRN:
+ * Efficient Context Window Extension of Large Language Models", section 3.2):
+ * pairs that turn `fast` times and more in `original` positions keep f_i, those
+ * that turn `slow` times and fewer have f_i / factor, with a linear ramp over i
+ * between; and an amplitude of 1 + 0.1 ln(factor). */
+typedef struct {
+  int32_t kind, rot; /* a misa_rope_kind; rot as in misa_rope_spec */
+  double base;       /* > 1 */
+  double factor;     /* >= 1; LINEAR and PARTS */
+  double original;   /* > 0, positions; PARTS, like fast >= slow > 0 */
+  double fast, slow;
+} misa_rope_scaling;
+
+/* Runs on the HOST: fills freq[0 .. rot/2 - 1] (host memory, to be copied to the
+ * device once) and *amplitude. */
+misa_status misa_rope_frequencies(const misa_rope_scaling* scaling, double* freq,
+                                  float* amplitude);
+
+/* ------------------------------------------- a cache with one scale per block
+ * The paged cache above with e4m3 codes and ONE scale for each block of
+ * block_tokens tokens of a page and kv head:
+ *   k_pages, v_pages  [pages, kv_heads, page_tokens, d]   e4m3 codes
+ *   k_scale, v_scale  [pages, kv_heads, page_tokens / block_tokens]  fp32
+ * cache->kv_dtype is MISA_FP8_E4M3, dk = dv in {64, 128, 256}; block_tokens is 16,
+ * 32, 64 or 128 and divides page_tokens; rows <= 65535.  The table, lengths and refs
+ * and the calls that keep them (misa_page_extend, ..fork, ..free, ..compact,
+ * ..copy) are those of misa_cache; codes and scales are buffers of misa_page_copy.
+ *
+ * A scale is a power of two: the smallest 2^e, e >= -100, with amax <= 448 * 2^e
+ * over the finite values that the block got so far.  A code is x / scale rounded
+ * to nearest even; infinities and NaN become NaN codes and set no scale.
+ *
+ * Batches of rows come packed: offsets [rows + 1] int32, ascending; entries
+ * offsets[r] .. offsets[r+1] - 1 of the packed arrays belong to row r, whose
+ * number may be zero.  Entries before offsets[0] and from offsets[rows] on
+ * (padding of a captured batch) are not read and their outputs left as they were.
+ * New tokens are the last ones of their row: with c of them, token i of row r is at
+ * position lengths[r] - c + i (misa_page_extend has counted them). */
+
+/* Write the rows' new tokens.  The first of them may go on in a block that holds
+ * earlier tokens: the block keeps its scale, or, where the new ones are louder,
+ * gets a larger one and its codes are rounded to that (exact but for codes that
+ * become subnormal).  What the block held at and behind the new tokens'
+ * positions counts for nothing but its scale.  Positions outside the table or
+ * without a page are skipped.  Rows must not share a block that is written
+ * (misa_page_fork sees to that).
+ *   k_new, v_new  [n, kv_heads, d]  bf16; v_new, v_pages and v_scale all NULL: a
+ *                 cache of keys alone (the indexer's)
+ * n = 0 is a no-op; n * kv_heads <= 2^25. */
+misa_status misa_block_write(const misa_cache* cache, int32_t block_tokens, int32_t n,
+                             const int32_t* offsets, const int32_t* lengths, const void* k_new,
+                             const void* v_new, void* k_pages, float* k_scale, void* v_pages,
+                             float* v_scale, const int32_t* table, hipStream_t stream);
+
+/* Read rows back: packed entry i of row r is its token first[r] + i - offsets[r]
+ * (first NULL: from token 0).  Tokens outside [0, lengths[r]) or without a page
+ * read as zeros (scale 1).
+ *   first         [rows] int32 or NULL
+ *   k_out, v_out  [n, kv_heads, d]  out_dtype (any misa_dtype), written: code *
+ *                 scale, rounded once (exact in bf16 down to its subnormals); fp8:
+ *                 the codes, with
+ *   k_out_scale, v_out_scale  [n, kv_heads]  fp32, written (fp8 only, else
+ *                 ignored).  With one kv head of 128 and rows of L tokens (offsets
+ *                 r * L) these are misa_*'s k and k_scale.
+ * Keys alone: v_pages, v_scale, v_out and v_out_scale NULL.  n = 0 is a no-op; n *
+ * kv_heads <= 2^28. */
+misa_status misa_block_read(const misa_cache* cache, int32_t block_tokens, int32_t n,
+                            int32_t out_dtype, const int32_t* offsets, const int32_t* first,
+                            const int32_t* lengths, const void* k_pages, const float* k_scale,
+                            const void* v_pages, const float* v_scale, const int32_t* table,
+                            void* k_out, float* k_out_scale, void* v_out, float* v_out_scale,
+                            hipStream_t stream);
+
+/* Attention of the rows' new tokens (one of each row, drafts, a prompt's chunk)
+ * over the block-scaled cache that holds them already, causal:
+ *   o[i, j, :] = sum_s p_s v[r, s, g, :],  p = softmax_s(scale * q[i,j,:] . k[r,s,g,:]),
+ *   lse[i, j] = log sum_s exp(scale * q . k),   g = j / (heads / kv_heads),
+ * over the tokens s of row r up to the query's own position, or with k > 0 those
+ * of them that idx[i, :] lists (any order, -1 padded, as the indexer's entry points
+ * write it).  Tokens whose table entry names no page are not visible.  A query
+ * without visible tokens gets o = 0 and lse = -INFINITY.  What the cache holds at
+ * invisible slots is never used, NaN or not.
+ *   most  the largest number of new tokens of a row: it picks the kernel and sizes
+ *         the workspace, and no result depends on it but by roundings
+ *   q    [n, heads, d]  bf16         out [n, heads, d]  bf16, written
+ *   idx  [n, k]  int32 (k > 0; k = 0: NULL)
+ *   lse  [n, heads]  fp32, written if non-NULL
+ * Scores, softmax and sums are fp32: q . codes and a score times log2(e) must be in
+ * its range, and cached values below 2^90; a weight goes into its products in 16 or
+ * 11 bits and never moves a sum by more than 2^-11 of itself, or 2^-31 of the
+ * largest.  Values in blocks whose scale is less than 2^-60 of the largest one of
+ * the row and head count to 2^-60 of that.  Limits: heads a multiple of kv_heads, heads <= 1024, n <= 2^20 and n * heads
+ * <= 2^26, 0 <= k <= 2^20, |scale| <= 2^127.  ws must hold
+ * misa_block_attend_workspace_bytes(...) bytes (0: invalid arguments or no workspace
+ * needed); it carries nothing from one call to the next. */
+size_t misa_block_attend_workspace_bytes(const misa_cache* cache, int32_t block_tokens,
+                                         int32_t heads, int32_t n, int32_t most, int32_t k);
+misa_status misa_block_attend(const misa_cache* cache, int32_t block_tokens, int32_t heads,
+                              int32_t n, int32_t most, int32_t k, float scale,
+                              const int32_t* offsets, const void* q, const void* k_pages,
+                              const float* k_scale, const void* v_pages, const float* v_scale,
+                              const int32_t* table, const int32_t* lengths, const int32_t* idx,
+                              void* out, float* lse, void* ws, size_t ws_bytes,
+                              hipStream_t stream);
+
 /* A static, human-readable name of a status code. */
 const char* misa_status_string(misa_status status);
 

@@ -32,6 +32,8 @@ MISA_ERR_WORKSPACE = -3
 MISA_ERR_HIP = -4
 
 MISA_F32, MISA_BF16, MISA_FP8_E4M3 = 0, 1, 2
+MISA_ROPE_HALF, MISA_ROPE_INTERLEAVED = 0, 1
+MISA_ROPE_PLAIN, MISA_ROPE_LINEAR, MISA_ROPE_PARTS = 0, 1, 2
 
 EXPORTED = (
     "misa_workspace_bytes", "misa_pool_keys", "misa_pool_keys_range", "misa_route",
@@ -39,7 +41,8 @@ EXPORTED = (
     "dsa_index_dense", "misa_hisa_workspace_bytes", "misa_hisa_score_topk", "misa_status_string",
     "misa_attend_workspace_bytes", "misa_attend", "misa_page_write", "misa_page_extend",
     "misa_page_fork", "misa_page_free", "misa_page_workspace_bytes", "misa_page_compact",
-    "misa_page_copy", "misa_rms_norm",
+    "misa_page_copy", "misa_rms_norm", "misa_rope", "misa_rope_frequencies", "misa_block_write",
+    "misa_block_read", "misa_block_attend_workspace_bytes", "misa_block_attend",
 )
 MISA_NOALLOC_SCRATCH_BYTES = 64 << 20
 
@@ -61,6 +64,16 @@ class misa_cache(ctypes.Structure):
 
 class misa_page_buffer(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("page_bytes", ctypes.c_int64), ("planes", ctypes.c_int32)]
+
+
+class misa_rope_spec(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("heads", "d", "first", "rot", "pairs", "x_dtype", "out_dtype")] + [
+        ("amplitude", ctypes.c_float), ("x_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64)]
+
+
+class misa_rope_scaling(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("rot", ctypes.c_int32)] + [
+        (n, ctypes.c_double) for n in ("base", "factor", "original", "fast", "slow")]
 
 
 if not os.path.exists(LIB_PATH):
@@ -102,11 +115,19 @@ _lib.misa_page_workspace_bytes.restype = _SZ
 _lib.misa_page_compact.argtypes = [_CHE] + [_P] * 9 + [_SZ, _P]
 _lib.misa_page_copy.argtypes = [ctypes.POINTER(misa_page_buffer), _I32, _I32, _I32, _P, _P, _P]
 _lib.misa_rms_norm.argtypes = [_I32] * 5 + [_F32] + [_P] * 7
+_lib.misa_rope.argtypes = [ctypes.POINTER(misa_rope_spec), _I32] + [_P] * 6
+_lib.misa_rope_frequencies.argtypes = [ctypes.POINTER(misa_rope_scaling), _P, ctypes.POINTER(_F32)]
+_lib.misa_block_write.argtypes = [_CHE, _I32, _I32] + [_P] * 10
+_lib.misa_block_read.argtypes = [_CHE, _I32, _I32, _I32] + [_P] * 13
+_lib.misa_block_attend_workspace_bytes.argtypes = [_CHE] + [_I32] * 5
+_lib.misa_block_attend_workspace_bytes.restype = _SZ
+_lib.misa_block_attend.argtypes = [_CHE] + [_I32] * 5 + [_F32] + [_P] * 12 + [_SZ, _P]
 for _f in ("misa_pool_keys", "misa_pool_keys_range", "misa_route", "misa_score_topk",
            "misa_decode_step", "misa_decode_step_noalloc", "misa_rerank", "dsa_index_dense",
            "misa_hisa_score_topk", "misa_attend", "misa_page_write", "misa_page_extend",
            "misa_page_fork", "misa_page_free", "misa_page_compact", "misa_page_copy",
-           "misa_rms_norm"):
+           "misa_rms_norm", "misa_rope", "misa_rope_frequencies", "misa_block_write", "misa_block_read",
+           "misa_block_attend"):
     getattr(_lib, _f).restype = ctypes.c_int
 _lib.misa_status_string.argtypes = [ctypes.c_int]
 _lib.misa_status_string.restype = ctypes.c_char_p
@@ -392,3 +413,88 @@ def misa_rms_norm(rows, n, groups, x_dtype, out_dtype, eps, x, residual, weight,
         rows, n, groups, x_dtype, out_dtype, eps, _dev(x, on), _dev(residual, on),
         _dev(weight, on), _dev(sum_out, on), _dev(out, on),
         _dev(out_scale, on)), stream)
+
+
+# ------------------------------------------------------------------ rotary positions
+
+
+def rope_spec(heads, d, first, rot, pairs, x_dtype, out_dtype, x_stride, out_stride, amplitude=1.0) -> misa_rope_spec:
+    return misa_rope_spec(heads, d, first, rot, pairs, x_dtype, out_dtype, amplitude, x_stride, out_stride)
+
+
+def rope_scaling(kind, rot, base, factor=1.0, original=0.0, fast=0.0, slow=0.0) -> misa_rope_scaling:
+    return misa_rope_scaling(kind, rot, base, factor, original, fast, slow)
+
+
+def misa_rope_frequencies(scaling):
+    """(radians a position of each pair, as a list, and the amplitude)."""
+    freq, amplitude = (ctypes.c_double * max(1, scaling.rot // 2))(), _F32()
+    _check(_lib.misa_rope_frequencies(ctypes.byref(scaling), freq, ctypes.byref(amplitude)), "misa_rope_frequencies")
+    return list(freq), amplitude.value
+
+
+def _heads_of(x, device, stride):
+    """_dev for tokens that are `stride` elements apart: [n, heads * d] or [n, heads, d], whose token
+    may be a part of a wider row."""
+    if x is None or x.__class__ is int:
+        return x
+    on = x.get_device()
+    if (on != device and (device is not None or on < 0)) or x.dim() < 2 or (
+            x.shape[0] > 0 and not (x[0].is_contiguous() and (x.shape[0] == 1 or x.stride(0) == stride))):
+        raise ValueError("tokens must be contiguous, their stride apart and on the device, all on one")
+    return x.data_ptr()
+
+
+_float64 = None
+
+
+def misa_rope(spec, n, x, pos, freq, out, out_scale, stream=None):
+    """x and out: [n, heads * d] or [n, heads, d] tensors with spec.x_stride and spec.out_stride
+    elements from token to token."""
+    global _float64
+    on = _device(x)
+    if freq.__class__ is not int and freq is not None and freq.dtype is not _float64:
+        import torch
+        _float64 = torch.float64
+        if freq.dtype is not _float64:
+            raise ValueError(f"frequencies must be torch.float64, not {freq.dtype}")
+    _call(_lib.misa_rope, on, (
+        ctypes.byref(spec), n, _heads_of(x, on, spec.x_stride), _ints(pos, on), _dev(freq, on),
+        _heads_of(out, on, spec.out_stride), _dev(out_scale, on)), stream)
+
+
+# ------------------------------------------------------------------ the block-scaled cache
+
+
+def misa_block_write(cache, block_tokens, n, offsets, lengths, k_new, v_new, k_pages, k_scale, v_pages,
+                     v_scale, table, stream=None):
+    on = _device(k_pages)
+    _call(_lib.misa_block_write, on, (
+        ctypes.byref(cache), block_tokens, n, _ints(offsets, on), _ints(lengths, on),
+        _dev(k_new, on), _dev(v_new, on), _dev(k_pages, on), _dev(k_scale, on),
+        _dev(v_pages, on), _dev(v_scale, on), _ints(table, on)), stream)
+
+
+def misa_block_read(cache, block_tokens, n, out_dtype, offsets, first, lengths, k_pages, k_scale,
+                    v_pages, v_scale, table, k_out, k_out_scale, v_out, v_out_scale, stream=None):
+    on = _device(k_pages)
+    _call(_lib.misa_block_read, on, (
+        ctypes.byref(cache), block_tokens, n, out_dtype, _ints(offsets, on), _ints(first, on),
+        _ints(lengths, on), _dev(k_pages, on), _dev(k_scale, on), _dev(v_pages, on),
+        _dev(v_scale, on), _ints(table, on), _dev(k_out, on), _dev(k_out_scale, on),
+        _dev(v_out, on), _dev(v_out_scale, on)), stream)
+
+
+def misa_block_attend_workspace_bytes(cache: misa_cache, block_tokens: int, heads: int, n: int, most: int,
+                                      k: int) -> int:
+    return int(_lib.misa_block_attend_workspace_bytes(ctypes.byref(cache), block_tokens, heads, n, most, k))
+
+
+def misa_block_attend(cache, block_tokens, heads, n, most, k, scale, offsets, q, k_pages, k_scale,
+                      v_pages, v_scale, table, lengths, idx, out, lse, ws, stream=None):
+    on = _device(q)
+    _call(_lib.misa_block_attend, on, (
+        ctypes.byref(cache), block_tokens, heads, n, most, k, scale, _ints(offsets, on),
+        _dev(q, on), _dev(k_pages, on), _dev(k_scale, on), _dev(v_pages, on), _dev(v_scale, on),
+        _ints(table, on), _ints(lengths, on), _ints(idx, on), _dev(out, on), _dev(lse, on),
+        _dev(ws, on), _nbytes(ws)), stream)

@@ -75,7 +75,10 @@ __device__ __forceinline__ int value_dim(int c, int j) {
 // loads are marked as not to be kept (the 8 rows above: 298 us, 322 with plain loads;
 // with two chunks that share a row through L2 it is the other way round, 564 us
 // against 505 us).
-template <int D, int DT, int RT, bool ONCE>
+//
+// PACKED (misa_block_attend): a unit is a query of a packed batch instead of a row,
+// and the scales are those of blocks of tokens.
+template <int D, int DT, int RT, bool ONCE, bool PACKED>
 __global__ __launch_bounds__(256) void attend_kernel(Args a) {
   constexpr int EB = DT == kFP8 ? 1 : 2;
   constexpr int ROW = D * EB;       // bytes of a cached row
@@ -108,8 +111,9 @@ __global__ __launch_bounds__(256) void attend_kernel(Args a) {
   if (row >= a.rows) return;
   const int head0 = kvh * a.share + chunk * 16 * RT;       // first query head
   const int nheads = min(16 * RT, a.share - chunk * 16 * RT);
-  int32_t len;
-  const int32_t todo = tokens_of(a, row, len);
+  Query query;
+  if (!query_of<PACKED>(a, row, query)) return;
+  const int32_t todo = tokens_of(a, query);
   const int32_t per = tiles_per_split(a, todo) * kTileTokens;
   const int32_t t0 = split * per, t1 = min(t0 + per, todo);
   if (t0 >= t1 && split > 0) return;  // nothing here; the join does not look at it
@@ -171,11 +175,12 @@ __global__ __launch_bounds__(256) void attend_kernel(Args a) {
     const int32_t tiles = (count + kTileTokens - 1) / kTileTokens;
     if (base != t0) __syncthreads();
     for (int32_t i = threadIdx.x; i < tiles * kTileTokens; i += 256) {
-      const uint32_t s = i < count ? slot_of(a, row, kvh, len, base + i) : kHidden;
+      const uint32_t s = i < count ? slot_of(a, row, query.table_row, kvh, query.len, base + i) : kHidden;
       sh.st.slot[i] = s;
       if constexpr (kFp8) {
-        sh.st.ks[i] = s == kHidden ? 0.f : a.k_scale[s];
-        sh.st.vs[i] = s == kHidden ? 0.f : a.v_scale[s];
+        const uint32_t unit = PACKED ? s >> a.shift : s;  // pages are whole blocks
+        sh.st.ks[i] = s == kHidden ? 0.f : a.k_scale[unit];
+        sh.st.vs[i] = s == kHidden ? 0.f : a.v_scale[unit];
       }
     }
     __syncthreads();
@@ -468,49 +473,46 @@ uint32_t grid_size(const Cache& c, const Plan& p) {
   return static_cast<uint32_t>((units + 7) / 8 * 8 * p.chunks);
 }
 
-template <int D, int DT, int RT>
+template <int D, int DT, int RT, bool PACKED>
 void launch_rows(const Cache& c, const Args& a, const Plan& p, hipStream_t st) {
   if (p.once)
-    attend_kernel<D, DT, RT, true><<<grid_size(c, p), 256, 0, st>>>(a);
+    attend_kernel<D, DT, RT, true, PACKED><<<grid_size(c, p), 256, 0, st>>>(a);
   else
-    attend_kernel<D, DT, RT, false><<<grid_size(c, p), 256, 0, st>>>(a);
+    attend_kernel<D, DT, RT, false, PACKED><<<grid_size(c, p), 256, 0, st>>>(a);
 }
 
-template <int D, int DT>
+template <int D, int DT, bool PACKED>
 hipError_t launch_dim(const Cache& c, const Args& a, const Plan& p, hipStream_t st) {
   if constexpr (D <= 128) {
     if (group_heads(c, a.share) == 32)
-      launch_rows<D, DT, 2>(c, a, p, st);
+      launch_rows<D, DT, 2, PACKED>(c, a, p, st);
     else
-      launch_rows<D, DT, 1>(c, a, p, st);
+      launch_rows<D, DT, 1, PACKED>(c, a, p, st);
   } else {
-    launch_rows<D, DT, 1>(c, a, p, st);
+    launch_rows<D, DT, 1, PACKED>(c, a, p, st);
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
-  attend_join_kernel<D><<<dim3(a.heads, c.rows), 256, 0, st>>>(a);
+  attend_join_kernel<D, PACKED><<<dim3(a.heads, c.rows), 256, 0, st>>>(a);
   return hipGetLastError();
 }
 
 template <int D>
 hipError_t launch_type(const Cache& c, const Args& a, const Plan& p, hipStream_t st) {
-  return c.dtype == kFP8 ? launch_dim<D, kFP8>(c, a, p, st) : launch_dim<D, kBF16>(c, a, p, st);
+  return c.dtype == kFP8 ? launch_dim<D, kFP8, false>(c, a, p, st) : launch_dim<D, kBF16, false>(c, a, p, st);
 }
 
-}  // namespace
-
-size_t attend_ws_bytes(const Cache& c, int32_t heads, int32_t k) {
-  const Plan p = plan(c, heads, k);
+// Workspace of a plan: the parts' sums.
+size_t parts_bytes(const Cache& c, int32_t heads, const Plan& p) {
   if (p.splits == 1) return 0;
   const size_t parts = static_cast<size_t>(c.rows) * heads * p.splits;
   return align_up(parts * sizeof(float2)) + parts * c.dv * sizeof(float);
 }
 
-hipError_t launch_attend(const Cache& c, int32_t heads, int32_t k, float scale, const void* q,
-                         const void* k_pages, const float* k_scale, const void* v_pages,
-                         const float* v_scale, const int32_t* table, const int32_t* lengths,
-                         const int32_t* idx, void* out, float* lse, void* ws, hipStream_t st) {
-  const Plan p = plan(c, heads, k);
+Args make_args(const Cache& c, int32_t heads, int32_t k, float scale, const Plan& p, const void* q,
+               const void* k_pages, const float* k_scale, const void* v_pages, const float* v_scale,
+               const int32_t* table, const int32_t* lengths, const int32_t* idx, void* out, float* lse,
+               void* ws) {
   Args a{};
   a.q = static_cast<const uint16_t*>(q);
   a.k_pages = static_cast<const uint8_t*>(k_pages);
@@ -536,11 +538,55 @@ hipError_t launch_attend(const Cache& c, int32_t heads, int32_t k, float scale, 
   a.kv_heads = c.kv_heads;
   a.scale2 = scale * kLog2e;
   a.div = make_div(c.P);
+  return a;
+}
+
+// The cache as queries of a packed batch see it: a row each.
+Cache with_rows(const Cache& c, int32_t n) {
+  Cache queries = c;
+  queries.rows = n;
+  return queries;
+}
+
+}  // namespace
+
+size_t attend_ws_bytes(const Cache& c, int32_t heads, int32_t k) {
+  return parts_bytes(c, heads, plan(c, heads, k));
+}
+
+hipError_t launch_attend(const Cache& c, int32_t heads, int32_t k, float scale, const void* q,
+                         const void* k_pages, const float* k_scale, const void* v_pages,
+                         const float* v_scale, const int32_t* table, const int32_t* lengths,
+                         const int32_t* idx, void* out, float* lse, void* ws, hipStream_t st) {
+  const Plan p = plan(c, heads, k);
+  const Args a = make_args(c, heads, k, scale, p, q, k_pages, k_scale, v_pages, v_scale, table,
+                           lengths, idx, out, lse, ws);
   if (c.latent()) return launch_attend_latent(c.dtype, a, grid_size(c, p), st);
   switch (c.dk) {
     case 64: return launch_type<64>(c, a, p, st);
     case 128: return launch_type<128>(c, a, p, st);
     default: return launch_type<256>(c, a, p, st);
+  }
+}
+
+size_t attend_queries_ws_bytes(const Cache& c, const BlockAttend& b) {
+  const Cache queries = with_rows(c, b.n);
+  return parts_bytes(queries, b.heads, plan(queries, b.heads, b.k));
+}
+
+hipError_t launch_attend_queries(const Cache& c, const BlockAttend& b, hipStream_t st) {
+  const Cache queries = with_rows(c, b.n);
+  Plan p = plan(queries, b.heads, b.k);
+  p.once &= b.most <= 1;  // queries of one row share its cache
+  Args a = make_args(queries, b.heads, b.k, b.scale, p, b.q, b.k_pages, b.k_scale, b.v_pages,
+                     b.v_scale, b.table, b.lengths, b.idx, b.out, b.lse, b.ws);
+  a.offsets = b.offsets;
+  a.table_rows = c.rows;
+  a.shift = __builtin_ctz(static_cast<uint32_t>(b.block));
+  switch (c.dk) {
+    case 64: return launch_dim<64, kFP8, true>(queries, a, p, st);
+    case 128: return launch_dim<128, kFP8, true>(queries, a, p, st);
+    default: return launch_dim<256, kFP8, true>(queries, a, p, st);
   }
 }
 

@@ -5,6 +5,7 @@
 #include "common.hpp"
 #include "launch.hpp"
 #include "mfma.hpp"
+#include "packed.hpp"
 
 namespace misa {
 
@@ -53,20 +54,44 @@ struct Args {
   int32_t tiles;  // that a workgroup works on at a time, a power of two
   float scale2;  // scale * log2(e): softmax by powers of two
   Div div;
+  // Queries of a packed batch (misa_block_attend): `rows` above counts queries, and
+  // 2^shift tokens share a scale.
+  const int32_t* offsets;
+  int32_t table_rows, shift;
 };
 
-// Tokens of row `row` to look at, and the pool slot of the t-th of them.
-__device__ __forceinline__ int32_t tokens_of(const Args& a, int row, int32_t& len) {
+// What one query sees: row `table_row` of the table, its first `len` tokens.
+struct Query {
+  int32_t table_row, len;
+};
+
+// Query i; false if no row has it.  PACKED: the new tokens of a row are its last
+// ones, and each sees the tokens up to itself.
+template <bool PACKED>
+__device__ __forceinline__ bool query_of(const Args& a, int i, Query& q) {
   const int32_t cap = a.row_pages * static_cast<int32_t>(a.div.P);
-  len = min(max(a.lengths[row], 0), cap);
-  return a.idx ? (len > 0 ? a.k : 0) : len;
+  if constexpr (PACKED) {
+    int32_t begin, end;
+    if (!row_of_entry(Packed{a.offsets, a.table_rows, a.rows}, i, q.table_row, begin, end)) return false;
+    const int64_t seen = static_cast<int64_t>(a.lengths[q.table_row]) - (end - 1 - i);
+    q.len = static_cast<int32_t>(seen < 0 ? 0 : seen < cap ? seen : cap);
+  } else {
+    q.table_row = i;
+    q.len = min(max(a.lengths[i], 0), cap);
+  }
+  return true;
 }
 
-__device__ __forceinline__ uint32_t slot_of(const Args& a, int row, int kvh, int32_t len, int32_t t) {
+// Tokens that a query looks at, and the pool slot of the t-th of them.
+__device__ __forceinline__ int32_t tokens_of(const Args& a, const Query& q) {
+  return a.idx ? (q.len > 0 ? a.k : 0) : q.len;
+}
+
+__device__ __forceinline__ uint32_t slot_of(const Args& a, int row, int table_row, int kvh, int32_t len, int32_t t) {
   const int32_t s = a.idx ? a.idx[static_cast<int64_t>(row) * a.k + t] : t;
   if (s < 0 || s >= len) return kHidden;
   const uint32_t e = div_page(s, a.div);
-  const int32_t page = a.table[static_cast<int64_t>(row) * a.row_pages + e];
+  const int32_t page = a.table[static_cast<int64_t>(table_row) * a.row_pages + e];
   if (page < 0 || page >= a.pages) return kHidden;
   return (static_cast<uint32_t>(page) * a.kv_heads + kvh) * a.div.P + (s - e * a.div.P);
 }
@@ -134,15 +159,16 @@ __device__ __forceinline__ float final_lse(float m, float l) {
 // for its peers' sums would need an arrival count that is known to start at zero.
 // 32 heads of one row, 16 splits: 3.5 us, a launch and two dependent loads; 32
 // rows of 128 heads of 512 in 4 splits (34 MB) 8.6 us, 3.9 TB/s.
-template <int D>
+template <int D, bool PACKED>
 __global__ __launch_bounds__(256) void attend_join_kernel(Args a) {
   constexpr int T = D / 4, GS = 256 / T;
   __shared__ float4 sums[GS][T];
   __shared__ float total[GS];
   const int head = blockIdx.x, row = blockIdx.y;
   const int d = threadIdx.x % T, grp = threadIdx.x / T;
-  int32_t len;
-  const int32_t todo = tokens_of(a, row, len);
+  Query query;
+  if (!query_of<PACKED>(a, row, query)) return;
+  const int32_t todo = tokens_of(a, query);
   const int32_t per = tiles_per_split(a, todo) * kTileTokens;
   const int32_t n = todo > 0 ? (todo + per - 1) / per : 1;  // split 0 always writes
   const int64_t at = static_cast<int64_t>(row) * a.heads + head;

@@ -1,0 +1,479 @@
+// Attention of several new tokens of a row at a time over the block-scaled cache
+// (misa_block_attend in misa.h): drafts and chunks of prompts.
+#include <algorithm>
+#include <cmath>
+
+#include "attend.hpp"
+
+namespace misa {
+
+namespace {
+
+typedef __attribute__((ext_vector_type(8))) _Float16 f16x8;
+
+constexpr int kRows = 128;  // rows (queries times the query heads of a kv head) of a workgroup
+constexpr float kLift = 7.f;  // weights go up to 2^(kSlack + kLift) < 65504, f16's largest
+constexpr int kNoGroup = -(1 << 30);
+constexpr int kFar = 60, kNear = 8;
+
+struct TileArgs {
+  const uint16_t* q;
+  const uint8_t *k_pages, *v_pages;
+  const float *k_scale, *v_scale;
+  const int32_t* table;
+  const int32_t* lengths;
+  Packed rows;
+  uint16_t* out;
+  float* lse;
+  float* part_o;    // [n, heads, splits, d] sums of a split
+  float2* part_ml;  // [n, heads, splits] maximum (log2) and sum; 0: nothing seen
+  int32_t heads, share, kv_heads, splits, row_pages, pages, shift;
+  uint32_t q_and, q_xor;  // a negative scale turns the queries' signs, a zero one clears them
+  float scale2;           // |scale| * log2(e), above zero
+  Div page, by_share;
+};
+
+// 16 codes -> 16 bf16 (TO16: f16) in two chunks, exact.
+template <bool F16>
+__device__ __forceinline__ void widen(uint4 c, uint4& lo, uint4& hi) {
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+  uint32_t r[8];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if constexpr (F16) {
+      r[2 * j] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[j], 1.f, false));
+      r[2 * j + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[j], 1.f, true));
+    } else {
+      r[2 * j] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[j], 1.f, false));
+      r[2 * j + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[j], 1.f, true));
+    }
+  }
+  lo = make_uint4(r[0], r[1], r[2], r[3]);
+  hi = make_uint4(r[4], r[5], r[6], r[7]);
+}
+
+__device__ __forceinline__ bool nan_code(uint32_t w) {
+  return (((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
+}
+
+__device__ __forceinline__ float halves_max(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float halves_sum(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// One workgroup of four waves per (tile of 128 rows, split, kv head): a wave has 32
+// rows, and all share the tiles of TK tokens in LDS, K widened to bf16 and V to f16
+// as they are staged, one of two buffers while the other is worked on.
+//   S^T = K Q^T, O^T = V^T P^T  (32x32x16), a lane keeps one row (l % 32),
+// so that the softmax is within a lane but for its other half, and P^T's operand is
+// S^T's registers: of 16 tokens, lane half g holds 4g .. 4g+3 and 8+4g .. 8+4g+3,
+// and V's transposing reads give them in that order.
+// Weights are f16 (11 bits), lifted by 2^7 so that what f16 loses is below 2^-31 of
+// the largest; maximum, sums and O are fp32.  V's scale goes into the weights
+// relative to a reference exponent, `eref`, which O's registers are in units of and
+// which follows the blocks' scales when they leave its neighbourhood.
+template <int D, int TK>
+__global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_tiles_kernel(TileArgs a) {
+  constexpr int CH = D / 8;              // 16-byte chunks of a widened row
+  constexpr int CC = D / 16;             // of a row of codes
+  constexpr int NC = TK * CC / 256;      // loads of K, and of V, a thread and tile
+  constexpr int KS = D / 16, NJ = D / 32;
+  constexpr int NH = TK / 32, NG = TK / 16;
+  __shared__ __attribute__((aligned(128))) uint4 kt[2][TK * CH];
+  __shared__ __attribute__((aligned(128))) uint4 vt[2][TK * CH];
+  __shared__ float k_unit[2][NG];
+  __shared__ int v_exp[2][NG];   // kNoGroup: no page there
+  __shared__ int any_nan[2][4];  // in V's codes, by the wave that staged them
+
+  const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int c = lane & 31, g = lane >> 5;
+  const int kvh = blockIdx.x % a.kv_heads;
+  const int rest = blockIdx.x / a.kv_heads;
+  const int split = rest % a.splits;
+  const int64_t units = unit_base(a.rows.n, a.share, kRows, a.rows.rows, 1);
+  const int64_t unit = units - 1 - rest / a.splits;  // the longest rows of a prompt first
+  const int32_t r = last_row(a.rows.rows, unit,
+                             [&](int32_t x) { return unit_base(a.rows.at(x), a.share, kRows, x, 1); });
+  const int32_t begin = a.rows.at(r), count = a.rows.at(r + 1) - begin;
+  const int64_t flat0 = (unit - unit_base(begin, a.share, kRows, r, 1)) * kRows;
+  const int64_t flats = static_cast<int64_t>(max(count, 0)) * a.share;  // below 2^27
+  if (flat0 < 0 || flat0 >= flats) return;
+  const int32_t cap = a.row_pages * static_cast<int32_t>(a.page.P);
+  const int64_t before = static_cast<int64_t>(a.lengths[r]) - count;  // tokens before the new ones
+  const auto seen_by = [&](int32_t t) {
+    const int64_t n = before + t + 1;
+    return static_cast<int32_t>(n < 0 ? 0 : n < cap ? n : cap);
+  };
+  const auto token_of = [&](int32_t flat) { return static_cast<int32_t>(div_page(flat, a.by_share)); };
+  const int32_t last = static_cast<int32_t>(min(flat0 + kRows, flats)) - 1;
+  const int32_t least = seen_by(token_of(static_cast<int32_t>(flat0))), most = seen_by(token_of(last));
+  const int32_t flat = static_cast<int32_t>(flat0) + wave * 32 + c;
+  const bool mine = flat <= last;
+  const int32_t token = token_of(min(flat, last));
+  const int32_t seen = seen_by(token);
+  const int64_t at = static_cast<int64_t>(begin + token) * a.heads + kvh * a.share + (min(flat, last) - token * a.share);
+  const bool busy = static_cast<int32_t>(flat0) + wave * 32 <= last;  // the wave has rows
+
+  const int32_t tiles = (most + TK - 1) / TK, per = (tiles + a.splits - 1) / a.splits;
+  const int32_t t0 = split * per, t1 = min(t0 + per, tiles);
+  if (t0 >= t1) {
+    if (mine && g == 0) {
+      if (a.splits > 1)
+        a.part_ml[at * a.splits + split] = make_float2(-INFINITY, 0.f);
+      else if (a.lse)
+        a.lse[at] = -INFINITY;
+    }
+    if (mine && a.splits == 1)
+      for (int i = 0; i < D / 16; ++i)
+        *reinterpret_cast<uint4*>(a.out + at * D + (2 * i + g) * 8) = make_uint4(0, 0, 0, 0);
+    return;
+  }
+
+  bf16x8 qf[KS];
+#pragma unroll
+  for (int s = 0; s < KS; ++s) {
+    uint4 x = *reinterpret_cast<const uint4*>(a.q + at * D + 16 * s + 8 * g);
+    x.x = (x.x & a.q_and) ^ a.q_xor;
+    x.y = (x.y & a.q_and) ^ a.q_xor;
+    x.z = (x.z & a.q_and) ^ a.q_xor;
+    x.w = (x.w & a.q_and) ^ a.q_xor;
+    qf[s] = as_bf16x8(x);
+  }
+
+  // Staging: thread i has chunk i % CC of tokens i / CC, + 256 / CC, ...; the first
+  // 2 * NG threads the scales of the groups of 16 tokens, which are in one block.
+  const int32_t* table = a.table + static_cast<int64_t>(r) * a.row_pages;
+  const auto page_at = [&](int32_t t) {
+    if (t >= most) return -1;
+    const int32_t p = table[div_page(t, a.page)];
+    return p >= 0 && p < a.pages ? p : -1;
+  };
+  const auto slot_at = [&](int32_t t, int32_t page) {
+    const uint32_t in = static_cast<uint32_t>(t) - div_page(t, a.page) * a.page.P;
+    return (static_cast<uint32_t>(page) * a.kv_heads + kvh) * a.page.P + in;
+  };
+  int32_t pages[NC], group_page = -1;
+  uint4 kc[NC], vc[NC];
+  float group_unit = 0.f;  // 0: no page there
+  const int my_token = threadIdx.x / CC, my_chunk = threadIdx.x % CC, my_group = threadIdx.x % NG;
+  const bool scales = threadIdx.x < 2 * NG;
+  const auto find = [&](int32_t tile) {
+#pragma unroll
+    for (int i = 0; i < NC; ++i) pages[i] = page_at(tile * TK + my_token + i * (256 / CC));
+    if (scales) group_page = page_at(tile * TK + my_group * 16);
+  };
+  const auto load = [&](int32_t tile) {
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int32_t t = tile * TK + my_token + i * (256 / CC);
+      kc[i] = vc[i] = make_uint4(0, 0, 0, 0);
+      if (pages[i] >= 0) {
+        const uint64_t from = static_cast<uint64_t>(slot_at(t, pages[i])) * D + my_chunk * 16;
+        kc[i] = *reinterpret_cast<const uint4*>(a.k_pages + from);
+        vc[i] = *reinterpret_cast<const uint4*>(a.v_pages + from);
+      }
+    }
+    if (scales) {
+      group_unit = 0.f;
+      if (group_page >= 0)
+        group_unit = (threadIdx.x < NG ? a.k_scale : a.v_scale)[slot_at(tile * TK + my_group * 16, group_page) >> a.shift];
+    }
+  };
+  // Swizzles of the chunks, so that 16 rows' reads of a chunk (K) and four rows' of
+  // 64 bytes (V) are in different banks.
+  const auto k_at = [](int row, int chunk) { return row * CH + (chunk ^ (D == 64 ? row >> 1 & 7 : row & 15)); };
+  const auto v_at = [](int row, int chunk) { return row * CH + (chunk ^ (D == 64 ? (row >> 1 & 1) << 2 : (row & 3) << 2)); };
+  const auto stage = [&](int32_t tile, int b) {
+    bool nan = false;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int row = my_token + i * (256 / CC);
+      uint4 lo, hi;
+      widen<false>(kc[i], lo, hi);
+      kt[b][k_at(row, 2 * my_chunk)] = lo;
+      kt[b][k_at(row, 2 * my_chunk + 1)] = hi;
+      widen<true>(vc[i], lo, hi);
+      vt[b][v_at(row, 2 * my_chunk)] = lo;
+      vt[b][v_at(row, 2 * my_chunk + 1)] = hi;
+      nan |= nan_code(vc[i].x) || nan_code(vc[i].y) || nan_code(vc[i].z) || nan_code(vc[i].w);
+    }
+    if ((tile + 1) * TK > least) {  // only a tile that hides tokens asks
+      const bool any = __any(nan);
+      if (lane == 0) any_nan[b][wave] = any;
+    }
+    if (threadIdx.x < NG)
+      k_unit[b][my_group] = group_unit;
+    else if (scales)
+      v_exp[b][my_group] = group_unit == 0.f ? kNoGroup : static_cast<int>(__float_as_uint(group_unit) >> 23) - 127;
+  };
+
+  f32x16 acc[NJ];
+#pragma unroll
+  for (int j = 0; j < NJ; ++j)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) acc[j][e] = 0.f;
+  float m = -INFINITY, l = 0.f;  // of this lane's row, and of its half of the tokens
+  int eref = kNoGroup, loudest = kNoGroup;
+  const int vrow = 4 * g + (lane & 15) / 4, vcol = 2 * (lane >> 4 & 1) + (lane & 3) / 2;  // transposing reads
+
+  const auto compute = [&](int32_t tile, int b) {
+    f32x16 st[NH];
+#pragma unroll
+    for (int h = 0; h < NH; ++h) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) st[h][e] = 0.f;
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+        st[h] = mfma32_bf16(as_bf16x8(kt[b][k_at(32 * h + c, 2 * s + g)]), qf[s], st[h]);
+    }
+    float unit_k[NG];
+    int unit_v[NG];
+    bool hides = (tile + 1) * TK > least;
+#pragma unroll
+    for (int i = 0; i < NG; ++i) {
+      unit_k[i] = fmaxf(__uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(k_unit[b][i]))) * a.scale2, 1e-44f);
+      unit_v[i] = __builtin_amdgcn_readfirstlane(v_exp[b][i]);
+      hides |= unit_v[i] == kNoGroup;
+    }
+    const auto place = [&](int h, int e) { return tile * TK + 32 * h + 8 * (e / 4) + 4 * g + e % 4; };
+    if (hides) {
+#pragma unroll
+      for (int h = 0; h < NH; ++h)
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          st[h][e] = place(h, e) < seen && unit_v[2 * h + e / 8] != kNoGroup ? st[h][e] : -INFINITY;
+    }
+    float high = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < NG; ++i) {
+      float x = st[i / 2][i % 2 * 8];
+#pragma unroll
+      for (int e = 1; e < 8; ++e) x = fmaxf(x, st[i / 2][i % 2 * 8 + e]);
+      high = fmaxf(high, x * unit_k[i]);
+    }
+    if (__any(high > m + kSlack)) {
+      const float next = fmaxf(m, halves_max(high));
+      const float f = next == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - next);
+      m = next;
+      l *= f;
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) acc[j] *= f;
+    }
+    const float mb = m == -INFINITY ? 0.f : m;
+    bool nan = false;
+    if (hides && (tile + 1) * TK > least)
+      nan = __builtin_amdgcn_readfirstlane(any_nan[b][0] | any_nan[b][1] | any_nan[b][2] | any_nan[b][3]) != 0;
+#pragma unroll
+    for (int i = 0; i < NG; ++i) {
+      int e = unit_v[i];
+      if (e == kNoGroup) e = eref;  // its weights are zero
+      if (e > eref || e < eref - kNear) {
+        loudest = max(loudest, e);
+        const int next = max(e, loudest - kFar);
+        const float f = __builtin_amdgcn_ldexpf(1.f, max(eref - next, -200));
+        eref = next;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) acc[j] *= f;
+      }
+      // Far below the reference a block's values no longer count, but its weights do.
+      const float lift = kLift + static_cast<float>(max(e - eref, -100));
+      const float base = lift - mb;
+      f16x8 w;
+      float sum = 0.f;
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(st[i / 2][i % 2 * 8 + x], unit_k[i], base));
+        sum += p;
+        w[x] = static_cast<_Float16>(p);
+      }
+      l += sum * __builtin_amdgcn_exp2f(-lift);
+      f16x8 shown;  // 1 where the row sees the token
+      if (nan) {
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+          shown[x] = place(i / 2, i % 2 * 8 + x) < seen ? static_cast<_Float16>(1.f) : static_cast<_Float16>(0.f);
+      }
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        const auto part = [&](int row) {
+          const uint8_t* p = reinterpret_cast<const uint8_t*>(&vt[b][v_at(row, 4 * j + vcol)]) + (lane & 1) * 8;
+          return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)p);
+        };
+        const s16x4 y0 = part(16 * i + vrow), y1 = part(16 * i + 8 + vrow);
+        f16x8 v = __builtin_bit_cast(f16x8, __builtin_shufflevector(y0, y1, 0, 1, 2, 3, 4, 5, 6, 7));
+        if (nan) {  // NaN values reach the rows that see them, and no others
+          f16x8 bad;
+          f32x16 hits;
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            const bool is = v[x] != v[x];
+            bad[x] = is ? static_cast<_Float16>(1.f) : static_cast<_Float16>(0.f);
+            v[x] = is ? static_cast<_Float16>(0.f) : v[x];
+          }
+#pragma unroll
+          for (int y = 0; y < 16; ++y) hits[y] = 0.f;
+          hits = __builtin_amdgcn_mfma_f32_32x32x16_f16(bad, shown, hits, 0, 0, 0);
+#pragma unroll
+          for (int y = 0; y < 16; ++y) acc[j][y] = hits[y] > 0.f ? NAN : acc[j][y];
+        }
+        acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, w, acc[j], 0, 0, 0);
+      }
+    }
+  };
+
+  find(t0);
+  load(t0);
+  stage(t0, 0);
+  if (t0 + 1 < t1) {
+    find(t0 + 1);
+    load(t0 + 1);
+  }
+  for (int32_t tile = t0; tile < t1; ++tile) {
+    const int b = (tile - t0) & 1;
+    __syncthreads();
+    if (tile + 2 < t1) find(tile + 2);
+    if (busy) compute(tile, b);
+    if (tile + 1 < t1) stage(tile + 1, b ^ 1);
+    if (tile + 2 < t1) load(tile + 2);
+  }
+
+  l = halves_sum(l);
+  if (!mine) return;
+  const float unit_o = __builtin_amdgcn_ldexpf(1.f, max(eref, -200) - static_cast<int>(kLift));
+  const int64_t part = at * a.splits + split;
+  if (g == 0) {
+    if (a.splits > 1)
+      a.part_ml[part] = make_float2(m, l);
+    else if (a.lse)
+      a.lse[at] = l == 0.f ? -INFINITY : final_lse(m, l);
+  }
+  const float f = a.splits > 1 ? unit_o : l == 0.f ? 0.f : unit_o / l;
+#pragma unroll
+  for (int j = 0; j < NJ; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int d = 32 * j + 8 * e + 4 * g;
+      const float4 o = make_float4(acc[j][4 * e] * f, acc[j][4 * e + 1] * f, acc[j][4 * e + 2] * f, acc[j][4 * e + 3] * f);
+      if (a.splits > 1) {
+        *reinterpret_cast<float4*>(a.part_o + part * D + d) = o;
+      } else {
+        bf16x2 x, y;
+        x[0] = static_cast<__bf16>(o.x);
+        x[1] = static_cast<__bf16>(o.y);
+        y[0] = static_cast<__bf16>(o.z);
+        y[1] = static_cast<__bf16>(o.w);
+        *reinterpret_cast<uint2*>(a.out + at * D + d) =
+            make_uint2(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, y));
+      }
+    }
+}
+
+// The splits of a query's heads joined: D / 4 threads a head, 1024 / D heads a
+// workgroup.
+template <int D>
+__global__ __launch_bounds__(256) void join_tiles_kernel(TileArgs a) {
+  constexpr int T = D / 4;
+  const int32_t i = blockIdx.x;
+  int32_t r, begin, end;
+  if (!row_of_entry(a.rows, i, r, begin, end)) return;
+  const int head = blockIdx.y * (256 / T) + threadIdx.x / T, d = threadIdx.x % T * 4;
+  if (head >= a.heads) return;
+  const int64_t at = static_cast<int64_t>(i) * a.heads + head;
+  const float2* ml = a.part_ml + at * a.splits;
+  float m = -INFINITY, l = 0.f;
+  for (int s = 0; s < a.splits; ++s) m = fmaxf(m, ml[s].x);
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s = 0; s < a.splits; ++s) {
+    const float2 x = ml[s];
+    if (x.y == 0.f) continue;  // nothing seen, nothing written
+    const float4 y = *reinterpret_cast<const float4*>(a.part_o + (at * a.splits + s) * D + d);
+    const float f = part_factor(x.x, x.y, m);
+    l += x.y * f;
+    o.x += y.x * f;
+    o.y += y.y * f;
+    o.z += y.z * f;
+    o.w += y.w * f;
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  if (d == 0 && a.lse) a.lse[at] = l == 0.f ? -INFINITY : final_lse(m, l);
+  bf16x2 x, y;
+  x[0] = static_cast<__bf16>(o.x * inv);
+  x[1] = static_cast<__bf16>(o.y * inv);
+  y[0] = static_cast<__bf16>(o.z * inv);
+  y[1] = static_cast<__bf16>(o.w * inv);
+  *reinterpret_cast<uint2*>(a.out + at * D + d) =
+      make_uint2(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, y));
+}
+
+constexpr int kSlots = 512;  // workgroups that the card holds at a time
+constexpr int kMaxParts = 32;
+
+int64_t tile_units(const Cache& c, const BlockAttend& b) {
+  return unit_base(b.n, b.heads / c.kv_heads, kRows, c.rows, 1);
+}
+
+int32_t tile_splits(const Cache& c, const BlockAttend& b) {
+  const int64_t groups = tile_units(c, b) * c.kv_heads;
+  const int64_t longest = (static_cast<int64_t>(c.row_pages) * c.P + 255) / 256;  // four tiles a split
+  return static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>({kSlots / groups, longest, kMaxParts})));
+}
+
+template <int D, int TK>
+hipError_t launch_tiles_dim(const TileArgs& a, uint32_t grid, hipStream_t st) {
+  attend_tiles_kernel<D, TK><<<grid, 256, 0, st>>>(a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.splits == 1) return e;
+  const int per = 1024 / D;
+  join_tiles_kernel<D><<<dim3(a.rows.n, (a.heads + per - 1) / per), 256, 0, st>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t attend_tiles_ws_bytes(const Cache& c, const BlockAttend& b) {
+  const int32_t splits = tile_splits(c, b);
+  if (splits == 1) return 0;
+  const size_t parts = static_cast<size_t>(b.n) * b.heads * splits;
+  return align_up(parts * sizeof(float2)) + parts * c.dv * sizeof(float);
+}
+
+hipError_t launch_attend_tiles(const Cache& c, const BlockAttend& b, hipStream_t st) {
+  TileArgs a{};
+  a.q = static_cast<const uint16_t*>(b.q);
+  a.k_pages = static_cast<const uint8_t*>(b.k_pages);
+  a.v_pages = static_cast<const uint8_t*>(b.v_pages);
+  a.k_scale = b.k_scale;
+  a.v_scale = b.v_scale;
+  a.table = b.table;
+  a.lengths = b.lengths;
+  a.rows = Packed{b.offsets, c.rows, b.n};
+  a.out = static_cast<uint16_t*>(b.out);
+  a.lse = b.lse;
+  a.heads = b.heads;
+  a.share = b.heads / c.kv_heads;
+  a.kv_heads = c.kv_heads;
+  a.splits = tile_splits(c, b);
+  const size_t parts = static_cast<size_t>(b.n) * b.heads * a.splits;
+  a.part_ml = static_cast<float2*>(b.ws);
+  a.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(b.ws) + align_up(parts * sizeof(float2)));
+  a.row_pages = c.row_pages;
+  a.pages = c.pages;
+  a.shift = __builtin_ctz(static_cast<uint32_t>(b.block));
+  a.q_and = b.scale == 0.f ? 0u : 0xFFFFFFFFu;
+  a.q_xor = b.scale < 0.f ? 0x80008000u : 0u;
+  a.scale2 = b.scale == 0.f ? 1.f : std::fabs(b.scale) * kLog2e;
+  a.page = make_div(c.P);
+  a.by_share = make_div(a.share);
+  const uint32_t grid = static_cast<uint32_t>(tile_units(c, b) * c.kv_heads * a.splits);
+  switch (c.dk) {
+    case 64: return launch_tiles_dim<64, 64>(a, grid, st);
+    case 128: return launch_tiles_dim<128, 64>(a, grid, st);
+    default: return launch_tiles_dim<256, 32>(a, grid, st);
+  }
+}
+
+}  // namespace misa

@@ -144,8 +144,10 @@ __global__ __launch_bounds__(512) void attend_latent_kernel(Args a) {
   const int row = unit / a.splits, split = unit - row * a.splits;
   if (row >= a.rows) return;
   const int head0 = chunk * kLatentHeads + hw * 16;
-  int32_t len;
-  const int32_t todo = tokens_of(a, row, len);
+  Query own;
+  query_of<false>(a, row, own);
+  const int32_t len = own.len;
+  const int32_t todo = tokens_of(a, own);
   const int32_t per = tiles_per_split(a, todo) * kTileTokens;
   const int32_t t0 = split * per, t1 = min(t0 + per, todo);
   if (t0 >= t1 && split > 0) return;
@@ -235,7 +237,7 @@ __global__ __launch_bounds__(512) void attend_latent_kernel(Args a) {
   }
   auto fill = [&](int32_t base) {  // slots (and scales) of the stage at `base`: one per thread
     const int32_t i = threadIdx.x, count = min(kLatentStage, t1 - base);
-    const uint32_t s = i < count ? slot_of(a, row, 0, len, base + i) : kHidden;
+    const uint32_t s = i < count ? slot_of(a, row, row, 0, len, base + i) : kHidden;
     slots[i] = s;
     if constexpr (kFp8) scales[i] = s == kHidden ? 0.f : a.k_scale[s];
   };
@@ -397,7 +399,7 @@ hipError_t launch_attend_latent(int32_t dtype, const Args& a, uint32_t grid, hip
     attend_latent_kernel<kBF16><<<grid, 512, 0, st>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
-  attend_join_kernel<kLatentV><<<dim3(a.heads, a.rows), 256, 0, st>>>(a);
+  attend_join_kernel<kLatentV, false><<<dim3(a.heads, a.rows), 256, 0, st>>>(a);
   return hipGetLastError();
 }
 

@@ -1,0 +1,342 @@
+// The cache with one scale per block of tokens and head (misa_block_write and
+// misa_block_read in misa.h).  Every id read from device memory (rows' ranges,
+// lengths, pages) is range-checked before it becomes an address.
+#include <algorithm>
+
+#include "common.hpp"
+#include "launch.hpp"
+#include "packed.hpp"
+#include "quant.hpp"
+
+namespace misa {
+
+namespace {
+
+constexpr int kLeastScale = -100;  // exponent of the scale of a block of zeros
+
+// The smallest 2^k, k >= -100, with amax <= 448 * 2^k = 1.75 * 2^(8 + k), for a
+// finite amax >= 0.
+__device__ __forceinline__ float block_scale(float amax) {
+  const uint32_t u = __float_as_uint(amax);
+  const int e = static_cast<int>(u >> 23) - 127;
+  const int k = e - 8 + ((u & 0x7FFFFFu) > 0x600000u);
+  return __uint_as_float(static_cast<uint32_t>(max(k, kLeastScale) + 127) << 23);
+}
+
+struct WriteArgs {
+  Packed rows;
+  const int32_t* lengths;
+  const uint16_t* fresh[2];  // k_new, v_new
+  uint8_t* pages_of[2];
+  float* scale[2];
+  const int32_t* table;
+  int32_t row_pages, pages, P, kv_heads, B;
+  int32_t by_token;  // units are packed entries, not blocks
+};
+
+// One workgroup per (block with new tokens, kv head, keys or values): D / 8 lanes
+// hold eight values each of a token, and NP rounds of tokens a block, so that the
+// block's values are read once, before its scale is known, and stay in registers.
+//
+// Units go by blocks (a row's c tokens touch at most floor(c / B) + 2) or, where
+// there are fewer of them, by tokens: the first of a row and those that begin a
+// block are at work, the other workgroups leave (32 rows with a token each: 32
+// units for 64).
+template <int D, int NP>
+__global__ __launch_bounds__(256) void block_write_kernel(WriteArgs a) {
+  constexpr int LPR = D / 8, TP = 256 / LPR;  // lanes of a token, tokens of a round
+  __shared__ float tops[4];
+  const int which = blockIdx.z, head = blockIdx.y;
+  int32_t r, begin, end;
+  int64_t block;  // of the row
+  const int64_t u = blockIdx.x;
+  if (a.by_token) {
+    if (!row_of_entry(a.rows, static_cast<int32_t>(u), r, begin, end)) return;
+  } else {
+    r = last_row(a.rows.rows, u, [&](int32_t x) { return unit_base(a.rows.at(x), 1, a.B, x, 2); });
+    begin = a.rows.at(r);
+    end = a.rows.at(r + 1);
+    if (begin >= end) return;
+  }
+  const int64_t stop = a.lengths[r], start = stop - (end - begin);  // positions of the new tokens
+  const int64_t from = start > 0 ? start : 0;
+  if (a.by_token) {
+    const int64_t p = start + (u - begin);
+    if (p < from || (p != from && p % a.B != 0)) return;
+    block = p / a.B;
+  } else {
+    const int64_t j = u - unit_base(begin, 1, a.B, r, 2);
+    if (j < 0) return;
+    block = from / a.B + j;
+  }
+  const int64_t p0 = block * a.B;  // the block's first position
+  if (p0 >= stop || p0 >= static_cast<int64_t>(a.row_pages) * a.P) return;
+  const int32_t e = static_cast<int32_t>(p0 / a.P);
+  const int32_t page = a.table[static_cast<int64_t>(r) * a.row_pages + e];
+  if (page < 0 || page >= a.pages) return;
+  const int64_t slot0 = (static_cast<int64_t>(page) * a.kv_heads + head) * a.P + (p0 - static_cast<int64_t>(e) * a.P);
+  const int32_t low = static_cast<int32_t>(from > p0 ? from - p0 : 0);            // first new token
+  const int32_t high = static_cast<int32_t>(stop - p0 < a.B ? stop - p0 : a.B);  // one past the last
+  const int lane = threadIdx.x % LPR, tok = threadIdx.x / LPR;
+
+  const uint16_t* src = a.fresh[which];
+  const int64_t entry0 = begin + (p0 - start);  // packed entry of the block's first token
+  uint4 x[NP];
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    const int32_t t = i * TP + tok;
+    x[i] = make_uint4(0, 0, 0, 0);
+    if (t >= low && t < high)
+      x[i] = *reinterpret_cast<const uint4*>(src + ((entry0 + t) * a.kv_heads + head) * D + lane * 8);
+  }
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float y0 = fabsf(__uint_as_float(w[j] << 16)), y1 = fabsf(__uint_as_float(w[j] & 0xFFFF0000u));
+      top = fmaxf(top, y0 < INFINITY ? y0 : 0.f);
+      top = fmaxf(top, y1 < INFINITY ? y1 : 0.f);
+    }
+  }
+  top = lanes_reduce<kWave, true>(top);
+  if (lane_id() == 0) tops[threadIdx.x / kWave] = top;
+  float* scale = a.scale[which] + slot0 / a.B;
+  const float had = low > 0 ? *scale : 0.f;
+  __syncthreads();
+  float unit = block_scale(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])));
+  const bool grown = low > 0 && had < unit;
+  if (low > 0 && had > unit) unit = had;
+  const float inv = 1.f / unit;  // exact
+  uint8_t* dst = a.pages_of[which] + slot0 * D + lane * 8;
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    const int32_t t = i * TP + tok;
+    if (t >= low && t < high) {
+      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+      float y[8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        y[2 * j] = __uint_as_float(w[j] << 16);
+        y[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] = fabsf(y[j]) < INFINITY ? y[j] : NAN;
+      *reinterpret_cast<uint2*>(dst + static_cast<int64_t>(t) * D) =
+          make_uint2(e4m3_pack4(y[0], y[1], y[2], y[3], inv), e4m3_pack4(y[4], y[5], y[6], y[7], inv));
+    }
+    if (grown && t < low) {  // earlier tokens, to the larger scale
+      uint2* old = reinterpret_cast<uint2*>(dst + static_cast<int64_t>(t) * D);
+      const uint2 z = *old;
+      const float f = had * inv;
+      uint32_t c[2] = {z.x, z.y};
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        c[j] = e4m3_pack4(fp8_to_f32(c[j]), __builtin_amdgcn_cvt_f32_fp8(c[j], 1),
+                          __builtin_amdgcn_cvt_f32_fp8(c[j], 2), __builtin_amdgcn_cvt_f32_fp8(c[j], 3), f);
+      *old = make_uint2(c[0], c[1]);
+    }
+  }
+  if (threadIdx.x == 0) *scale = unit;
+}
+
+template <int D>
+hipError_t launch_write_dim(const WriteArgs& a, uint32_t units, int32_t parts, hipStream_t st) {
+  const dim3 grid(units, a.kv_heads, parts);
+  const int rounds = std::max(1, a.B * (D / 8) / 256);
+  if (rounds == 1) block_write_kernel<D, 1><<<grid, 256, 0, st>>>(a);
+  if (rounds == 2) block_write_kernel<D, 2><<<grid, 256, 0, st>>>(a);
+  if (rounds == 4) block_write_kernel<D, 4><<<grid, 256, 0, st>>>(a);
+  if constexpr (D >= 128)
+    if (rounds == 8) block_write_kernel<D, 8><<<grid, 256, 0, st>>>(a);
+  if constexpr (D >= 256)
+    if (rounds == 16) block_write_kernel<D, 16><<<grid, 256, 0, st>>>(a);
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------- reading back
+
+struct ReadArgs {
+  Packed rows;
+  const int32_t *first, *lengths, *table;
+  const uint8_t* pages_of[2];
+  const float* scale[2];
+  void* out[2];
+  float* out_scale[2];
+  int32_t row_pages, pages, P, kv_heads, B;
+};
+
+// 16 codes -> 16 values of OUT at `dst`.
+template <int OUT>
+__device__ __forceinline__ void put16(void* dst, int64_t at, uint4 c, float scale) {
+  if constexpr (OUT == kFP8) {
+    *reinterpret_cast<uint4*>(static_cast<uint8_t*>(dst) + at) = c;
+  } else {
+    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+    float y[16];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      y[4 * j] = fp8_to_f32(w[j]) * scale;
+      y[4 * j + 1] = __builtin_amdgcn_cvt_f32_fp8(w[j], 1) * scale;
+      y[4 * j + 2] = __builtin_amdgcn_cvt_f32_fp8(w[j], 2) * scale;
+      y[4 * j + 3] = __builtin_amdgcn_cvt_f32_fp8(w[j], 3) * scale;
+    }
+    if constexpr (OUT == kF32) {
+      float4* o = reinterpret_cast<float4*>(static_cast<float*>(dst) + at);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[j] = make_float4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
+    } else {
+      typedef __attribute__((ext_vector_type(8))) __bf16 B8;
+      B8 lo, hi;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        lo[j] = static_cast<__bf16>(y[j]);
+        hi[j] = static_cast<__bf16>(y[8 + j]);
+      }
+      uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(dst) + at);
+      o[0] = __builtin_bit_cast(uint4, lo);
+      o[1] = __builtin_bit_cast(uint4, hi);
+    }
+  }
+}
+
+constexpr int kReadRounds = 4;
+
+// D / 16 lanes per (packed token, kv head), 16 codes each, and four of those a
+// lane, whose loads are under way together.
+template <int D, int OUT>
+__global__ __launch_bounds__(256) void block_read_kernel(ReadArgs a) {
+  constexpr int LPR = D / 16, IP = 256 / LPR;  // lanes of an item, items of a round
+  const int which = blockIdx.y;
+  const int lane = threadIdx.x % LPR;
+  const int64_t items = static_cast<int64_t>(a.rows.n) * a.kv_heads;
+  const int64_t item0 = static_cast<int64_t>(blockIdx.x) * (IP * kReadRounds);
+  // The rows of the workgroup's first and last token; mostly the same.
+  const int32_t t0 = static_cast<int32_t>(item0 / a.kv_heads);
+  const int32_t t1 = static_cast<int32_t>((min(item0 + IP * kReadRounds, items) - 1) / a.kv_heads);
+  const auto offset = [&](int32_t x) { return static_cast<int64_t>(a.rows.at(x)); };
+  const int32_t r0 = last_row(a.rows.rows, t0, offset);
+  int32_t r1 = r0;
+  if (a.rows.at(r0 + 1) <= t1) r1 = last_row(a.rows.rows, t1, offset);
+  uint4 code[kReadRounds];
+  float unit[kReadRounds];
+  int64_t item[kReadRounds];
+#pragma unroll
+  for (int i = 0; i < kReadRounds; ++i) {
+    item[i] = item0 + i * IP + threadIdx.x / LPR;
+    code[i] = make_uint4(0, 0, 0, 0);
+    unit[i] = 1.f;
+    if (item[i] >= items) {
+      item[i] = -1;
+      continue;
+    }
+    const int32_t t = static_cast<int32_t>(static_cast<uint32_t>(item[i]) / static_cast<uint32_t>(a.kv_heads));
+    const int32_t head = static_cast<int32_t>(item[i] - static_cast<int64_t>(t) * a.kv_heads);
+    int32_t lo = r0, hi = r1;  // the last row whose entries begin at or before t
+    while (lo < hi) {
+      const int32_t mid = lo + (hi - lo + 1) / 2;
+      if (a.rows.at(mid) <= t)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    const int32_t begin = a.rows.at(lo);
+    if (t < begin || t >= a.rows.at(lo + 1)) {  // padding
+      item[i] = -1;
+      continue;
+    }
+    const int64_t p = static_cast<int64_t>(a.first ? a.first[lo] : 0) + (t - begin);
+    if (p < 0 || p >= a.lengths[lo] || p >= static_cast<int64_t>(a.row_pages) * a.P) continue;
+    const uint32_t e = static_cast<uint32_t>(p) / static_cast<uint32_t>(a.P);
+    const int32_t page = a.table[static_cast<int64_t>(lo) * a.row_pages + e];
+    if (page < 0 || page >= a.pages) continue;
+    const int64_t slot = (static_cast<int64_t>(page) * a.kv_heads + head) * a.P + (p - static_cast<int64_t>(e) * a.P);
+    code[i] = *reinterpret_cast<const uint4*>(a.pages_of[which] + slot * D + lane * 16);
+    unit[i] = a.scale[which][static_cast<uint32_t>(slot) / static_cast<uint32_t>(a.B)];
+  }
+#pragma unroll
+  for (int i = 0; i < kReadRounds; ++i) {
+    if (item[i] < 0) continue;
+    put16<OUT>(a.out[which], item[i] * D + lane * 16, code[i], unit[i]);
+    if (OUT == kFP8 && lane == 0) a.out_scale[which][item[i]] = unit[i];
+  }
+}
+
+template <int D>
+hipError_t launch_read_dim(const ReadArgs& a, int32_t out_dtype, int32_t parts, hipStream_t st) {
+  const int64_t items = static_cast<int64_t>(a.rows.n) * a.kv_heads;  // at most 2^28
+  const int per = 256 / (D / 16) * kReadRounds;
+  const dim3 grid(static_cast<uint32_t>((items + per - 1) / per), parts);
+  switch (out_dtype) {
+    case kF32: block_read_kernel<D, kF32><<<grid, 256, 0, st>>>(a); break;
+    case kBF16: block_read_kernel<D, kBF16><<<grid, 256, 0, st>>>(a); break;
+    default: block_read_kernel<D, kFP8><<<grid, 256, 0, st>>>(a); break;
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_block_write(const Cache& c, int32_t block, int32_t n, const int32_t* offsets,
+                              const int32_t* lengths, const void* k_new, const void* v_new,
+                              void* k_pages, float* k_scale, void* v_pages, float* v_scale,
+                              const int32_t* table, hipStream_t st) {
+  WriteArgs a{};
+  a.rows = Packed{offsets, c.rows, n};
+  a.lengths = lengths;
+  a.fresh[0] = static_cast<const uint16_t*>(k_new);
+  a.fresh[1] = static_cast<const uint16_t*>(v_new);
+  a.pages_of[0] = static_cast<uint8_t*>(k_pages);
+  a.pages_of[1] = static_cast<uint8_t*>(v_pages);
+  a.scale[0] = k_scale;
+  a.scale[1] = v_scale;
+  a.table = table;
+  a.row_pages = c.row_pages;
+  a.pages = c.pages;
+  a.P = c.P;
+  a.kv_heads = c.kv_heads;
+  a.B = block;
+  const int64_t blocks = unit_base(n, 1, block, c.rows, 2);
+  a.by_token = n <= blocks;
+  const uint32_t units = static_cast<uint32_t>(a.by_token ? n : blocks);
+  const int32_t parts = v_pages ? 2 : 1;
+  switch (c.dk) {
+    case 64: return launch_write_dim<64>(a, units, parts, st);
+    case 128: return launch_write_dim<128>(a, units, parts, st);
+    default: return launch_write_dim<256>(a, units, parts, st);
+  }
+}
+
+hipError_t launch_block_read(const Cache& c, int32_t block, int32_t n, int32_t out_dtype,
+                             const int32_t* offsets, const int32_t* first, const int32_t* lengths,
+                             const void* k_pages, const float* k_scale, const void* v_pages,
+                             const float* v_scale, const int32_t* table, void* k_out,
+                             float* k_out_scale, void* v_out, float* v_out_scale, hipStream_t st) {
+  ReadArgs a{};
+  a.rows = Packed{offsets, c.rows, n};
+  a.first = first;
+  a.lengths = lengths;
+  a.table = table;
+  a.pages_of[0] = static_cast<const uint8_t*>(k_pages);
+  a.pages_of[1] = static_cast<const uint8_t*>(v_pages);
+  a.scale[0] = k_scale;
+  a.scale[1] = v_scale;
+  a.out[0] = k_out;
+  a.out[1] = v_out;
+  a.out_scale[0] = k_out_scale;
+  a.out_scale[1] = v_out_scale;
+  a.row_pages = c.row_pages;
+  a.pages = c.pages;
+  a.P = c.P;
+  a.kv_heads = c.kv_heads;
+  a.B = block;
+  const int32_t parts = v_pages ? 2 : 1;
+  switch (c.dk) {
+    case 64: return launch_read_dim<64>(a, out_dtype, parts, st);
+    case 128: return launch_read_dim<128>(a, out_dtype, parts, st);
+    default: return launch_read_dim<256>(a, out_dtype, parts, st);
+  }
+}
+
+}  // namespace misa

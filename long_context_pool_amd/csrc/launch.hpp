@@ -171,6 +171,47 @@ hipError_t launch_rms_norm(int32_t rows, int32_t n, int32_t groups, int32_t x_dt
                            const float* weight, void* sum_out, void* out, float* out_scale,
                            hipStream_t st);
 
+// ------------------------------------------------- block-scaled cache, rotary positions
+
+// Packed batches (offsets [rows + 1]); block: tokens that share a scale.
+hipError_t launch_block_write(const Cache& c, int32_t block, int32_t n, const int32_t* offsets,
+                              const int32_t* lengths, const void* k_new, const void* v_new,
+                              void* k_pages, float* k_scale, void* v_pages, float* v_scale,
+                              const int32_t* table, hipStream_t st);
+hipError_t launch_block_read(const Cache& c, int32_t block, int32_t n, int32_t out_dtype,
+                             const int32_t* offsets, const int32_t* first, const int32_t* lengths,
+                             const void* k_pages, const float* k_scale, const void* v_pages,
+                             const float* v_scale, const int32_t* table, void* k_out,
+                             float* k_out_scale, void* v_out, float* v_out_scale, hipStream_t st);
+
+struct BlockAttend {  // the arguments of misa_block_attend
+  int32_t block, heads, n, most, k;
+  float scale;
+  const int32_t* offsets;
+  const void *q, *k_pages;
+  const float* k_scale;
+  const void* v_pages;
+  const float* v_scale;
+  const int32_t *table, *lengths, *idx;
+  void* out;
+  float* lse;
+  void* ws;
+};
+// One query at a time (attend.hip), or tiles of a row's queries (attend_block.hip).
+size_t attend_queries_ws_bytes(const Cache& c, const BlockAttend& b);
+hipError_t launch_attend_queries(const Cache& c, const BlockAttend& b, hipStream_t st);
+size_t attend_tiles_ws_bytes(const Cache& c, const BlockAttend& b);
+hipError_t launch_attend_tiles(const Cache& c, const BlockAttend& b, hipStream_t st);
+
+constexpr int32_t kMaxRopeRow = 32768, kMaxRot = 1024;
+struct Rope {
+  int32_t heads, d, first, rot, pairs, x_dtype, out_dtype;
+  float amplitude;
+  int64_t x_stride, out_stride;
+};
+hipError_t launch_rope(const Rope& r, int32_t n, const void* x, const int32_t* pos,
+                       const double* freq, void* out, float* out_scale, hipStream_t st);
+
 inline size_t align_up(size_t x, size_t a = 256) { return (x + a - 1) / a * a; }
 
 // The fixed device scratch of the no-allocation decode step: its size, and
