@@ -4,6 +4,7 @@
 #include <cmath>
 
 #include "attend.hpp"
+#include "quant.hpp"
 
 namespace misa {
 
@@ -15,6 +16,7 @@ constexpr int kRows = 128;  // rows (queries times the query heads of a kv head)
 constexpr float kLift = 7.f;  // weights go up to 2^(kSlack + kLift) < 65504, f16's largest
 constexpr int kNoGroup = -(1 << 30);
 constexpr int kFar = 60, kNear = 8;
+constexpr int kGroups = 128;  // groups of 16 tokens that are looked up at a time
 
 struct TileArgs {
   const uint16_t* q;
@@ -33,33 +35,35 @@ struct TileArgs {
   Div page, by_share;
 };
 
-// 16 codes -> 16 bf16 (TO16: f16) in two chunks, exact.
+// 16 codes -> 16 bf16 (F16: f16) times a power of two, in two chunks, exact.
 template <bool F16>
-__device__ __forceinline__ void widen(uint4 c, uint4& lo, uint4& hi) {
+__device__ __forceinline__ void widen(uint4 c, float scale, uint4& lo, uint4& hi) {
   const uint32_t w[4] = {c.x, c.y, c.z, c.w};
   uint32_t r[8];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     if constexpr (F16) {
-      r[2 * j] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[j], 1.f, false));
-      r[2 * j + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[j], 1.f, true));
+      r[2 * j] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[j], scale, false));
+      r[2 * j + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[j], scale, true));
     } else {
-      r[2 * j] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[j], 1.f, false));
-      r[2 * j + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[j], 1.f, true));
+      r[2 * j] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[j], scale, false));
+      r[2 * j + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[j], scale, true));
     }
   }
   lo = make_uint4(r[0], r[1], r[2], r[3]);
   hi = make_uint4(r[4], r[5], r[6], r[7]);
 }
 
-__device__ __forceinline__ bool nan_code(uint32_t w) {
-  return (((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
-}
-
 __device__ __forceinline__ float halves_max(float x) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
   return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
+
+// 0xFF for each of four codes that is NaN.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
+  return ((((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7) * 0xFFu;
+}
+
 __device__ __forceinline__ float halves_sum(float x) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
@@ -83,11 +87,14 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_tiles_kernel(Til
   constexpr int NC = TK * CC / 256;      // loads of K, and of V, a thread and tile
   constexpr int KS = D / 16, NJ = D / 32;
   constexpr int NH = TK / 32, NG = TK / 16;
+  constexpr int GT = kGroups / NG;       // tiles of a stage of groups
   __shared__ __attribute__((aligned(128))) uint4 kt[2][TK * CH];
   __shared__ __attribute__((aligned(128))) uint4 vt[2][TK * CH];
-  __shared__ float k_unit[2][NG];
-  __shared__ int v_exp[2][NG];   // kNoGroup: no page there
-  __shared__ int any_nan[2][4];  // in V's codes, by the wave that staged them
+  // Groups of 16 tokens: their slots (kHidden: no page there), K's scales, the exponents of V's.
+  __shared__ __attribute__((aligned(16))) uint32_t slots[2][kGroups];
+  __shared__ __attribute__((aligned(16))) float k_unit[2][kGroups];
+  __shared__ __attribute__((aligned(16))) int v_exp[2][kGroups];
+  __shared__ int any_nan;  // in V's codes of tiles with tokens that some rows do not see
 
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int c = lane & 31, g = lane >> 5;
@@ -144,71 +151,85 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_tiles_kernel(Til
     qf[s] = as_bf16x8(x);
   }
 
-  // Staging: thread i has chunk i % CC of tokens i / CC, + 256 / CC, ...; the first
-  // 2 * NG threads the scales of the groups of 16 tokens, which are in one block.
+  // Groups of 16 tokens, which are in one page and block: a stage of them at a time
+  // is looked up, while the stage before is worked on.
   const int32_t* table = a.table + static_cast<int64_t>(r) * a.row_pages;
-  const auto page_at = [&](int32_t t) {
-    if (t >= most) return -1;
-    const int32_t p = table[div_page(t, a.page)];
-    return p >= 0 && p < a.pages ? p : -1;
-  };
+  int32_t group_page = -1;
+  uint32_t group_slot = kHidden;
+  float group_k = 0.f, group_v = 0.f;
   const auto slot_at = [&](int32_t t, int32_t page) {
     const uint32_t in = static_cast<uint32_t>(t) - div_page(t, a.page) * a.page.P;
     return (static_cast<uint32_t>(page) * a.kv_heads + kvh) * a.page.P + in;
   };
-  int32_t pages[NC], group_page = -1;
-  uint4 kc[NC], vc[NC];
-  float group_unit = 0.f;  // 0: no page there
-  const int my_token = threadIdx.x / CC, my_chunk = threadIdx.x % CC, my_group = threadIdx.x % NG;
-  const bool scales = threadIdx.x < 2 * NG;
-  const auto find = [&](int32_t tile) {
-#pragma unroll
-    for (int i = 0; i < NC; ++i) pages[i] = page_at(tile * TK + my_token + i * (256 / CC));
-    if (scales) group_page = page_at(tile * TK + my_group * 16);
+  const auto group_token = [&](int32_t stage) { return (t0 + stage * GT) * TK + static_cast<int32_t>(threadIdx.x) * 16; };
+  const auto find_page = [&](int32_t stage) {
+    const int32_t t = group_token(stage);
+    group_page = -1;
+    if (threadIdx.x < kGroups && t < min(most, t1 * TK)) group_page = table[div_page(t, a.page)];
   };
-  const auto load = [&](int32_t tile) {
-#pragma unroll
-    for (int i = 0; i < NC; ++i) {
-      const int32_t t = tile * TK + my_token + i * (256 / CC);
-      kc[i] = vc[i] = make_uint4(0, 0, 0, 0);
-      if (pages[i] >= 0) {
-        const uint64_t from = static_cast<uint64_t>(slot_at(t, pages[i])) * D + my_chunk * 16;
-        kc[i] = *reinterpret_cast<const uint4*>(a.k_pages + from);
-        vc[i] = *reinterpret_cast<const uint4*>(a.v_pages + from);
-      }
-    }
-    if (scales) {
-      group_unit = 0.f;
-      if (group_page >= 0)
-        group_unit = (threadIdx.x < NG ? a.k_scale : a.v_scale)[slot_at(tile * TK + my_group * 16, group_page) >> a.shift];
+  const auto find_scales = [&](int32_t stage) {
+    group_slot = kHidden;
+    if (group_page >= 0 && group_page < a.pages) {
+      group_slot = slot_at(group_token(stage), group_page);
+      group_k = a.k_scale[group_slot >> a.shift];
+      group_v = a.v_scale[group_slot >> a.shift];
     }
   };
+  const auto keep_groups = [&](int32_t stage) {
+    if (threadIdx.x >= kGroups) return;
+    slots[stage & 1][threadIdx.x] = group_slot;
+    k_unit[stage & 1][threadIdx.x] = group_k;
+    v_exp[stage & 1][threadIdx.x] =
+        group_slot == kHidden ? kNoGroup : static_cast<int>(__float_as_uint(group_v) >> 23) - 127;
+  };
+
+  // Thread i has chunk i % CC of tokens i / CC, + 256 / CC, ...
   // Swizzles of the chunks, so that 16 rows' reads of a chunk (K) and four rows' of
   // 64 bytes (V) are in different banks.
   const auto k_at = [](int row, int chunk) { return row * CH + (chunk ^ (D == 64 ? row >> 1 & 7 : row & 15)); };
   const auto v_at = [](int row, int chunk) { return row * CH + (chunk ^ (D == 64 ? (row >> 1 & 1) << 2 : (row & 3) << 2)); };
-  const auto stage = [&](int32_t tile, int b) {
-    bool nan = false;
+  const int my_token = threadIdx.x / CC, my_chunk = threadIdx.x % CC;
+  uint4 kc[NC], vc[NC];
+  float ku[NC];
+  const auto load = [&](int32_t tile) {
+    const int32_t n = tile - t0, stage = n / GT & 1, first = n % GT * NG;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int row = my_token + i * (256 / CC);
+      const uint32_t s = slots[stage][first + row / 16];
+      ku[i] = k_unit[stage][first + row / 16];
+      kc[i] = vc[i] = make_uint4(0, 0, 0, 0);
+      if (s != kHidden && tile * TK + row < most) {
+        const uint64_t from = static_cast<uint64_t>(s + row % 16) * D + my_chunk * 16;
+        kc[i] = *reinterpret_cast<const uint4*>(a.k_pages + from);
+        vc[i] = *reinterpret_cast<const uint4*>(a.v_pages + from);
+      }
+    }
+  };
+  const auto widen_tile = [&](int32_t tile, int b) {
+    if ((tile + 1) * TK > least) {  // not every row sees every token: a NaN must not meet a weight of zero
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        uint32_t* w = reinterpret_cast<uint32_t*>(&vc[i]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t bad = nan_bytes(w[j]);
+          if (bad) any_nan = 1;
+          w[j] &= ~bad;
+        }
+      }
+    }
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int row = my_token + i * (256 / CC);
       uint4 lo, hi;
-      widen<false>(kc[i], lo, hi);
+      widen<false>(kc[i], ku[i], lo, hi);
       kt[b][k_at(row, 2 * my_chunk)] = lo;
       kt[b][k_at(row, 2 * my_chunk + 1)] = hi;
-      widen<true>(vc[i], lo, hi);
+      widen<true>(vc[i], 1.f, lo, hi);
       vt[b][v_at(row, 2 * my_chunk)] = lo;
       vt[b][v_at(row, 2 * my_chunk + 1)] = hi;
-      nan |= nan_code(vc[i].x) || nan_code(vc[i].y) || nan_code(vc[i].z) || nan_code(vc[i].w);
     }
-    if ((tile + 1) * TK > least) {  // only a tile that hides tokens asks
-      const bool any = __any(nan);
-      if (lane == 0) any_nan[b][wave] = any;
-    }
-    if (threadIdx.x < NG)
-      k_unit[b][my_group] = group_unit;
-    else if (scales)
-      v_exp[b][my_group] = group_unit == 0.f ? kNoGroup : static_cast<int>(__float_as_uint(group_unit) >> 23) - 127;
   };
 
   f32x16 acc[NJ];
@@ -221,6 +242,15 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_tiles_kernel(Til
   const int vrow = 4 * g + (lane & 15) / 4, vcol = 2 * (lane >> 4 & 1) + (lane & 3) / 2;  // transposing reads
 
   const auto compute = [&](int32_t tile, int b) {
+    const int32_t n = tile - t0, stage = n / GT & 1, first = n % GT * NG;
+    int unit_v[NG];
+    bool all = (tile + 1) * TK <= least, near = true;  // every row sees every token; scales near the reference
+#pragma unroll
+    for (int i = 0; i < NG; ++i) {
+      unit_v[i] = __builtin_amdgcn_readfirstlane(v_exp[stage][first + i]);
+      all = all && unit_v[i] != kNoGroup;
+      near = near && (unit_v[i] == kNoGroup || (unit_v[i] <= eref && unit_v[i] >= eref - kNear));
+    }
     f32x16 st[NH];
 #pragma unroll
     for (int h = 0; h < NH; ++h) {
@@ -230,31 +260,22 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_tiles_kernel(Til
       for (int s = 0; s < KS; ++s)
         st[h] = mfma32_bf16(as_bf16x8(kt[b][k_at(32 * h + c, 2 * s + g)]), qf[s], st[h]);
     }
-    float unit_k[NG];
-    int unit_v[NG];
-    bool hides = (tile + 1) * TK > least;
-#pragma unroll
-    for (int i = 0; i < NG; ++i) {
-      unit_k[i] = fmaxf(__uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(k_unit[b][i]))) * a.scale2, 1e-44f);
-      unit_v[i] = __builtin_amdgcn_readfirstlane(v_exp[b][i]);
-      hides |= unit_v[i] == kNoGroup;
-    }
-    const auto place = [&](int h, int e) { return tile * TK + 32 * h + 8 * (e / 4) + 4 * g + e % 4; };
-    if (hides) {
+    if (!all) {
+      __builtin_amdgcn_sched_barrier(0);  // a branch, not 32 selects in every tile
 #pragma unroll
       for (int h = 0; h < NH; ++h)
 #pragma unroll
         for (int e = 0; e < 16; ++e)
-          st[h][e] = place(h, e) < seen && unit_v[2 * h + e / 8] != kNoGroup ? st[h][e] : -INFINITY;
+          st[h][e] = tile * TK + 32 * h + 8 * (e / 4) + 4 * g + e % 4 < seen && unit_v[2 * h + e / 8] != kNoGroup
+                         ? st[h][e] : -INFINITY;
     }
     float high = -INFINITY;
 #pragma unroll
     for (int i = 0; i < NG; ++i) {
-      float x = st[i / 2][i % 2 * 8];
 #pragma unroll
-      for (int e = 1; e < 8; ++e) x = fmaxf(x, st[i / 2][i % 2 * 8 + e]);
-      high = fmaxf(high, x * unit_k[i]);
+      for (int e = 0; e < 8; ++e) high = fmaxf(high, st[i / 2][i % 2 * 8 + e]);
     }
+    high *= a.scale2;
     if (__any(high > m + kSlack)) {
       const float next = fmaxf(m, halves_max(high));
       const float f = next == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - next);
@@ -264,85 +285,92 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_tiles_kernel(Til
       for (int j = 0; j < NJ; ++j) acc[j] *= f;
     }
     const float mb = m == -INFINITY ? 0.f : m;
-    bool nan = false;
-    if (hides && (tile + 1) * TK > least)
-      nan = __builtin_amdgcn_readfirstlane(any_nan[b][0] | any_nan[b][1] | any_nan[b][2] | any_nan[b][3]) != 0;
+    // Groups whose scales are not near the reference are taken one at a time, the
+    // others' weights zero meanwhile.
+    int pass = 0;
+    do {
+      if (!near) {
+        int e = unit_v[0];
 #pragma unroll
-    for (int i = 0; i < NG; ++i) {
-      int e = unit_v[i];
-      if (e == kNoGroup) e = eref;  // its weights are zero
-      if (e > eref || e < eref - kNear) {
-        loudest = max(loudest, e);
-        const int next = max(e, loudest - kFar);
-        const float f = __builtin_amdgcn_ldexpf(1.f, max(eref - next, -200));
-        eref = next;
+        for (int i = 1; i < NG; ++i) e = pass == i ? unit_v[i] : e;
+        if (e != kNoGroup) {
+          loudest = max(loudest, e);
+          const int next = max(e, loudest - kFar);
+          const float f = __builtin_amdgcn_ldexpf(1.f, max(eref - next, -200));
+          eref = next;
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) acc[j] *= f;
-      }
-      // Far below the reference a block's values no longer count, but its weights do.
-      const float lift = kLift + static_cast<float>(max(e - eref, -100));
-      const float base = lift - mb;
-      f16x8 w;
-      float sum = 0.f;
-#pragma unroll
-      for (int x = 0; x < 8; ++x) {
-        const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(st[i / 2][i % 2 * 8 + x], unit_k[i], base));
-        sum += p;
-        w[x] = static_cast<_Float16>(p);
-      }
-      l += sum * __builtin_amdgcn_exp2f(-lift);
-      f16x8 shown;  // 1 where the row sees the token
-      if (nan) {
-#pragma unroll
-        for (int x = 0; x < 8; ++x)
-          shown[x] = place(i / 2, i % 2 * 8 + x) < seen ? static_cast<_Float16>(1.f) : static_cast<_Float16>(0.f);
-      }
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        const auto part = [&](int row) {
-          const uint8_t* p = reinterpret_cast<const uint8_t*>(&vt[b][v_at(row, 4 * j + vcol)]) + (lane & 1) * 8;
-          return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)p);
-        };
-        const s16x4 y0 = part(16 * i + vrow), y1 = part(16 * i + 8 + vrow);
-        f16x8 v = __builtin_bit_cast(f16x8, __builtin_shufflevector(y0, y1, 0, 1, 2, 3, 4, 5, 6, 7));
-        if (nan) {  // NaN values reach the rows that see them, and no others
-          f16x8 bad;
-          f32x16 hits;
-#pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            const bool is = v[x] != v[x];
-            bad[x] = is ? static_cast<_Float16>(1.f) : static_cast<_Float16>(0.f);
-            v[x] = is ? static_cast<_Float16>(0.f) : v[x];
-          }
-#pragma unroll
-          for (int y = 0; y < 16; ++y) hits[y] = 0.f;
-          hits = __builtin_amdgcn_mfma_f32_32x32x16_f16(bad, shown, hits, 0, 0, 0);
-#pragma unroll
-          for (int y = 0; y < 16; ++y) acc[j][y] = hits[y] > 0.f ? NAN : acc[j][y];
+          for (int j = 0; j < NJ; ++j) acc[j] *= f;
         }
-        acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, w, acc[j], 0, 0, 0);
       }
-    }
+#pragma unroll
+      for (int i = 0; i < NG; ++i) {
+        // Far below the reference a block's values no longer count, but its weights do.
+        const float lift = kLift + static_cast<float>(unit_v[i] == kNoGroup ? 0 : max(unit_v[i] - eref, -100));
+        const bool now = near || pass == i;
+        const float base = now ? lift - mb : -INFINITY;
+        f16x8 w;
+        float sum = 0.f;
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(st[i / 2][i % 2 * 8 + x], a.scale2, base));
+          sum += p;
+          w[x] = static_cast<_Float16>(p);
+        }
+        l += sum * (now ? __builtin_amdgcn_exp2f(-lift) : 0.f);
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          const auto part = [&](int row) {
+            const uint8_t* p = reinterpret_cast<const uint8_t*>(&vt[b][v_at(row, 4 * j + vcol)]) + (lane & 1) * 8;
+            return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)p);
+          };
+          const s16x4 y0 = part(16 * i + vrow), y1 = part(16 * i + 8 + vrow);
+          const f16x8 v = __builtin_bit_cast(f16x8, __builtin_shufflevector(y0, y1, 0, 1, 2, 3, 4, 5, 6, 7));
+          acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, w, acc[j], 0, 0, 0);
+        }
+      }
+    } while (!near && ++pass < NG);
   };
 
-  find(t0);
+  if (threadIdx.x == 0) any_nan = 0;
+  find_page(0);
+  find_scales(0);
+  keep_groups(0);
+  __syncthreads();
   load(t0);
-  stage(t0, 0);
-  if (t0 + 1 < t1) {
-    find(t0 + 1);
-    load(t0 + 1);
-  }
+  widen_tile(t0, 0);
   for (int32_t tile = t0; tile < t1; ++tile) {
     const int b = (tile - t0) & 1;
     __syncthreads();
-    if (tile + 2 < t1) find(tile + 2);
+    const bool more = tile + 1 < t1;
+    if (more) load(tile + 1);
+    const int32_t n = tile - t0, stage = n / GT + 1;
+    if (t0 + stage * GT < t1) {  // the next stage's groups, over three tiles
+      if (n % GT == 0) find_page(stage);
+      if (n % GT == 1) find_scales(stage);
+      if (n % GT == 2) keep_groups(stage);
+    }
     if (busy) compute(tile, b);
-    if (tile + 1 < t1) stage(tile + 1, b ^ 1);
-    if (tile + 2 < t1) load(tile + 2);
+    if (more) widen_tile(tile + 1, b ^ 1);
   }
 
   l = halves_sum(l);
+  __syncthreads();
   if (!mine) return;
+  if (any_nan) {  // the NaN values left out above, for the rows that see them
+    for (int32_t s = max(t0 * TK, least / TK * TK); s < min(t1 * TK, seen); ++s) {
+      const int32_t page = table[div_page(s, a.page)];
+      if (page < 0 || page >= a.pages) continue;
+      const uint8_t* v = a.v_pages + static_cast<uint64_t>(slot_at(s, page)) * D + 4 * g;
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t bad = nan_bytes(*reinterpret_cast<const uint32_t*>(v + 32 * j + 8 * e));
+#pragma unroll
+          for (int x = 0; x < 4; ++x) acc[j][4 * e + x] = bad >> 8 * x & 1 ? NAN : acc[j][4 * e + x];
+        }
+    }
+  }
   const float unit_o = __builtin_amdgcn_ldexpf(1.f, max(eref, -200) - static_cast<int>(kLift));
   const int64_t part = at * a.splits + split;
   if (g == 0) {
