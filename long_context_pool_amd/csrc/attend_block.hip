@@ -91,9 +91,9 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_tiles_kernel(Til
   __shared__ __attribute__((aligned(128))) uint4 kt[2][TK * CH];
   __shared__ __attribute__((aligned(128))) uint4 vt[2][TK * CH];
   // Groups of 16 tokens: their slots (kHidden: no page there), K's scales, the exponents of V's.
-  __shared__ __attribute__((aligned(16))) uint32_t slots[2][kGroups];
-  __shared__ __attribute__((aligned(16))) float k_unit[2][kGroups];
-  __shared__ __attribute__((aligned(16))) int v_exp[2][kGroups];
+  __shared__ __attribute__((aligned(16))) uint32_t slots[2 * kGroups];
+  __shared__ __attribute__((aligned(16))) float k_unit[2 * kGroups];
+  __shared__ __attribute__((aligned(16))) int v_exp[2 * kGroups];
   __shared__ int any_nan;  // in V's codes of tiles with tokens that some rows do not see
 
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -177,9 +177,9 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_tiles_kernel(Til
   };
   const auto keep_groups = [&](int32_t stage) {
     if (threadIdx.x >= kGroups) return;
-    slots[stage & 1][threadIdx.x] = group_slot;
-    k_unit[stage & 1][threadIdx.x] = group_k;
-    v_exp[stage & 1][threadIdx.x] =
+    slots[(stage & 1) * kGroups + threadIdx.x] = group_slot;
+    k_unit[(stage & 1) * kGroups + threadIdx.x] = group_k;
+    v_exp[(stage & 1) * kGroups + threadIdx.x] =
         group_slot == kHidden ? kNoGroup : static_cast<int>(__float_as_uint(group_v) >> 23) - 127;
   };
 
@@ -187,35 +187,46 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_tiles_kernel(Til
   // Swizzles of the chunks, so that 16 rows' reads of a chunk (K) and four rows' of
   // 64 bytes (V) are in different banks.
   const auto k_at = [](int row, int chunk) { return row * CH + (chunk ^ (D == 64 ? row >> 1 & 7 : row & 15)); };
-  const auto v_at = [](int row, int chunk) { return row * CH + (chunk ^ (D == 64 ? (row >> 1 & 1) << 2 : (row & 3) << 2)); };
+  const auto v_at = [](int row, int chunk) {
+    return row * CH + (D == 64 ? chunk ^ (row >> 1 & 1) << 2 : chunk ^ (row & 3) << 2);
+  };
   const int my_token = threadIdx.x / CC, my_chunk = threadIdx.x % CC;
+  // Rows i of a thread are a multiple of 16 apart (or it has one): one address
+  // within a group.
+  const uint8_t* k_from = a.k_pages + (my_token % 16) * D + my_chunk * 16;
+  const uint8_t* v_from = a.v_pages + (my_token % 16) * D + my_chunk * 16;
   uint4 kc[NC], vc[NC];
   float ku[NC];
+  bool there[NC];
   const auto load = [&](int32_t tile) {
-    const int32_t n = tile - t0, stage = n / GT & 1, first = n % GT * NG;
+    const int32_t n = tile - t0, first = (n & (2 * GT - 1)) * NG + my_token / 16;
+    const uint32_t* slot = &slots[first];
+    const float* unit = &k_unit[first];
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-      const int row = my_token + i * (256 / CC);
-      const uint32_t s = slots[stage][first + row / 16];
-      ku[i] = k_unit[stage][first + row / 16];
-      kc[i] = vc[i] = make_uint4(0, 0, 0, 0);
-      if (s != kHidden && tile * TK + row < most) {
-        const uint64_t from = static_cast<uint64_t>(s + row % 16) * D + my_chunk * 16;
-        kc[i] = *reinterpret_cast<const uint4*>(a.k_pages + from);
-        vc[i] = *reinterpret_cast<const uint4*>(a.v_pages + from);
-      }
+      const uint32_t s = slot[i * (256 / CC) / 16];
+      ku[i] = unit[i * (256 / CC) / 16];
+      there[i] = s != kHidden;
+      const uint64_t off = static_cast<uint64_t>(there[i] ? s : 0) * D;  // some page: what it holds is not used
+      kc[i] = *reinterpret_cast<const uint4*>(k_from + off);
+      vc[i] = *reinterpret_cast<const uint4*>(v_from + off);
     }
   };
   const auto widen_tile = [&](int32_t tile, int b) {
-    if ((tile + 1) * TK > least) {  // not every row sees every token: a NaN must not meet a weight of zero
+    bool whole = (tile + 1) * TK <= least;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) whole = whole && !__any(!there[i]);
+    if (!whole) {  // not every row sees every token: a NaN must not meet a weight of zero
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
+        const bool seen = there[i] && tile * TK + my_token + i * (256 / CC) < most;
         uint32_t* w = reinterpret_cast<uint32_t*>(&vc[i]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const uint32_t bad = nan_bytes(w[j]);
+          const uint32_t bad = seen ? nan_bytes(w[j]) : 0u;
           if (bad) any_nan = 1;
-          w[j] &= ~bad;
+          w[j] = seen ? w[j] & ~bad : 0u;
         }
       }
     }
@@ -242,14 +253,15 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_tiles_kernel(Til
   const int vrow = 4 * g + (lane & 15) / 4, vcol = 2 * (lane >> 4 & 1) + (lane & 3) / 2;  // transposing reads
 
   const auto compute = [&](int32_t tile, int b) {
-    const int32_t n = tile - t0, stage = n / GT & 1, first = n % GT * NG;
+    const int32_t first = ((tile - t0) & (2 * GT - 1)) * NG;
     int unit_v[NG];
-    bool all = (tile + 1) * TK <= least, near = true;  // every row sees every token; scales near the reference
+    bool all = (tile + 1) * TK <= least;  // every row sees every token
+    int loud = kNoGroup;
 #pragma unroll
     for (int i = 0; i < NG; ++i) {
-      unit_v[i] = __builtin_amdgcn_readfirstlane(v_exp[stage][first + i]);
+      unit_v[i] = __builtin_amdgcn_readfirstlane(v_exp[first + i]);
       all = all && unit_v[i] != kNoGroup;
-      near = near && (unit_v[i] == kNoGroup || (unit_v[i] <= eref && unit_v[i] >= eref - kNear));
+      loud = max(loud, unit_v[i]);
     }
     f32x16 st[NH];
 #pragma unroll
@@ -276,59 +288,47 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_tiles_kernel(Til
       for (int e = 0; e < 8; ++e) high = fmaxf(high, st[i / 2][i % 2 * 8 + e]);
     }
     high *= a.scale2;
-    if (__any(high > m + kSlack)) {
+    // A new reference maximum or exponent: O's registers follow.
+    if (__any(high > m + kSlack) || loud > eref || (loud < eref - kNear && loud != kNoGroup)) {
       const float next = fmaxf(m, halves_max(high));
-      const float f = next == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - next);
+      float f = next == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - next);
       m = next;
       l *= f;
+      if (loud != kNoGroup) {
+        loudest = max(loudest, loud);
+        const int unit = loud <= eref && loud >= eref - kNear ? eref : max(loud, loudest - kFar);
+        f = __builtin_amdgcn_ldexpf(f, max(eref - unit, -200));
+        eref = unit;
+      }
 #pragma unroll
       for (int j = 0; j < NJ; ++j) acc[j] *= f;
     }
     const float mb = m == -INFINITY ? 0.f : m;
-    // Groups whose scales are not near the reference are taken one at a time, the
-    // others' weights zero meanwhile.
-    int pass = 0;
-    do {
-      if (!near) {
-        int e = unit_v[0];
 #pragma unroll
-        for (int i = 1; i < NG; ++i) e = pass == i ? unit_v[i] : e;
-        if (e != kNoGroup) {
-          loudest = max(loudest, e);
-          const int next = max(e, loudest - kFar);
-          const float f = __builtin_amdgcn_ldexpf(1.f, max(eref - next, -200));
-          eref = next;
+    for (int i = 0; i < NG; ++i) {
+      // Far below the reference a block's values no longer count, but its weights do.
+      const int lift = static_cast<int>(kLift) + max(unit_v[i] - eref, -100);
+      const float base = static_cast<float>(lift) - mb;
+      f16x8 w;
+      float sum = 0.f;
 #pragma unroll
-          for (int j = 0; j < NJ; ++j) acc[j] *= f;
-        }
+      for (int x = 0; x < 8; ++x) {
+        const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(st[i / 2][i % 2 * 8 + x], a.scale2, base));
+        sum += p;
+        w[x] = static_cast<_Float16>(p);
       }
+      l = __builtin_fmaf(sum, __uint_as_float(static_cast<uint32_t>(127 - lift) << 23), l);  // sum * 2^-lift
 #pragma unroll
-      for (int i = 0; i < NG; ++i) {
-        // Far below the reference a block's values no longer count, but its weights do.
-        const float lift = kLift + static_cast<float>(unit_v[i] == kNoGroup ? 0 : max(unit_v[i] - eref, -100));
-        const bool now = near || pass == i;
-        const float base = now ? lift - mb : -INFINITY;
-        f16x8 w;
-        float sum = 0.f;
-#pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(st[i / 2][i % 2 * 8 + x], a.scale2, base));
-          sum += p;
-          w[x] = static_cast<_Float16>(p);
-        }
-        l += sum * (now ? __builtin_amdgcn_exp2f(-lift) : 0.f);
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-          const auto part = [&](int row) {
-            const uint8_t* p = reinterpret_cast<const uint8_t*>(&vt[b][v_at(row, 4 * j + vcol)]) + (lane & 1) * 8;
-            return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)p);
-          };
-          const s16x4 y0 = part(16 * i + vrow), y1 = part(16 * i + 8 + vrow);
-          const f16x8 v = __builtin_bit_cast(f16x8, __builtin_shufflevector(y0, y1, 0, 1, 2, 3, 4, 5, 6, 7));
-          acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, w, acc[j], 0, 0, 0);
-        }
+      for (int j = 0; j < NJ; ++j) {
+        const auto part = [&](int row) {
+          const uint8_t* p = reinterpret_cast<const uint8_t*>(&vt[b][v_at(row, 4 * j + vcol)]) + (lane & 1) * 8;
+          return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)p);
+        };
+        const s16x4 y0 = part(16 * i + vrow), y1 = part(16 * i + 8 + vrow);
+        const f16x8 v = __builtin_bit_cast(f16x8, __builtin_shufflevector(y0, y1, 0, 1, 2, 3, 4, 5, 6, 7));
+        acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, w, acc[j], 0, 0, 0);
       }
-    } while (!near && ++pass < NG);
+    }
   };
 
   if (threadIdx.x == 0) any_nan = 0;
