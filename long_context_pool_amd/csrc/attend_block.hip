@@ -12,10 +12,11 @@ namespace {
 
 typedef __attribute__((ext_vector_type(8))) _Float16 f16x8;
 
-constexpr int kRows = 128;  // rows (queries times the query heads of a kv head) of a workgroup
+constexpr int kThreads = 256;
+constexpr int kRows = kThreads / 2;  // rows (queries times the query heads of a kv head) of a workgroup
 constexpr float kLift = 7.f;  // weights go up to 2^(kSlack + kLift) < 65504, f16's largest
-constexpr int kNoGroup = -(1 << 30);
-constexpr int kFar = 60, kNear = 8;
+constexpr float kNoGroup = -1e9f;  // the exponent of a group without a page
+constexpr float kFar = 60.f, kNear = 8.f;
 constexpr int kGroups = 128;  // groups of 16 tokens that are looked up at a time
 
 struct TileArgs {
@@ -81,10 +82,10 @@ __device__ __forceinline__ float halves_sum(float x) {
 // relative to a reference exponent, `eref`, which O's registers are in units of and
 // which follows the blocks' scales when they leave its neighbourhood.
 template <int D, int TK>
-__global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_tiles_kernel(TileArgs a) {
+__global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attend_tiles_kernel(TileArgs a) {
   constexpr int CH = D / 8;              // 16-byte chunks of a widened row
   constexpr int CC = D / 16;             // of a row of codes
-  constexpr int NC = TK * CC / 256;      // loads of K, and of V, a thread and tile
+  constexpr int NC = TK * CC / kThreads;  // loads of K, and of V, a thread and tile
   constexpr int KS = D / 16, NJ = D / 32;
   constexpr int NH = TK / 32, NG = TK / 16;
   constexpr int GT = kGroups / NG;       // tiles of a stage of groups
@@ -93,7 +94,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_tiles_kernel(Til
   // Groups of 16 tokens: their slots (kHidden: no page there), K's scales, the exponents of V's.
   __shared__ __attribute__((aligned(16))) uint32_t slots[2 * kGroups];
   __shared__ __attribute__((aligned(16))) float k_unit[2 * kGroups];
-  __shared__ __attribute__((aligned(16))) int v_exp[2 * kGroups];
+  __shared__ __attribute__((aligned(16))) float v_exp[2 * kGroups];
   __shared__ int any_nan;  // in V's codes of tiles with tokens that some rows do not see
 
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -180,10 +181,10 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_tiles_kernel(Til
     slots[(stage & 1) * kGroups + threadIdx.x] = group_slot;
     k_unit[(stage & 1) * kGroups + threadIdx.x] = group_k;
     v_exp[(stage & 1) * kGroups + threadIdx.x] =
-        group_slot == kHidden ? kNoGroup : static_cast<int>(__float_as_uint(group_v) >> 23) - 127;
+        group_slot == kHidden ? kNoGroup : static_cast<float>(static_cast<int>(__float_as_uint(group_v) >> 23) - 127);
   };
 
-  // Thread i has chunk i % CC of tokens i / CC, + 256 / CC, ...
+  // Thread i has chunk i % CC of tokens i / CC, + kThreads / CC, ...
   // Swizzles of the chunks, so that 16 rows' reads of a chunk (K) and four rows' of
   // 64 bytes (V) are in different banks.
   const auto k_at = [](int row, int chunk) { return row * CH + (chunk ^ (D == 64 ? row >> 1 & 7 : row & 15)); };
@@ -197,22 +198,38 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_tiles_kernel(Til
   const uint8_t* v_from = a.v_pages + (my_token % 16) * D + my_chunk * 16;
   uint4 kc[NC], vc[NC];
   float ku[NC];
-  bool there[NC];
-  const auto load = [&](int32_t tile) {
-    const int32_t n = tile - t0, first = (n & (2 * GT - 1)) * NG + my_token / 16;
-    const uint32_t* slot = &slots[first];
-    const float* unit = &k_unit[first];
+  bool there[NC];  // V's tokens
+  const auto load_k = [&](int32_t tile) {
+    const int32_t first = ((tile - t0) & (2 * GT - 1)) * NG + my_token / 16;
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-      const uint32_t s = slot[i * (256 / CC) / 16];
-      ku[i] = unit[i * (256 / CC) / 16];
-      there[i] = s != kHidden;
-      const uint64_t off = static_cast<uint64_t>(there[i] ? s : 0) * D;  // some page: what it holds is not used
+      const uint32_t s = slots[first + i * (kThreads / CC) / 16];
+      ku[i] = k_unit[first + i * (kThreads / CC) / 16];
+      const uint64_t off = static_cast<uint64_t>(s != kHidden ? s : 0) * D;  // some page: what it holds is not used
       kc[i] = *reinterpret_cast<const uint4*>(k_from + off);
+    }
+  };
+  const auto load_v = [&](int32_t tile) {
+    const int32_t first = ((tile - t0) & (2 * GT - 1)) * NG + my_token / 16;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const uint32_t s = slots[first + i * (kThreads / CC) / 16];
+      there[i] = s != kHidden;
+      const uint64_t off = static_cast<uint64_t>(there[i] ? s : 0) * D;
       vc[i] = *reinterpret_cast<const uint4*>(v_from + off);
     }
   };
-  const auto widen_tile = [&](int32_t tile, int b) {
+  const auto widen_k = [&](int b) {
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int row = my_token + i * (kThreads / CC);
+      uint4 lo, hi;
+      widen<false>(kc[i], ku[i], lo, hi);
+      kt[b][k_at(row, 2 * my_chunk)] = lo;
+      kt[b][k_at(row, 2 * my_chunk + 1)] = hi;
+    }
+  };
+  const auto widen_v = [&](int32_t tile, int b) {
     bool whole = (tile + 1) * TK <= least;
 #pragma unroll
     for (int i = 0; i < NC; ++i) whole = whole && !__any(!there[i]);
@@ -220,7 +237,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_tiles_kernel(Til
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
-        const bool seen = there[i] && tile * TK + my_token + i * (256 / CC) < most;
+        const bool seen = there[i] && tile * TK + my_token + i * (kThreads / CC) < most;
         uint32_t* w = reinterpret_cast<uint32_t*>(&vc[i]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -232,11 +249,8 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_tiles_kernel(Til
     }
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-      const int row = my_token + i * (256 / CC);
+      const int row = my_token + i * (kThreads / CC);
       uint4 lo, hi;
-      widen<false>(kc[i], ku[i], lo, hi);
-      kt[b][k_at(row, 2 * my_chunk)] = lo;
-      kt[b][k_at(row, 2 * my_chunk + 1)] = hi;
       widen<true>(vc[i], 1.f, lo, hi);
       vt[b][v_at(row, 2 * my_chunk)] = lo;
       vt[b][v_at(row, 2 * my_chunk + 1)] = hi;
@@ -249,55 +263,60 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_tiles_kernel(Til
 #pragma unroll
     for (int e = 0; e < 16; ++e) acc[j][e] = 0.f;
   float m = -INFINITY, l = 0.f;  // of this lane's row, and of its half of the tokens
-  int eref = kNoGroup, loudest = kNoGroup;
+  float eref = kNoGroup, loudest = kNoGroup;  // whole numbers, uniform
   const int vrow = 4 * g + (lane & 15) / 4, vcol = 2 * (lane >> 4 & 1) + (lane & 3) / 2;  // transposing reads
 
-  const auto compute = [&](int32_t tile, int b) {
-    const int32_t first = ((tile - t0) & (2 * GT - 1)) * NG;
-    int unit_v[NG];
-    bool all = (tile + 1) * TK <= least;  // every row sees every token
-    int loud = kNoGroup;
+  const auto score = [&](int b, f32x16 (&st)[NH]) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < NG; ++i) {
-      unit_v[i] = __builtin_amdgcn_readfirstlane(v_exp[first + i]);
-      all = all && unit_v[i] != kNoGroup;
-      loud = max(loud, unit_v[i]);
-    }
-    f32x16 st[NH];
-#pragma unroll
-    for (int h = 0; h < NH; ++h) {
+    for (int h = 0; h < NH; ++h)
 #pragma unroll
       for (int e = 0; e < 16; ++e) st[h][e] = 0.f;
 #pragma unroll
-      for (int s = 0; s < KS; ++s)
+    for (int s = 0; s < KS; ++s)
+#pragma unroll
+      for (int h = 0; h < NH; ++h)
         st[h] = mfma32_bf16(as_bf16x8(kt[b][k_at(32 * h + c, 2 * s + g)]), qf[s], st[h]);
+  };
+  // The exponents of a tile's groups, uniform but in vector registers: as scalars they
+  // would cost the way there and its waits (a third of the weights' time).
+  const auto exponents = [&](int32_t tile, float (&ve)[NG]) __attribute__((always_inline)) {
+    const int32_t first = ((tile - t0) & (2 * GT - 1)) * NG;
+#pragma unroll
+    for (int i = 0; i < NG; ++i) ve[i] = v_exp[first + i];
+  };
+  // Weights of a tile from its scores.
+  const auto weigh = [&](int32_t tile, const float (&ve)[NG], f32x16 (&st)[NH], f16x8 (&w)[NG]) __attribute__((always_inline)) {
+    float loud = ve[0], still = ve[0];
+#pragma unroll
+    for (int i = 1; i < NG; ++i) {
+      loud = fmaxf(loud, ve[i]);
+      still = fminf(still, ve[i]);
     }
-    if (!all) {
+    if ((tile + 1) * TK > least || __any(still == kNoGroup)) {  // some row does not see some token
       __builtin_amdgcn_sched_barrier(0);  // a branch, not 32 selects in every tile
 #pragma unroll
       for (int h = 0; h < NH; ++h)
 #pragma unroll
         for (int e = 0; e < 16; ++e)
-          st[h][e] = tile * TK + 32 * h + 8 * (e / 4) + 4 * g + e % 4 < seen && unit_v[2 * h + e / 8] != kNoGroup
+          st[h][e] = tile * TK + 32 * h + 8 * (e / 4) + 4 * g + e % 4 < seen && ve[2 * h + e / 8] != kNoGroup
                          ? st[h][e] : -INFINITY;
     }
     float high = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < NG; ++i) {
+    for (int h = 0; h < NH; ++h)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) high = fmaxf(high, st[i / 2][i % 2 * 8 + e]);
-    }
+      for (int e = 0; e < 16; ++e) high = fmaxf(high, st[h][e]);
     high *= a.scale2;
     // A new reference maximum or exponent: O's registers follow.
-    if (__any(high > m + kSlack) || loud > eref || (loud < eref - kNear && loud != kNoGroup)) {
+    if (__any(high > m + kSlack || loud > eref || (loud < eref - kNear && loud != kNoGroup))) {
       const float next = fmaxf(m, halves_max(high));
       float f = next == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - next);
       m = next;
       l *= f;
       if (loud != kNoGroup) {
-        loudest = max(loudest, loud);
-        const int unit = loud <= eref && loud >= eref - kNear ? eref : max(loud, loudest - kFar);
-        f = __builtin_amdgcn_ldexpf(f, max(eref - unit, -200));
+        loudest = fmaxf(loudest, loud);
+        const float unit = loud <= eref && loud >= eref - kNear ? eref : fmaxf(loud, loudest - kFar);
+        f = __builtin_amdgcn_ldexpf(f, static_cast<int>(fmaxf(eref - unit, -200.f)));
         eref = unit;
       }
 #pragma unroll
@@ -307,17 +326,20 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_tiles_kernel(Til
 #pragma unroll
     for (int i = 0; i < NG; ++i) {
       // Far below the reference a block's values no longer count, but its weights do.
-      const int lift = static_cast<int>(kLift) + max(unit_v[i] - eref, -100);
-      const float base = static_cast<float>(lift) - mb;
-      f16x8 w;
+      const float lift = kLift + fmaxf(ve[i] - eref, -100.f), base = lift - mb;
       float sum = 0.f;
 #pragma unroll
       for (int x = 0; x < 8; ++x) {
         const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(st[i / 2][i % 2 * 8 + x], a.scale2, base));
         sum += p;
-        w[x] = static_cast<_Float16>(p);
+        w[i][x] = static_cast<_Float16>(p);
       }
-      l = __builtin_fmaf(sum, __uint_as_float(static_cast<uint32_t>(127 - lift) << 23), l);  // sum * 2^-lift
+      l += __builtin_amdgcn_ldexpf(sum, static_cast<int>(-lift));
+    }
+  };
+  const auto add_values = [&](int b, const f16x8 (&w)[NG]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < NG; ++i)
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
         const auto part = [&](int row) {
@@ -326,8 +348,17 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_tiles_kernel(Til
         };
         const s16x4 y0 = part(16 * i + vrow), y1 = part(16 * i + 8 + vrow);
         const f16x8 v = __builtin_bit_cast(f16x8, __builtin_shufflevector(y0, y1, 0, 1, 2, 3, 4, 5, 6, 7));
-        acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, w, acc[j], 0, 0, 0);
+        acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, w[i], acc[j], 0, 0, 0);
       }
+  };
+  // The next stage's, over three tiles; before a tile's loads, for which the
+  // compiler's waits where the branches meet would otherwise be too.
+  const auto next_groups = [&](int32_t n) {
+    const int32_t stage = n / GT + 1;
+    if (t0 + stage * GT < t1) {
+      if (n % GT == 0) find_page(stage);
+      if (n % GT == 1) find_scales(stage);
+      if (n % GT == 2) keep_groups(stage);
     }
   };
 
@@ -336,21 +367,29 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_tiles_kernel(Til
   find_scales(0);
   keep_groups(0);
   __syncthreads();
-  load(t0);
-  widen_tile(t0, 0);
+  load_k(t0);
+  load_v(t0);
+  widen_k(0);
+  f32x16 st[NH];
+  f16x8 w[NG];
+  widen_v(t0, 0);
   for (int32_t tile = t0; tile < t1; ++tile) {
-    const int b = (tile - t0) & 1;
+    const int32_t n = tile - t0;
     __syncthreads();
-    const bool more = tile + 1 < t1;
-    if (more) load(tile + 1);
-    const int32_t n = tile - t0, stage = n / GT + 1;
-    if (t0 + stage * GT < t1) {  // the next stage's groups, over three tiles
-      if (n % GT == 0) find_page(stage);
-      if (n % GT == 1) find_scales(stage);
-      if (n % GT == 2) keep_groups(stage);
+    next_groups(n);
+    load_k(min(tile + 1, t1 - 1));  // no branch: the compiler would wait where it ends
+    load_v(min(tile + 1, t1 - 1));
+    if (busy) {
+      float ve[NG];
+      exponents(tile, ve);
+      score(n & 1, st);
+      weigh(tile, ve, st, w);
+      add_values(n & 1, w);
     }
-    if (busy) compute(tile, b);
-    if (more) widen_tile(tile + 1, b ^ 1);
+    if (tile + 1 < t1) {
+      widen_k(n + 1 & 1);
+      widen_v(tile + 1, n + 1 & 1);
+    }
   }
 
   l = halves_sum(l);
@@ -371,7 +410,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void attend_tiles_kernel(Til
         }
     }
   }
-  const float unit_o = __builtin_amdgcn_ldexpf(1.f, max(eref, -200) - static_cast<int>(kLift));
+  const float unit_o = __builtin_amdgcn_ldexpf(1.f, static_cast<int>(fmaxf(eref, -200.f) - kLift));
   const int64_t part = at * a.splits + split;
   if (g == 0) {
     if (a.splits > 1)
@@ -452,7 +491,7 @@ int32_t tile_splits(const Cache& c, const BlockAttend& b) {
 
 template <int D, int TK>
 hipError_t launch_tiles_dim(const TileArgs& a, uint32_t grid, hipStream_t st) {
-  attend_tiles_kernel<D, TK><<<grid, 256, 0, st>>>(a);
+  attend_tiles_kernel<D, TK><<<grid, kThreads, 0, st>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
   const int per = 1024 / D;
