@@ -438,9 +438,11 @@ def _heads_of(x, device, stride):
     may be a part of a wider row."""
     if x is None or x.__class__ is int:
         return x
-    on = x.get_device()
-    if (on != device and (device is not None or on < 0)) or x.dim() < 2 or (
-            x.shape[0] > 0 and not (x[0].is_contiguous() and (x.shape[0] == 1 or x.stride(0) == stride))):
+    on, at, size = x.get_device(), x.stride(), x.shape
+    inner = len(at) - 1
+    if (on != device and (device is not None or on < 0)) or not (
+            1 <= inner <= 2 and (at[inner] == 1 or size[inner] == 1) and (at[0] == stride or size[0] <= 1) and (
+                inner == 1 or at[1] == size[2] or size[1] == 1)):
         raise ValueError("tokens must be contiguous, their stride apart and on the device, all on one")
     return x.data_ptr()
 

@@ -13,7 +13,8 @@ namespace {
 typedef __attribute__((ext_vector_type(8))) _Float16 f16x8;
 
 constexpr int kThreads = 256;
-constexpr int kRows = kThreads / 2;  // rows (queries times the query heads of a kv head) of a workgroup
+constexpr int kRowShift = 7, kRows = 1 << kRowShift;  // rows (queries times the query heads of a kv head) of a workgroup
+static_assert(kRows == kThreads / 2, "32 rows a wave");
 constexpr float kLift = 7.f;  // weights go up to 2^(kSlack + kLift) < 65504, f16's largest
 constexpr float kNoGroup = -1e9f;  // the exponent of a group without a page
 constexpr float kFar = 60.f, kNear = 8.f;
@@ -102,12 +103,12 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attend_tiles_kerne
   const int kvh = blockIdx.x % a.kv_heads;
   const int rest = blockIdx.x / a.kv_heads;
   const int split = rest % a.splits;
-  const int64_t units = unit_base(a.rows.n, a.share, kRows, a.rows.rows, 1);
+  const int64_t units = unit_base(a.rows.n, a.share, kRowShift, a.rows.rows, 1);
   const int64_t unit = units - 1 - rest / a.splits;  // the longest rows of a prompt first
   const int32_t r = last_row(a.rows.rows, unit,
-                             [&](int32_t x) { return unit_base(a.rows.at(x), a.share, kRows, x, 1); });
+                             [&](int32_t x) { return unit_base(a.rows.at(x), a.share, kRowShift, x, 1); });
   const int32_t begin = a.rows.at(r), count = a.rows.at(r + 1) - begin;
-  const int64_t flat0 = (unit - unit_base(begin, a.share, kRows, r, 1)) * kRows;
+  const int64_t flat0 = (unit - unit_base(begin, a.share, kRowShift, r, 1)) * kRows;
   const int64_t flats = static_cast<int64_t>(max(count, 0)) * a.share;  // below 2^27
   if (flat0 < 0 || flat0 >= flats) return;
   const int32_t cap = a.row_pages * static_cast<int32_t>(a.page.P);
@@ -480,7 +481,7 @@ constexpr int kSlots = 512;  // workgroups that the card holds at a time
 constexpr int kMaxParts = 32;
 
 int64_t tile_units(const Cache& c, const BlockAttend& b) {
-  return unit_base(b.n, b.heads / c.kv_heads, kRows, c.rows, 1);
+  return unit_base(b.n, b.heads / c.kv_heads, kRowShift, c.rows, 1);
 }
 
 int32_t tile_splits(const Cache& c, const BlockAttend& b) {

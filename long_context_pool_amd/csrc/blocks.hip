@@ -12,6 +12,8 @@ namespace misa {
 
 namespace {
 
+typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
+
 constexpr int kLeastScale = -100;  // exponent of the scale of a block of zeros
 
 // The smallest 2^k, k >= -100, with amax <= 448 * 2^k = 1.75 * 2^(8 + k), for a
@@ -30,30 +32,32 @@ struct WriteArgs {
   uint8_t* pages_of[2];
   float* scale[2];
   const int32_t* table;
-  int32_t row_pages, pages, P, kv_heads, B;
+  int32_t row_pages, pages, P, kv_heads, shift;  // 2^shift tokens a block
   int32_t by_token;  // units are packed entries, not blocks
 };
 
-// One workgroup per (block with new tokens, kv head, keys or values): D / 8 lanes
-// hold eight values each of a token, and NP rounds of tokens a block, so that the
-// block's values are read once, before its scale is known, and stay in registers.
+// One workgroup per (block with new tokens, kv head), for its keys and its values:
+// D / 8 lanes hold eight values each of a token, and NP rounds of tokens a block, so
+// that the block's values are read once, before its scale is known, and stay in
+// registers.  (KV = 1: one of the two, by blockIdx.z, where both would take more
+// registers than are there, or keys alone.)
 //
 // Units go by blocks (a row's c tokens touch at most floor(c / B) + 2) or, where
 // there are fewer of them, by tokens: the first of a row and those that begin a
 // block are at work, the other workgroups leave (32 rows with a token each: 32
 // units for 64).
-template <int D, int NP>
+template <int D, int NP, int KV>
 __global__ __launch_bounds__(256) void block_write_kernel(WriteArgs a) {
   constexpr int LPR = D / 8, TP = 256 / LPR;  // lanes of a token, tokens of a round
-  __shared__ float tops[4];
-  const int which = blockIdx.z, head = blockIdx.y;
+  __shared__ float tops[KV][4];
+  const int head = blockIdx.y, B = 1 << a.shift;
   int32_t r, begin, end;
   int64_t block;  // of the row
   const int64_t u = blockIdx.x;
   if (a.by_token) {
     if (!row_of_entry(a.rows, static_cast<int32_t>(u), r, begin, end)) return;
   } else {
-    r = last_row(a.rows.rows, u, [&](int32_t x) { return unit_base(a.rows.at(x), 1, a.B, x, 2); });
+    r = last_row(a.rows.rows, u, [&](int32_t x) { return unit_base(a.rows.at(x), 1, a.shift, x, 2); });
     begin = a.rows.at(r);
     end = a.rows.at(r + 1);
     if (begin >= end) return;
@@ -62,96 +66,112 @@ __global__ __launch_bounds__(256) void block_write_kernel(WriteArgs a) {
   const int64_t from = start > 0 ? start : 0;
   if (a.by_token) {
     const int64_t p = start + (u - begin);
-    if (p < from || (p != from && p % a.B != 0)) return;
-    block = p / a.B;
+    if (p < from || (p != from && (p & (B - 1)) != 0)) return;
+    block = p >> a.shift;
   } else {
-    const int64_t j = u - unit_base(begin, 1, a.B, r, 2);
+    const int64_t j = u - unit_base(begin, 1, a.shift, r, 2);
     if (j < 0) return;
-    block = from / a.B + j;
+    block = (from >> a.shift) + j;
   }
-  const int64_t p0 = block * a.B;  // the block's first position
+  const int64_t p0 = block << a.shift;  // the block's first position
   if (p0 >= stop || p0 >= static_cast<int64_t>(a.row_pages) * a.P) return;
-  const int32_t e = static_cast<int32_t>(p0 / a.P);
+  const int32_t e = static_cast<int32_t>(static_cast<uint32_t>(p0) / static_cast<uint32_t>(a.P));  // p0 < 2^30
   const int32_t page = a.table[static_cast<int64_t>(r) * a.row_pages + e];
-  if (page < 0 || page >= a.pages) return;
-  const int64_t slot0 = (static_cast<int64_t>(page) * a.kv_heads + head) * a.P + (p0 - static_cast<int64_t>(e) * a.P);
   const int32_t low = static_cast<int32_t>(from > p0 ? from - p0 : 0);            // first new token
-  const int32_t high = static_cast<int32_t>(stop - p0 < a.B ? stop - p0 : a.B);  // one past the last
+  const int32_t high = static_cast<int32_t>(stop - p0 < B ? stop - p0 : B);  // one past the last
   const int lane = threadIdx.x % LPR, tok = threadIdx.x / LPR;
 
-  const uint16_t* src = a.fresh[which];
   const int64_t entry0 = begin + (p0 - start);  // packed entry of the block's first token
-  uint4 x[NP];
-  float top = 0.f;
+  uint4 x[KV][NP];
 #pragma unroll
-  for (int i = 0; i < NP; ++i) {
-    const int32_t t = i * TP + tok;
-    x[i] = make_uint4(0, 0, 0, 0);
-    if (t >= low && t < high)
-      x[i] = *reinterpret_cast<const uint4*>(src + ((entry0 + t) * a.kv_heads + head) * D + lane * 8);
-  }
+  for (int v = 0; v < KV; ++v) {
+    const uint16_t* src = a.fresh[KV == 1 ? blockIdx.z : v] + head * D + lane * 8;
 #pragma unroll
-  for (int i = 0; i < NP; ++i) {
-    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float y0 = fabsf(__uint_as_float(w[j] << 16)), y1 = fabsf(__uint_as_float(w[j] & 0xFFFF0000u));
-      top = fmaxf(top, y0 < INFINITY ? y0 : 0.f);
-      top = fmaxf(top, y1 < INFINITY ? y1 : 0.f);
+    for (int i = 0; i < NP; ++i) {
+      const int32_t t = i * TP + tok;
+      x[v][i] = make_uint4(0, 0, 0, 0);
+      if (t >= low && t < high) x[v][i] = *reinterpret_cast<const uint4*>(src + (entry0 + t) * a.kv_heads * D);
     }
   }
-  top = lanes_reduce<kWave, true>(top);
-  if (lane_id() == 0) tops[threadIdx.x / kWave] = top;
-  float* scale = a.scale[which] + slot0 / a.B;
-  const float had = low > 0 ? *scale : 0.f;
-  __syncthreads();
-  float unit = block_scale(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])));
-  const bool grown = low > 0 && had < unit;
-  if (low > 0 && had > unit) unit = had;
-  const float inv = 1.f / unit;  // exact
-  uint8_t* dst = a.pages_of[which] + slot0 * D + lane * 8;
+  if (page < 0 || page >= a.pages) return;
+  const int64_t slot0 = (static_cast<int64_t>(page) * a.kv_heads + head) * a.P + (p0 - static_cast<int64_t>(e) * a.P);
+  float had[KV];
 #pragma unroll
-  for (int i = 0; i < NP; ++i) {
-    const int32_t t = i * TP + tok;
-    if (t >= low && t < high) {
-      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-      float y[8];
+  for (int v = 0; v < KV; ++v) {
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const uint32_t w[4] = {x[v][i].x, x[v][i].y, x[v][i].z, x[v][i].w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        y[2 * j] = __uint_as_float(w[j] << 16);
-        y[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+        const float y0 = fabsf(__uint_as_float(w[j] << 16)), y1 = fabsf(__uint_as_float(w[j] & 0xFFFF0000u));
+        top = fmaxf(top, y0 < INFINITY ? y0 : 0.f);
+        top = fmaxf(top, y1 < INFINITY ? y1 : 0.f);
       }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = fabsf(y[j]) < INFINITY ? y[j] : NAN;
-      *reinterpret_cast<uint2*>(dst + static_cast<int64_t>(t) * D) =
-          make_uint2(e4m3_pack4(y[0], y[1], y[2], y[3], inv), e4m3_pack4(y[4], y[5], y[6], y[7], inv));
     }
-    if (grown && t < low) {  // earlier tokens, to the larger scale
-      uint2* old = reinterpret_cast<uint2*>(dst + static_cast<int64_t>(t) * D);
-      const uint2 z = *old;
-      const float f = had * inv;
-      uint32_t c[2] = {z.x, z.y};
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        c[j] = e4m3_pack4(fp8_to_f32(c[j]), __builtin_amdgcn_cvt_f32_fp8(c[j], 1),
-                          __builtin_amdgcn_cvt_f32_fp8(c[j], 2), __builtin_amdgcn_cvt_f32_fp8(c[j], 3), f);
-      *old = make_uint2(c[0], c[1]);
-    }
+    top = lanes_reduce<kWave, true>(top);
+    if (lane_id() == 0) tops[v][threadIdx.x / kWave] = top;
+    had[v] = low > 0 ? a.scale[KV == 1 ? blockIdx.z : v][slot0 >> a.shift] : 0.f;
   }
-  if (threadIdx.x == 0) *scale = unit;
+  __syncthreads();
+#pragma unroll
+  for (int v = 0; v < KV; ++v) {
+    const int which = KV == 1 ? blockIdx.z : v;
+    float unit = block_scale(fmaxf(fmaxf(tops[v][0], tops[v][1]), fmaxf(tops[v][2], tops[v][3])));
+    const bool grown = low > 0 && had[v] < unit;
+    if (low > 0 && had[v] > unit) unit = had[v];
+    const float inv = 1.f / unit;  // exact
+    uint8_t* dst = a.pages_of[which] + slot0 * D + lane * 8;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const int32_t t = i * TP + tok;
+      if (t >= low && t < high) {
+        const uint32_t w[4] = {x[v][i].x, x[v][i].y, x[v][i].z, x[v][i].w};
+        float y[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          y[2 * j] = __uint_as_float(w[j] << 16);
+          y[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = fabsf(y[j]) < INFINITY ? y[j] : NAN;
+        *reinterpret_cast<uint2*>(dst + static_cast<int64_t>(t) * D) =
+            make_uint2(e4m3_pack4(y[0], y[1], y[2], y[3], inv), e4m3_pack4(y[4], y[5], y[6], y[7], inv));
+      }
+      if (grown && t < low) {  // earlier tokens, to the larger scale
+        uint2* old = reinterpret_cast<uint2*>(dst + static_cast<int64_t>(t) * D);
+        const uint2 z = *old;
+        const float f = had[v] * inv;
+        uint32_t c[2] = {z.x, z.y};
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          c[j] = e4m3_pack4(fp8_to_f32(c[j]), __builtin_amdgcn_cvt_f32_fp8(c[j], 1),
+                            __builtin_amdgcn_cvt_f32_fp8(c[j], 2), __builtin_amdgcn_cvt_f32_fp8(c[j], 3), f);
+        *old = make_uint2(c[0], c[1]);
+      }
+    }
+    if (threadIdx.x == 0) a.scale[which][slot0 >> a.shift] = unit;
+  }
+}
+
+template <int D, int NP>
+void launch_write_rounds(const WriteArgs& a, uint32_t units, int32_t parts, hipStream_t st) {
+  if (NP <= 4 && parts == 2)
+    block_write_kernel<D, NP, NP <= 4 ? 2 : 1><<<dim3(units, a.kv_heads), 256, 0, st>>>(a);
+  else
+    block_write_kernel<D, NP, 1><<<dim3(units, a.kv_heads, parts), 256, 0, st>>>(a);
 }
 
 template <int D>
 hipError_t launch_write_dim(const WriteArgs& a, uint32_t units, int32_t parts, hipStream_t st) {
-  const dim3 grid(units, a.kv_heads, parts);
-  const int rounds = std::max(1, a.B * (D / 8) / 256);
-  if (rounds == 1) block_write_kernel<D, 1><<<grid, 256, 0, st>>>(a);
-  if (rounds == 2) block_write_kernel<D, 2><<<grid, 256, 0, st>>>(a);
-  if (rounds == 4) block_write_kernel<D, 4><<<grid, 256, 0, st>>>(a);
+  const int rounds = std::max(1, (D / 8 << a.shift) / 256);
+  if (rounds == 1) launch_write_rounds<D, 1>(a, units, parts, st);
+  if (rounds == 2) launch_write_rounds<D, 2>(a, units, parts, st);
+  if (rounds == 4) launch_write_rounds<D, 4>(a, units, parts, st);
   if constexpr (D >= 128)
-    if (rounds == 8) block_write_kernel<D, 8><<<grid, 256, 0, st>>>(a);
+    if (rounds == 8) launch_write_rounds<D, 8>(a, units, parts, st);
   if constexpr (D >= 256)
-    if (rounds == 16) block_write_kernel<D, 16><<<grid, 256, 0, st>>>(a);
+    if (rounds == 16) launch_write_rounds<D, 16>(a, units, parts, st);
   return hipGetLastError();
 }
 
@@ -164,14 +184,28 @@ struct ReadArgs {
   const float* scale[2];
   void* out[2];
   float* out_scale[2];
-  int32_t row_pages, pages, P, kv_heads, B;
+  int32_t row_pages, pages, P, kv_heads, shift;  // 2^shift tokens a block
 };
 
+template <bool ONCE>
+__device__ __forceinline__ uint4 get(const uint8_t* p) {
+  const u32x4* q = reinterpret_cast<const u32x4*>(p);
+  return __builtin_bit_cast(uint4, ONCE ? __builtin_nontemporal_load(q) : *q);
+}
+template <bool ONCE, typename V>
+__device__ __forceinline__ void put(void* p, const V& x) {
+  const u32x4 y = __builtin_bit_cast(u32x4, x);
+  if constexpr (ONCE)
+    __builtin_nontemporal_store(y, static_cast<u32x4*>(p));
+  else
+    *static_cast<u32x4*>(p) = y;
+}
+
 // 16 codes -> 16 values of OUT at `dst`.
-template <int OUT>
+template <int OUT, bool ONCE>
 __device__ __forceinline__ void put16(void* dst, int64_t at, uint4 c, float scale) {
   if constexpr (OUT == kFP8) {
-    *reinterpret_cast<uint4*>(static_cast<uint8_t*>(dst) + at) = c;
+    put<ONCE>(static_cast<uint8_t*>(dst) + at, c);
   } else {
     const uint32_t w[4] = {c.x, c.y, c.z, c.w};
     float y[16];
@@ -183,9 +217,9 @@ __device__ __forceinline__ void put16(void* dst, int64_t at, uint4 c, float scal
       y[4 * j + 3] = __builtin_amdgcn_cvt_f32_fp8(w[j], 3) * scale;
     }
     if constexpr (OUT == kF32) {
-      float4* o = reinterpret_cast<float4*>(static_cast<float*>(dst) + at);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) o[j] = make_float4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
+      for (int j = 0; j < 4; ++j)
+        put<ONCE>(static_cast<float*>(dst) + at + 4 * j, make_float4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]));
     } else {
       typedef __attribute__((ext_vector_type(8))) __bf16 B8;
       B8 lo, hi;
@@ -194,18 +228,21 @@ __device__ __forceinline__ void put16(void* dst, int64_t at, uint4 c, float scal
         lo[j] = static_cast<__bf16>(y[j]);
         hi[j] = static_cast<__bf16>(y[8 + j]);
       }
-      uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(dst) + at);
-      o[0] = __builtin_bit_cast(uint4, lo);
-      o[1] = __builtin_bit_cast(uint4, hi);
+      put<ONCE>(static_cast<uint16_t*>(dst) + at, lo);
+      put<ONCE>(static_cast<uint16_t*>(dst) + at + 8, hi);
     }
   }
 }
 
-constexpr int kReadRounds = 4;
+constexpr int kReadRounds = 2;
 
-// D / 16 lanes per (packed token, kv head), 16 codes each, and four of those a
-// lane, whose loads are under way together.
-template <int D, int OUT>
+// D / 16 lanes per (packed token, kv head), 16 codes each, and two of those a lane,
+// whose loads are under way together.  The row of a workgroup's tokens, mostly one,
+// is looked up once: a lookup each cost 8 rows of 131072 keys (213 MB) 20 of 70 us.
+// Bound by HBM traffic, 5.1 TB/s there.
+//
+// ONCE: much is moved, and marked as not to be kept (41.7 us there, 47.1 without).
+template <int D, int OUT, bool ONCE>
 __global__ __launch_bounds__(256) void block_read_kernel(ReadArgs a) {
   constexpr int LPR = D / 16, IP = 256 / LPR;  // lanes of an item, items of a round
   const int which = blockIdx.y;
@@ -222,6 +259,22 @@ __global__ __launch_bounds__(256) void block_read_kernel(ReadArgs a) {
   uint4 code[kReadRounds];
   float unit[kReadRounds];
   int64_t item[kReadRounds];
+  const auto fetch = [&](int i, int32_t r, int32_t t, int32_t head, int32_t begin, int32_t end, int32_t first, int32_t len)
+                         __attribute__((always_inline)) {
+    if (t < begin || t >= end) {  // padding
+      item[i] = -1;
+      return;
+    }
+    const int64_t p = static_cast<int64_t>(first) + (t - begin);
+    if (p < 0 || p >= len || p >= static_cast<int64_t>(a.row_pages) * a.P) return;
+    const uint32_t e = static_cast<uint32_t>(p) / static_cast<uint32_t>(a.P);
+    const int32_t page = a.table[static_cast<int64_t>(r) * a.row_pages + e];
+    if (page < 0 || page >= a.pages) return;
+    const int64_t slot = (static_cast<int64_t>(page) * a.kv_heads + head) * a.P + (p - static_cast<int64_t>(e) * a.P);
+    code[i] = get<ONCE>(a.pages_of[which] + slot * D + lane * 16);
+    unit[i] = a.scale[which][static_cast<uint32_t>(slot) >> a.shift];
+  };
+  const int32_t begin0 = a.rows.at(r0), end0 = a.rows.at(r0 + 1), first0 = a.first ? a.first[r0] : 0, len0 = a.lengths[r0];
 #pragma unroll
   for (int i = 0; i < kReadRounds; ++i) {
     item[i] = item0 + i * IP + threadIdx.x / LPR;
@@ -233,6 +286,10 @@ __global__ __launch_bounds__(256) void block_read_kernel(ReadArgs a) {
     }
     const int32_t t = static_cast<int32_t>(static_cast<uint32_t>(item[i]) / static_cast<uint32_t>(a.kv_heads));
     const int32_t head = static_cast<int32_t>(item[i] - static_cast<int64_t>(t) * a.kv_heads);
+    if (r0 == r1) {  // uniform: the row's numbers are there already
+      fetch(i, r0, t, head, begin0, end0, first0, len0);
+      continue;
+    }
     int32_t lo = r0, hi = r1;  // the last row whose entries begin at or before t
     while (lo < hi) {
       const int32_t mid = lo + (hi - lo + 1) / 2;
@@ -241,39 +298,37 @@ __global__ __launch_bounds__(256) void block_read_kernel(ReadArgs a) {
       else
         hi = mid - 1;
     }
-    const int32_t begin = a.rows.at(lo);
-    if (t < begin || t >= a.rows.at(lo + 1)) {  // padding
-      item[i] = -1;
-      continue;
-    }
-    const int64_t p = static_cast<int64_t>(a.first ? a.first[lo] : 0) + (t - begin);
-    if (p < 0 || p >= a.lengths[lo] || p >= static_cast<int64_t>(a.row_pages) * a.P) continue;
-    const uint32_t e = static_cast<uint32_t>(p) / static_cast<uint32_t>(a.P);
-    const int32_t page = a.table[static_cast<int64_t>(lo) * a.row_pages + e];
-    if (page < 0 || page >= a.pages) continue;
-    const int64_t slot = (static_cast<int64_t>(page) * a.kv_heads + head) * a.P + (p - static_cast<int64_t>(e) * a.P);
-    code[i] = *reinterpret_cast<const uint4*>(a.pages_of[which] + slot * D + lane * 16);
-    unit[i] = a.scale[which][static_cast<uint32_t>(slot) / static_cast<uint32_t>(a.B)];
+    fetch(i, lo, t, head, a.rows.at(lo), a.rows.at(lo + 1), a.first ? a.first[lo] : 0, a.lengths[lo]);
   }
 #pragma unroll
   for (int i = 0; i < kReadRounds; ++i) {
     if (item[i] < 0) continue;
-    put16<OUT>(a.out[which], item[i] * D + lane * 16, code[i], unit[i]);
+    put16<OUT, ONCE>(a.out[which], item[i] * D + lane * 16, code[i], unit[i]);
     if (OUT == kFP8 && lane == 0) a.out_scale[which][item[i]] = unit[i];
   }
 }
 
-template <int D>
-hipError_t launch_read_dim(const ReadArgs& a, int32_t out_dtype, int32_t parts, hipStream_t st) {
+constexpr int64_t kReadOnceBytes = int64_t{32} << 20;
+
+template <int D, int OUT>
+hipError_t launch_read_out(const ReadArgs& a, int32_t parts, hipStream_t st) {
   const int64_t items = static_cast<int64_t>(a.rows.n) * a.kv_heads;  // at most 2^28
   const int per = 256 / (D / 16) * kReadRounds;
   const dim3 grid(static_cast<uint32_t>((items + per - 1) / per), parts);
-  switch (out_dtype) {
-    case kF32: block_read_kernel<D, kF32><<<grid, 256, 0, st>>>(a); break;
-    case kBF16: block_read_kernel<D, kBF16><<<grid, 256, 0, st>>>(a); break;
-    default: block_read_kernel<D, kFP8><<<grid, 256, 0, st>>>(a); break;
-  }
+  if (items * D * parts * (1 + elem_bytes<OUT>()) >= kReadOnceBytes)
+    block_read_kernel<D, OUT, true><<<grid, 256, 0, st>>>(a);
+  else
+    block_read_kernel<D, OUT, false><<<grid, 256, 0, st>>>(a);
   return hipGetLastError();
+}
+
+template <int D>
+hipError_t launch_read_dim(const ReadArgs& a, int32_t out_dtype, int32_t parts, hipStream_t st) {
+  switch (out_dtype) {
+    case kF32: return launch_read_out<D, kF32>(a, parts, st);
+    case kBF16: return launch_read_out<D, kBF16>(a, parts, st);
+    default: return launch_read_out<D, kFP8>(a, parts, st);
+  }
 }
 
 }  // namespace
@@ -296,8 +351,8 @@ hipError_t launch_block_write(const Cache& c, int32_t block, int32_t n, const in
   a.pages = c.pages;
   a.P = c.P;
   a.kv_heads = c.kv_heads;
-  a.B = block;
-  const int64_t blocks = unit_base(n, 1, block, c.rows, 2);
+  a.shift = __builtin_ctz(static_cast<uint32_t>(block));
+  const int64_t blocks = unit_base(n, 1, a.shift, c.rows, 2);
   a.by_token = n <= blocks;
   const uint32_t units = static_cast<uint32_t>(a.by_token ? n : blocks);
   const int32_t parts = v_pages ? 2 : 1;
@@ -330,7 +385,7 @@ hipError_t launch_block_read(const Cache& c, int32_t block, int32_t n, int32_t o
   a.pages = c.pages;
   a.P = c.P;
   a.kv_heads = c.kv_heads;
-  a.B = block;
+  a.shift = __builtin_ctz(static_cast<uint32_t>(block));
   const int32_t parts = v_pages ? 2 : 1;
   switch (c.dk) {
     case 64: return launch_read_dim<64>(a, out_dtype, parts, st);

@@ -39,12 +39,13 @@ __device__ __forceinline__ bool row_of_entry(const Packed& p, int32_t i, int32_t
   return i >= begin && i < end;
 }
 
-// Units of `size` entries each, where a row whose entries touch at most
-// floor(c * times / size) + spare units has unit_base(r + 1) - unit_base(r) of
-// them, and the rows' units follow one another: no prefix sum is needed.
-__host__ __device__ __forceinline__ int64_t unit_base(int64_t entries, int32_t times, int32_t size,
+// Units of 2^shift entries each (entries times `times`), where a row whose c entries
+// touch at most floor(c * times / 2^shift) + spare units has unit_base(r + 1) -
+// unit_base(r) of them, and the rows' units follow one another: no prefix sum is
+// needed.
+__host__ __device__ __forceinline__ int64_t unit_base(int64_t entries, int32_t times, int32_t shift,
                                                       int32_t r, int32_t spare) {
-  return entries * times / size + static_cast<int64_t>(r) * spare;
+  return (entries * times >> shift) + static_cast<int64_t>(r) * spare;
 }
 
 }  // namespace misa
