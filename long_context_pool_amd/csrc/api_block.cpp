@@ -50,10 +50,13 @@ misa_status check_block_attend(const misa_cache* cache, int32_t heads, misa::Blo
   return MISA_OK;
 }
 
+// One query at a time where each has a list of its own, or a row has one new token;
+// otherwise tiles of a row's queries share its keys and values.
+bool one_by_one(const misa::BlockAttend& b) { return b.k > 0 || b.most <= 1; }
 
 size_t attend_need(const Cache& c, const misa::BlockAttend& b) {
   if (b.n == 0) return 0;
-  return misa::queries_together(c, b) > 0 ? misa::attend_queries_ws_bytes(c, b) : misa::attend_tiles_ws_bytes(c, b);
+  return one_by_one(b) ? misa::attend_queries_ws_bytes(c, b) : misa::attend_tiles_ws_bytes(c, b);
 }
 
 }  // namespace
@@ -205,7 +208,7 @@ misa_status misa_block_attend(const misa_cache* cache, int32_t block_tokens, int
   MISA_TRY(check_out(out, true));
   MISA_TRY(check_out(lse, false));
   MISA_TRY(check_ws(ws, ws_bytes, attend_need(c, b)));
-  return from_hip(misa::queries_together(c, b) > 0 ? misa::launch_attend_queries(c, b, stream)
+  return from_hip(one_by_one(b) ? misa::launch_attend_queries(c, b, stream)
                                 : misa::launch_attend_tiles(c, b, stream));
 }
 

@@ -77,10 +77,7 @@ __device__ __forceinline__ int value_dim(int c, int j) {
 // against 505 us).
 //
 // PACKED (misa_block_attend): a unit is a query of a packed batch instead of a row,
-// and the scales are those of blocks of tokens.  Where a row has several new tokens, a
-// few of them share its cache as further query heads would: `heads` below are (query,
-// head) pairs, each with its own last token; the workgroups of a group's other queries
-// leave at once.
+// and the scales are those of blocks of tokens.
 template <int D, int DT, int RT, bool ONCE, bool PACKED>
 __global__ __launch_bounds__(256) void attend_kernel(Args a) {
   constexpr int EB = DT == kFP8 ? 1 : 2;
@@ -103,7 +100,6 @@ __global__ __launch_bounds__(256) void attend_kernel(Args a) {
   };
   __shared__ __attribute__((aligned(16))) Shared sh;
   __shared__ float top[4][RT][16];
-  __shared__ int any_nan;  // in values of tokens that some of the queries do not see
 
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int c = lane & 15, g = lane >> 4;
@@ -113,14 +109,10 @@ __global__ __launch_bounds__(256) void attend_kernel(Args a) {
   const int split = unit % a.splits;
   const int kvh = unit / a.splits % a.kv_heads, row = unit / a.splits / a.kv_heads;
   if (row >= a.rows) return;
-  Query query;
-  if (!query_of<PACKED>(a, row, query) || query.first != row) return;
   const int head0 = kvh * a.share + chunk * 16 * RT;       // first query head
-  const int nheads = min(16 * RT, query.count * a.share - chunk * 16 * RT);
-  const auto pair_at = [&](int h) {  // (query, query head) h of the workgroup's in q, lse and out
-    const int t = PACKED ? div_page(chunk * 16 * RT + h, a.by_share) : 0;
-    return (static_cast<int64_t>(row) + t) * a.heads + head0 + h - t * a.share;
-  };
+  const int nheads = min(16 * RT, a.share - chunk * 16 * RT);
+  Query query;
+  if (!query_of<PACKED>(a, row, query)) return;
   const int32_t todo = tokens_of(a, query);
   const int32_t per = tiles_per_split(a, todo) * kTileTokens;
   const int32_t t0 = split * per, t1 = min(t0 + per, todo);
@@ -131,7 +123,7 @@ __global__ __launch_bounds__(256) void attend_kernel(Args a) {
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
     const int h = r * 16 + c;
-    const uint16_t* src = a.q + pair_at(h < nheads ? h : 0) * D;
+    const uint16_t* src = a.q + (static_cast<int64_t>(row) * a.heads + head0 + (h < nheads ? h : 0)) * D;
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
       const int d0 = kFp8 ? 64 * (s / 2) + 16 * g + 8 * (s % 2) : 32 * s + 8 * g;
@@ -141,10 +133,8 @@ __global__ __launch_bounds__(256) void attend_kernel(Args a) {
 
   f32x4 acc[RT][NJ];
   float m[RT], l[RT];  // reference maximum of the head (all lanes alike), this lane's part of the sum
-  int32_t end[RT];     // one past its last token
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
-    end[r] = PACKED ? query.first_seen + static_cast<int32_t>(div_page(chunk * 16 * RT + r * 16 + c, a.by_share)) : 0;
     m[r] = -INFINITY;
     l[r] = 0.f;
 #pragma unroll
@@ -180,13 +170,12 @@ __global__ __launch_bounds__(256) void attend_kernel(Args a) {
     }
   };
 
-  if (PACKED && threadIdx.x == 0) any_nan = 0;  // read behind the next barrier
   for (int32_t base = t0; base < t1; base += kStage) {
     const int32_t count = min(kStage, t1 - base);
     const int32_t tiles = (count + kTileTokens - 1) / kTileTokens;
     if (base != t0) __syncthreads();
     for (int32_t i = threadIdx.x; i < tiles * kTileTokens; i += 256) {
-      const uint32_t s = i < count ? slot_of(a, row, query.table_row, kvh, PACKED ? query.last_len : query.len, base + i) : kHidden;
+      const uint32_t s = i < count ? slot_of(a, row, query.table_row, kvh, query.len, base + i) : kHidden;
       sh.st.slot[i] = s;
       if constexpr (kFp8) {
         const uint32_t unit = PACKED ? s >> a.shift : s;  // pages are whole blocks
@@ -237,9 +226,6 @@ __global__ __launch_bounds__(256) void attend_kernel(Args a) {
       bool hidden = false;
 #pragma unroll
       for (int i = 0; i < 8; ++i) hidden |= sl[i] == kHidden;
-      // Tokens of a tile that some of the queries do not see yet.
-      const int32_t token0 = base + tile * 32 + 4 * g;  // this lane's: token0 + i % 4 + i / 4 * 16
-      const bool edge = PACKED && !a.idx && query.count > 1 && base + tile * 32 + 32 > query.len;
       bf16x8 ph[RT], pl[RT];
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
@@ -249,8 +235,6 @@ __global__ __launch_bounds__(256) void attend_kernel(Args a) {
           float y = st[r][i / 4][i % 4] * a.scale2;
           if constexpr (kFp8) y *= ks[i];
           x[i] = sl[i] == kHidden ? -INFINITY : y;
-          if constexpr (PACKED)
-            if (edge) x[i] = token0 + i % 4 + i / 4 * 16 < end[r] ? x[i] : -INFINITY;
           high = fmaxf(high, x[i]);
         }
         if (__any(high > m[r] + kSlack)) {  // wave-uniform
@@ -277,18 +261,6 @@ __global__ __launch_bounds__(256) void attend_kernel(Args a) {
         for (int i = 0; i < 8; ++i)
 #pragma unroll
           for (int u = 0; u < VW; ++u) vreg[i][u] = sl[i] == kHidden ? 0u : vreg[i][u];
-      }
-      if constexpr (PACKED) {
-        if (edge) {  // NaN of a token must not meet the weights, zero, of queries before it
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-#pragma unroll
-            for (int u = 0; u < VW; ++u) {
-              const uint32_t bad = token0 + i % 4 + i / 4 * 16 < query.len ? 0u : nan_bytes(vreg[i][u]);
-              if (bad) any_nan = 1;
-              vreg[i][u] &= ~bad;
-            }
-        }
       }
 #pragma unroll
       for (int u = 0; u < VW; ++u) {
@@ -359,27 +331,11 @@ __global__ __launch_bounds__(256) void attend_kernel(Args a) {
     __syncthreads();
   }
   if (wave != 0) return;
-  if constexpr (PACKED) {
-    if (t0 < t1 && any_nan) {  // the NaN values left out above, for the queries that see them
-      for (int32_t s = max(t0, query.len); s < t1; ++s) {
-        const uint32_t slot = slot_of(a, row, query.table_row, kvh, query.last_len, s);
-        if (slot == kHidden) continue;
-        const uint8_t* v = a.v_pages + static_cast<uint64_t>(slot) * ROW;
-#pragma unroll
-        for (int r = 0; r < RT; ++r)
-#pragma unroll
-          for (int j = 0; j < NJ; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              acc[r][j][e] = s < end[r] && (v[value_dim<D, DT>(4 * g + e, j)] & 0x7F) == 0x7F ? NAN : acc[r][j][e];
-      }
-    }
-  }
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
     const int h = r * 16 + c;
     if (h >= nheads) continue;
-    const int64_t at = pair_at(h);
+    const int64_t at = static_cast<int64_t>(row) * a.heads + head0 + h;
     if (a.splits == 1) {
       const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];
       if (g == 0 && a.lse) a.lse[at] = l[r] == 0.f ? -INFINITY : final_lse(mall[r], l[r]);
@@ -413,18 +369,15 @@ int32_t tiles_at_once(const Cache& c) { return c.latent() ? 2 : 4; }
 // more and the registers hold them (8 rows of 8000 bf16 tokens of 8 heads of 128,
 // 256 query heads: 49.7 us with 32, 58.2 with 16; heads of 64 31.3 and 30.3, fp8
 // 24.8 and 25.8).
-// Several queries of a packed batch have up to 48 pairs with the query heads, so that
-// they read the cache once.
-int group_heads(const Cache& c, int32_t share, bool queries) {
+int group_heads(const Cache& c, int32_t share) {
   if (c.latent()) return kLatentHeads;
-  if (queries && share > 32 && c.dk <= 128) return 48;
   return share > 16 && c.dk <= 128 ? 32 : 16;
 }
 
 // Workgroups that a CU holds at a time, by the kernels' registers.
-int resident(const Cache& c, int32_t per) {
+int resident(const Cache& c, int32_t share) {
   const int one = c.dk == 64 ? 4 : c.dk == 128 ? 3 : 2;
-  return per == 48 ? 2 : per == 32 ? one - 1 : one;
+  return group_heads(c, share) == 32 ? one - 1 : one;
 }
 
 constexpr int kCus = 256;
@@ -464,13 +417,13 @@ int32_t latent_splits(int64_t groups, int64_t tokens, int64_t heads, int64_t lim
 // and 24.1 us; one row of 2000, 64 heads on 8, 9.7 us in sixteen, 24.8 us whole.
 // Groups beyond half of one round stay whole: 8 fp8 heads, rows of 32768 tokens, 48
 // rows in two splits 539 us, 49 rows whole 632 us.
-int32_t dense_splits(const Cache& c, int32_t heads, int32_t per_group, int64_t groups, int64_t tokens,
+int32_t dense_splits(const Cache& c, int32_t heads, int32_t share, int64_t groups, int64_t tokens,
                      int64_t limit) {
-  const int32_t held = resident(c, per_group);
+  const int32_t held = resident(c, share);
   const int64_t most = std::min<int64_t>(kCus * held / groups, limit);
   const int32_t all = static_cast<int32_t>((tokens + kTileTokens - 1) / kTileTokens);
   const int32_t tile_bytes = kTileTokens * (c.dk + c.dv) * (c.dtype == kFP8 ? 1 : 2);
-  const double each = tile_bytes * 8.5e-5 + per_group * c.dk * 1e-4;
+  const double each = tile_bytes * 8.5e-5 + group_heads(c, share) * c.dk * 1e-4;
   const double sums = 3.3e-6 * c.rows * heads * c.dk;
   int32_t best = 1;
   double least = 0;
@@ -487,7 +440,7 @@ int32_t dense_splits(const Cache& c, int32_t heads, int32_t per_group, int64_t g
 }
 
 struct Plan {
-  int32_t chunks, splits, per;  // per: query heads of a workgroup
+  int32_t chunks, splits;
   bool once;
 };
 
@@ -496,11 +449,10 @@ struct Plan {
 // are not kept.
 constexpr int64_t kOnceBytes = int64_t{64} << 20;
 
-Plan plan(const Cache& c, int32_t heads, int32_t k, bool queries = false) {
+Plan plan(const Cache& c, int32_t heads, int32_t k) {
   const int32_t share = heads / c.kv_heads;
-  const int32_t per = group_heads(c, share, queries);
+  const int32_t per = group_heads(c, share);
   Plan p;
-  p.per = per;
   p.chunks = (share + per - 1) / per;
   const int64_t groups = static_cast<int64_t>(c.rows) * c.kv_heads * p.chunks;
   const int64_t most = k > 0 ? k : static_cast<int64_t>(c.row_pages) * c.P;
@@ -509,7 +461,7 @@ Plan plan(const Cache& c, int32_t heads, int32_t k, bool queries = false) {
   if (c.latent()) {
     p.splits = latent_splits(groups, most, static_cast<int64_t>(c.rows) * heads, limit);
   } else {
-    p.splits = dense_splits(c, heads, per, groups, most, limit);
+    p.splits = dense_splits(c, heads, share, groups, most, limit);
   }
   const int64_t row_bytes = static_cast<int64_t>(c.dk + c.dv) * (c.dtype == kFP8 ? 1 : 2);
   p.once = p.chunks == 1 && c.rows * most * c.kv_heads * row_bytes >= kOnceBytes;
@@ -532,9 +484,7 @@ void launch_rows(const Cache& c, const Args& a, const Plan& p, hipStream_t st) {
 template <int D, int DT, bool PACKED>
 hipError_t launch_dim(const Cache& c, const Args& a, const Plan& p, hipStream_t st) {
   if constexpr (D <= 128) {
-    if (PACKED && p.per == 48)
-      launch_rows<D, DT, PACKED ? 3 : 2, PACKED>(c, a, p, st);
-    else if (p.per == 32)
+    if (group_heads(c, a.share) == 32)
       launch_rows<D, DT, 2, PACKED>(c, a, p, st);
     else
       launch_rows<D, DT, 1, PACKED>(c, a, p, st);
@@ -591,30 +541,11 @@ Args make_args(const Cache& c, int32_t heads, int32_t k, float scale, const Plan
   return a;
 }
 
-}  // namespace
-
-// The queries of a row that are worked on together: all of them where a workgroup
-// holds their pairs with the query heads, one with a list of its own or alone; 0: too many.
-int32_t queries_together(const Cache& c, const BlockAttend& b) {
-  if (b.k > 0 || b.most <= 1) return 1;
-  const int64_t pairs = static_cast<int64_t>(b.most) * (b.heads / c.kv_heads);
-  return pairs <= (c.dk <= 128 ? 48 : 16) ? b.most : 0;
-}
-
-namespace {
-
-// A packed batch as the plan sees it: a row for each group of queries, whose (query,
-// head) pairs are its heads.
-struct Groups {
-  Cache cache;
-  int32_t heads, together;
-};
-
-Groups groups_of(const Cache& c, const BlockAttend& b) {
-  Groups g{c, b.heads, queries_together(c, b)};
-  g.heads *= g.together;
-  g.cache.rows = (b.n - 1) / g.together + 1;
-  return g;
+// The cache as queries of a packed batch see it: a row each.
+Cache with_rows(const Cache& c, int32_t n) {
+  Cache queries = c;
+  queries.rows = n;
+  return queries;
 }
 
 }  // namespace
@@ -639,23 +570,19 @@ hipError_t launch_attend(const Cache& c, int32_t heads, int32_t k, float scale, 
 }
 
 size_t attend_queries_ws_bytes(const Cache& c, const BlockAttend& b) {
-  const Groups g = groups_of(c, b);
-  return parts_bytes(g.cache, g.heads, plan(g.cache, g.heads, b.k, g.together > 1));
+  const Cache queries = with_rows(c, b.n);
+  return parts_bytes(queries, b.heads, plan(queries, b.heads, b.k));
 }
 
 hipError_t launch_attend_queries(const Cache& c, const BlockAttend& b, hipStream_t st) {
-  const Groups g = groups_of(c, b);
-  Plan p = plan(g.cache, g.heads, b.k, g.together > 1);
-  p.once &= b.k == 0;  // lists of one row's queries share its cache
-  Cache queries = c;
-  queries.rows = b.n;
+  const Cache queries = with_rows(c, b.n);
+  Plan p = plan(queries, b.heads, b.k);
+  p.once &= b.most <= 1;  // queries of one row share its cache
   Args a = make_args(queries, b.heads, b.k, b.scale, p, b.q, b.k_pages, b.k_scale, b.v_pages,
                      b.v_scale, b.table, b.lengths, b.idx, b.out, b.lse, b.ws);
   a.offsets = b.offsets;
   a.table_rows = c.rows;
   a.shift = __builtin_ctz(static_cast<uint32_t>(b.block));
-  a.together = g.together;
-  a.by_share = make_div(a.share);
   switch (c.dk) {
     case 64: return launch_dim<64, kFP8, true>(queries, a, p, st);
     case 128: return launch_dim<128, kFP8, true>(queries, a, p, st);

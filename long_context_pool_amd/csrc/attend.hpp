@@ -54,19 +54,15 @@ struct Args {
   int32_t tiles;  // that a workgroup works on at a time, a power of two
   float scale2;  // scale * log2(e): softmax by powers of two
   Div div;
-  // Queries of a packed batch (misa_block_attend): `rows` above counts queries, 2^shift
-  // tokens share a scale, and `together` queries of a row are worked on at a time.
+  // Queries of a packed batch (misa_block_attend): `rows` above counts queries, and
+  // 2^shift tokens share a scale.
   const int32_t* offsets;
-  int32_t table_rows, shift, together;
-  Div by_share;
+  int32_t table_rows, shift;
 };
 
-// What a query sees: row `table_row` of the table, its first `len` tokens.  Of the
-// `count` queries that are worked on together, query `first` and those behind it, each
-// sees one more: `first_seen` (below zero: more new tokens than the row has) to
-// `last_len`.
+// What one query sees: row `table_row` of the table, its first `len` tokens.
 struct Query {
-  int32_t table_row, len, first, count, first_seen, last_len;
+  int32_t table_row, len;
 };
 
 // Query i; false if no row has it.  PACKED: the new tokens of a row are its last
@@ -77,27 +73,18 @@ __device__ __forceinline__ bool query_of(const Args& a, int i, Query& q) {
   if constexpr (PACKED) {
     int32_t begin, end;
     if (!row_of_entry(Packed{a.offsets, a.table_rows, a.rows}, i, q.table_row, begin, end)) return false;
-    const int64_t len = max(a.lengths[q.table_row], 0);
-    const auto seen_by = [&](int32_t x) {
-      const int64_t seen = len - (end - 1 - x);
-      return static_cast<int32_t>(seen < cap ? seen : cap);
-    };
-    q.first = i - (i - begin) % a.together;
-    q.count = min(a.together, end - q.first);
-    q.len = max(seen_by(i), 0);
-    q.first_seen = seen_by(q.first);
-    q.last_len = max(seen_by(q.first + q.count - 1), 0);
+    const int64_t seen = static_cast<int64_t>(a.lengths[q.table_row]) - (end - 1 - i);
+    q.len = static_cast<int32_t>(seen < 0 ? 0 : seen < cap ? seen : cap);
   } else {
-    q.table_row = q.first = i;
-    q.count = 1;
-    q.len = q.first_seen = q.last_len = min(max(a.lengths[i], 0), cap);
+    q.table_row = i;
+    q.len = min(max(a.lengths[i], 0), cap);
   }
   return true;
 }
 
-// Tokens that a query (with a list, one alone) looks at, and the pool slot of the t-th of them.
+// Tokens that a query looks at, and the pool slot of the t-th of them.
 __device__ __forceinline__ int32_t tokens_of(const Args& a, const Query& q) {
-  return a.idx ? (q.len > 0 ? a.k : 0) : q.last_len;
+  return a.idx ? (q.len > 0 ? a.k : 0) : q.len;
 }
 
 __device__ __forceinline__ uint32_t slot_of(const Args& a, int row, int table_row, int kvh, int32_t len, int32_t t) {
@@ -136,11 +123,6 @@ __device__ __forceinline__ bf16x8 fp8x8_to_bf16(uint32_t lo, uint32_t hi) {
   r.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, false));
   r.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, true));
   return as_bf16x8(r);
-}
-
-// 0xFF for each of four codes that is NaN.
-__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
-  return ((((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7) * 0xFFu;
 }
 
 // What the sums of a part with maximum m and sum l count under the common

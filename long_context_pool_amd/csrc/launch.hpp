@@ -197,9 +197,7 @@ struct BlockAttend {  // the arguments of misa_block_attend
   float* lse;
   void* ws;
 };
-// One query at a time, or a few of a row (attend.hip), or tiles of a row's queries
-// (attend_block.hip).
-int32_t queries_together(const Cache& c, const BlockAttend& b);  // 0: only as tiles
+// One query at a time (attend.hip), or tiles of a row's queries (attend_block.hip).
 size_t attend_queries_ws_bytes(const Cache& c, const BlockAttend& b);
 hipError_t launch_attend_queries(const Cache& c, const BlockAttend& b, hipStream_t st);
 size_t attend_tiles_ws_bytes(const Cache& c, const BlockAttend& b);
