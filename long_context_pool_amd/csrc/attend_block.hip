@@ -13,8 +13,9 @@ namespace {
 typedef __attribute__((ext_vector_type(8))) _Float16 f16x8;
 
 constexpr int kThreads = 256;
-constexpr int kRowShift = 7, kRows = 1 << kRowShift;  // rows (queries times the query heads of a kv head) of a workgroup
-static_assert(kRows == kThreads / 2, "32 rows a wave");
+// Rows (queries times the query heads of a kv head) of a workgroup whose waves have RW
+// times 32 of them.
+constexpr int row_shift(int RW) { return RW == 4 ? 7 : 6; }
 constexpr float kLift = 7.f;  // weights go up to 2^(kSlack + kLift) < 65504, f16's largest
 constexpr float kNoGroup = -1e9f;  // the exponent of a group without a page
 constexpr float kFar = 60.f, kNear = 8.f;
@@ -82,13 +83,19 @@ __device__ __forceinline__ float halves_sum(float x) {
 // the largest; maximum, sums and O are fp32.  V's scale goes into the weights
 // relative to a reference exponent, `eref`, which O's registers are in units of and
 // which follows the blocks' scales when they leave its neighbourhood.
-template <int D, int TK>
+//
+// RW = 4: the waves have 32 rows each.  RW = 2: two have 32 rows and half the tokens of
+// a tile each, two the same rows and the other half; their sums are joined at the end.
+template <int D, int TK, int RW>
 __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attend_tiles_kernel(TileArgs a) {
+  constexpr int kRowShift = row_shift(RW), kRows = 1 << kRowShift;
   constexpr int CH = D / 8;              // 16-byte chunks of a widened row
   constexpr int CC = D / 16;             // of a row of codes
   constexpr int NC = TK * CC / kThreads;  // loads of K, and of V, a thread and tile
   constexpr int KS = D / 16, NJ = D / 32;
-  constexpr int NH = TK / 32, NG = TK / 16;
+  constexpr int NG = TK / 16;            // groups of 16 tokens
+  constexpr int NH = TK / 32 * RW / 4;   // a wave's halves of 32 tokens
+  static_assert(NH > 0, "a wave has 32 tokens of a tile");
   constexpr int GT = kGroups / NG;       // tiles of a stage of groups
   __shared__ __attribute__((aligned(128))) uint4 kt[2][TK * CH];
   __shared__ __attribute__((aligned(128))) uint4 vt[2][TK * CH];
@@ -96,10 +103,12 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attend_tiles_kerne
   __shared__ __attribute__((aligned(16))) uint32_t slots[2 * kGroups];
   __shared__ __attribute__((aligned(16))) float k_unit[2 * kGroups];
   __shared__ __attribute__((aligned(16))) float v_exp[2 * kGroups];
+  __shared__ float4 join[RW < 4 ? kRows : 1];
   __shared__ int any_nan;  // in V's codes of tiles with tokens that some rows do not see
 
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int c = lane & 31, g = lane >> 5;
+  const int wave_rows = 32 * (wave % RW), h0 = wave / RW * NH;  // first row, first half of the tokens
   const int kvh = blockIdx.x % a.kv_heads;
   const int rest = blockIdx.x / a.kv_heads;
   const int split = rest % a.splits;
@@ -120,16 +129,17 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attend_tiles_kerne
   const auto token_of = [&](int32_t flat) { return static_cast<int32_t>(div_page(flat, a.by_share)); };
   const int32_t last = static_cast<int32_t>(min(flat0 + kRows, flats)) - 1;
   const int32_t least = seen_by(token_of(static_cast<int32_t>(flat0))), most = seen_by(token_of(last));
-  const int32_t flat = static_cast<int32_t>(flat0) + wave * 32 + c;
+  const int32_t flat = static_cast<int32_t>(flat0) + wave_rows + c;
   const bool mine = flat <= last;
   const int32_t token = token_of(min(flat, last));
   const int32_t seen = seen_by(token);
   const int64_t at = static_cast<int64_t>(begin + token) * a.heads + kvh * a.share + (min(flat, last) - token * a.share);
-  const bool busy = static_cast<int32_t>(flat0) + wave * 32 <= last;  // the wave has rows
+  const bool busy = static_cast<int32_t>(flat0) + wave_rows <= last;  // the wave has rows
 
   const int32_t tiles = (most + TK - 1) / TK, per = (tiles + a.splits - 1) / a.splits;
   const int32_t t0 = split * per, t1 = min(t0 + per, tiles);
   if (t0 >= t1) {
+    if (h0 > 0) return;
     if (mine && g == 0) {
       if (a.splits > 1)
         a.part_ml[at * a.splits + split] = make_float2(-INFINITY, 0.f);
@@ -276,20 +286,20 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attend_tiles_kerne
     for (int s = 0; s < KS; ++s)
 #pragma unroll
       for (int h = 0; h < NH; ++h)
-        st[h] = mfma32_bf16(as_bf16x8(kt[b][k_at(32 * h + c, 2 * s + g)]), qf[s], st[h]);
+        st[h] = mfma32_bf16(as_bf16x8(kt[b][k_at(32 * (h0 + h) + c, 2 * s + g)]), qf[s], st[h]);
   };
   // The exponents of a tile's groups, uniform but in vector registers: as scalars they
   // would cost the way there and its waits (a third of the weights' time).
-  const auto exponents = [&](int32_t tile, float (&ve)[NG]) __attribute__((always_inline)) {
-    const int32_t first = ((tile - t0) & (2 * GT - 1)) * NG;
+  const auto exponents = [&](int32_t tile, float (&ve)[2 * NH]) __attribute__((always_inline)) {
+    const int32_t first = ((tile - t0) & (2 * GT - 1)) * NG + 2 * h0;
 #pragma unroll
-    for (int i = 0; i < NG; ++i) ve[i] = v_exp[first + i];
+    for (int i = 0; i < 2 * NH; ++i) ve[i] = v_exp[first + i];
   };
   // Weights of a tile from its scores.
-  const auto weigh = [&](int32_t tile, const float (&ve)[NG], f32x16 (&st)[NH], f16x8 (&w)[NG]) __attribute__((always_inline)) {
+  const auto weigh = [&](int32_t tile, const float (&ve)[2 * NH], f32x16 (&st)[NH], f16x8 (&w)[2 * NH]) __attribute__((always_inline)) {
     float loud = ve[0], still = ve[0];
 #pragma unroll
-    for (int i = 1; i < NG; ++i) {
+    for (int i = 1; i < 2 * NH; ++i) {
       loud = fmaxf(loud, ve[i]);
       still = fminf(still, ve[i]);
     }
@@ -299,7 +309,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attend_tiles_kerne
       for (int h = 0; h < NH; ++h)
 #pragma unroll
         for (int e = 0; e < 16; ++e)
-          st[h][e] = tile * TK + 32 * h + 8 * (e / 4) + 4 * g + e % 4 < seen && ve[2 * h + e / 8] != kNoGroup
+          st[h][e] = tile * TK + 32 * (h0 + h) + 8 * (e / 4) + 4 * g + e % 4 < seen && ve[2 * h + e / 8] != kNoGroup
                          ? st[h][e] : -INFINITY;
     }
     float high = -INFINITY;
@@ -325,7 +335,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attend_tiles_kerne
     }
     const float mb = m == -INFINITY ? 0.f : m;
 #pragma unroll
-    for (int i = 0; i < NG; ++i) {
+    for (int i = 0; i < 2 * NH; ++i) {
       // Far below the reference a block's values no longer count, but its weights do.
       const float lift = kLift + fmaxf(ve[i] - eref, -100.f), base = lift - mb;
       float sum = 0.f;
@@ -338,16 +348,16 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attend_tiles_kerne
       l += __builtin_amdgcn_ldexpf(sum, static_cast<int>(-lift));
     }
   };
-  const auto add_values = [&](int b, const f16x8 (&w)[NG]) __attribute__((always_inline)) {
+  const auto add_values = [&](int b, const f16x8 (&w)[2 * NH]) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < NG; ++i)
+    for (int i = 0; i < 2 * NH; ++i)
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
         const auto part = [&](int row) {
           const uint8_t* p = reinterpret_cast<const uint8_t*>(&vt[b][v_at(row, 4 * j + vcol)]) + (lane & 1) * 8;
           return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)p);
         };
-        const s16x4 y0 = part(16 * i + vrow), y1 = part(16 * i + 8 + vrow);
+        const s16x4 y0 = part(16 * (2 * h0 + i) + vrow), y1 = part(16 * (2 * h0 + i) + 8 + vrow);
         const f16x8 v = __builtin_bit_cast(f16x8, __builtin_shufflevector(y0, y1, 0, 1, 2, 3, 4, 5, 6, 7));
         acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, w[i], acc[j], 0, 0, 0);
       }
@@ -372,7 +382,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attend_tiles_kerne
   load_v(t0);
   widen_k(0);
   f32x16 st[NH];
-  f16x8 w[NG];
+  f16x8 w[2 * NH];
   widen_v(t0, 0);
   for (int32_t tile = t0; tile < t1; ++tile) {
     const int32_t n = tile - t0;
@@ -381,7 +391,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attend_tiles_kerne
     load_k(min(tile + 1, t1 - 1));  // no branch: the compiler would wait where it ends
     load_v(min(tile + 1, t1 - 1));
     if (busy) {
-      float ve[NG];
+      float ve[2 * NH];
       exponents(tile, ve);
       score(n & 1, st);
       weigh(tile, ve, st, w);
@@ -395,6 +405,31 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attend_tiles_kerne
 
   l = halves_sum(l);
   __syncthreads();
+  if constexpr (RW < 4) {  // the second half's sums to the first, through K's buffers
+    static_assert(sizeof(kt) >= sizeof(float) * D / 2 * kRows * 2, "two waves' O");
+    float* to = reinterpret_cast<float*>(kt) + wave_rows * 2 + lane;
+    if (h0 > 0) {
+      if (g == 0) join[wave_rows + c] = make_float4(m, l, eref, 0.f);
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) to[(16 * j + e) * (2 * kRows)] = acc[j][e];
+    }
+    __syncthreads();
+    if (h0 > 0) return;
+    const float4 x = join[wave_rows + c];
+    const float both = fmaxf(m, x.x), unit = fmaxf(eref, x.z);
+    const float f0 = part_factor(m, l, both), f1 = part_factor(x.x, x.y, both);
+    const float s0 = __builtin_amdgcn_ldexpf(f0, static_cast<int>(fmaxf(eref - unit, -200.f)));
+    const float s1 = __builtin_amdgcn_ldexpf(f1, static_cast<int>(fmaxf(x.z - unit, -200.f)));
+    m = both;
+    l = l * f0 + x.y * f1;
+    eref = unit;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[j][e] = acc[j][e] * s0 + to[(16 * j + e) * (2 * kRows)] * s1;
+  }
   if (!mine) return;
   if (any_nan) {  // the NaN values left out above, for the rows that see them
     for (int32_t s = max(t0 * TK, least / TK * TK); s < min(t1 * TK, seen); ++s) {
@@ -480,19 +515,27 @@ __global__ __launch_bounds__(256) void join_tiles_kernel(TileArgs a) {
 constexpr int kSlots = 512;  // workgroups that the card holds at a time
 constexpr int kMaxParts = 32;
 
-int64_t tile_units(const Cache& c, const BlockAttend& b) {
-  return unit_base(b.n, b.heads / c.kv_heads, kRowShift, c.rows, 1);
+int row_waves(const Cache& c, const BlockAttend& b) {
+  return c.dk <= 128 && static_cast<int64_t>(b.most) * (b.heads / c.kv_heads) <= 64 ? 2 : 4;
 }
 
+int64_t tile_units(const Cache& c, const BlockAttend& b) {
+  return unit_base(b.n, b.heads / c.kv_heads, row_shift(row_waves(c, b)), c.rows, 1);
+}
+
+// As many splits as fill the card once, of the units that rows with up to `most` new
+// tokens can have.
 int32_t tile_splits(const Cache& c, const BlockAttend& b) {
-  const int64_t groups = tile_units(c, b) * c.kv_heads;
+  const int64_t rows = 32 * row_waves(c, b), most = std::max(b.most, 1);
+  const int64_t whole = ((b.n - 1) / most + 1) * ((most * (b.heads / c.kv_heads) - 1) / rows + 1);
+  const int64_t groups = std::min(tile_units(c, b), whole) * c.kv_heads;
   const int64_t longest = (static_cast<int64_t>(c.row_pages) * c.P + 255) / 256;  // four tiles a split
   return static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>({kSlots / groups, longest, kMaxParts})));
 }
 
-template <int D, int TK>
+template <int D, int TK, int RW>
 hipError_t launch_tiles_dim(const TileArgs& a, uint32_t grid, hipStream_t st) {
-  attend_tiles_kernel<D, TK><<<grid, kThreads, 0, st>>>(a);
+  attend_tiles_kernel<D, TK, RW><<<grid, kThreads, 0, st>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
   const int per = 1024 / D;
@@ -537,10 +580,11 @@ hipError_t launch_attend_tiles(const Cache& c, const BlockAttend& b, hipStream_t
   a.page = make_div(c.P);
   a.by_share = make_div(a.share);
   const uint32_t grid = static_cast<uint32_t>(tile_units(c, b) * c.kv_heads * a.splits);
+  const bool two = row_waves(c, b) == 2;
   switch (c.dk) {
-    case 64: return launch_tiles_dim<64, 64>(a, grid, st);
-    case 128: return launch_tiles_dim<128, 64>(a, grid, st);
-    default: return launch_tiles_dim<256, 32>(a, grid, st);
+    case 64: return two ? launch_tiles_dim<64, 64, 2>(a, grid, st) : launch_tiles_dim<64, 64, 4>(a, grid, st);
+    case 128: return two ? launch_tiles_dim<128, 64, 2>(a, grid, st) : launch_tiles_dim<128, 64, 4>(a, grid, st);
+    default: return launch_tiles_dim<256, 32, 4>(a, grid, st);
   }
 }
 

@@ -17,6 +17,7 @@ from tests.serve_ref import check_e4m3
 FAKE = 1 << 20  # an aligned non-null address; never dereferenced (calls fail validation)
 gpu = pytest.mark.gpu
 E4M3 = torch.float8_e4m3fn
+MANY = 70  # new tokens of a row for which tiles of queries have their larger form, whatever the heads
 TYPES = {0: torch.float32, 1: torch.bfloat16, 2: E4M3}
 
 
@@ -173,7 +174,7 @@ def test_block_calls_refuse_arguments(misa):
                    dict(n=1 << 20, heads=128), dict(scale=3e38)):
         assert attend(**change) == -2, change
     long = misa.cache(1, 4096, 5000, 64, 1, 128, 128, misa.MISA_FP8_E4M3)
-    for most in (1, 40):
+    for most in (1, 5, 80):
         need = misa.misa_block_attend_workspace_bytes(long, 32, 8, most, most, 0)
         assert need > 0
         attend = _calls(misa, long)[2]
@@ -442,13 +443,13 @@ def test_read(misa, case, out):
 # ------------------------------------------------------------------ attention
 
 
-def _check_attend(misa, c, B, heads, k, scale, offsets, q, pools, table, lengths, idx, most, tiles=None, ws=None):
-    """Calls and compares; `tiles`: whether several queries share a pass."""
+def _check_attend(misa, c, B, heads, k, scale, offsets, q, pools, table, lengths, idx, most):
+    """Calls and compares; tiles of several queries hold weights to 11 bits."""
     n = q.shape[0]
     kp, ks, vp, vs = pools
     out, lse, out_tol, lse_tol, wide, written = ref.attend(misa, c, B, heads, k, scale, offsets, q, kp, ks, vp, vs, table,
                                                            lengths, idx)
-    if (k == 0 and most > 1) if tiles is None else tiles:
+    if k == 0 and most > 1:
         out_tol = out_tol + wide
     ln = torch.tensor(lengths, dtype=torch.int32)
     go = torch.full((n, heads, c.dk), 3.0, dtype=torch.bfloat16, device="cuda")
@@ -489,9 +490,9 @@ ATTEND = [
 
 @gpu
 @pytest.mark.parametrize("case", ATTEND, ids=str)
-@pytest.mark.parametrize("most", [1, 2])
+@pytest.mark.parametrize("most", [1, 2, MANY])
 def test_attend(misa, case, most):
-    """Both kernels on every case: `most` picks one, and no result depends on it."""
+    """Every kernel on every case: `most` picks one, and no result depends on it."""
     lengths, counts, P, B, kv, heads, d, front, behind = case
     _log(f"[gpu] block attend {case} {most}")
     g = torch.Generator().manual_seed(sum(lengths) + d)
@@ -503,7 +504,7 @@ def test_attend(misa, case, most):
 
 @gpu
 @pytest.mark.parametrize("scale", [0.0, -0.2, 1e-3, 3.0])
-@pytest.mark.parametrize("most", [1, 3])
+@pytest.mark.parametrize("most", [1, 3, MANY])
 def test_attend_scales(misa, scale, most):
     _log(f"[gpu] block attend scale {scale} {most}")
     g = torch.Generator().manual_seed(9)
@@ -514,7 +515,7 @@ def test_attend_scales(misa, scale, most):
 
 
 @gpu
-@pytest.mark.parametrize("most", [1, 3])
+@pytest.mark.parametrize("most", [1, 3, MANY])
 def test_attend_blocks_of_far_scales(misa, most):
     """Neighbouring blocks' scales up to 2^40 apart, either way: weights follow the values' scale."""
     _log(f"[gpu] block attend far scales {most}")
@@ -531,7 +532,7 @@ def test_attend_blocks_of_far_scales(misa, most):
 
 
 @gpu
-@pytest.mark.parametrize("most", [1, 3])
+@pytest.mark.parametrize("most", [1, 3, MANY])
 @pytest.mark.parametrize("d", [64, 128])
 def test_attend_nan_where_it_is_not_seen(misa, most, d):
     """NaN behind the row's end, in pages it lost, and at tokens that only later queries see."""
@@ -560,7 +561,7 @@ def test_attend_nan_where_it_is_not_seen(misa, most, d):
 
 
 @gpu
-@pytest.mark.parametrize("most", [1, 4])
+@pytest.mark.parametrize("most", [1, 4, MANY])
 def test_attend_long_rows_in_splits(misa, most):
     """Few queries, long rows: parts that are joined, some of them without tokens."""
     _log(f"[gpu] block attend splits {most}")
@@ -598,7 +599,7 @@ def test_attend_refused_or_unread_offsets(misa):
     lengths = [50, 60, 70]
     c, table, *pools = _pool(misa, g, lengths, 16, 16, 1, 64)
     q = torch.randn(12, 2, 64, generator=g).bfloat16()
-    for most in (1, 3):
+    for most in (1, 3, MANY):
         for offsets in ([0, 4, 4, 400], [-9, 4, 7, 12]):
             _check_attend(misa, c, 16, 2, 0, 0.1, torch.tensor(offsets, dtype=torch.int32), q, pools, table, lengths, None,
                           most)
@@ -632,7 +633,7 @@ def test_far_pages(misa):
     assert torch.all((vo.float() - vn.float()).abs() <= vn.float().abs() * 2.0 ** -4 + 2.0 ** -16)
     q = torch.randn(6, kv, d, generator=g).bfloat16()
     kc, vc = (x.cpu().float().view(rows, L, kv, d) for x in (ko, vo))
-    for most in (1, 3):
+    for most in (1, 3, MANY):
         off = _offsets([3, 3]).cuda()
         out = torch.empty(6, kv, d, dtype=torch.bfloat16, device="cuda")
         ws = torch.empty(misa.misa_block_attend_workspace_bytes(c, B, kv, 6, most, 0), dtype=torch.uint8, device="cuda")
