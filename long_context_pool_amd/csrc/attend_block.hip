@@ -197,10 +197,14 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attend_tiles_kerne
 
   // Thread i has chunk i % CC of tokens i / CC, + kThreads / CC, ...
   // Swizzles of the chunks, so that 16 rows' reads of a chunk (K) and four rows' of
-  // 64 bytes (V) are in different banks.
-  const auto k_at = [](int row, int chunk) { return row * CH + (chunk ^ (D == 64 ? row >> 1 & 7 : row & 15)); };
-  const auto v_at = [](int row, int chunk) {
-    return row * CH + (D == 64 ? chunk ^ (row >> 1 & 1) << 2 : chunk ^ (row & 3) << 2);
+  // 64 bytes (V) are in different banks, and so are eight threads' writes of every
+  // other chunk of a row (a quarter of all LDS cycles were conflicts of those).
+  const auto spread = [](int row, int chunk) { return D == 64 ? row & 1 : chunk >> 3 & 1; };
+  const auto k_at = [&](int row, int chunk) {
+    return row * CH + (chunk ^ (D == 64 ? row >> 1 & 7 : row & 15) ^ spread(row, chunk));
+  };
+  const auto v_at = [&](int row, int chunk) {
+    return row * CH + (chunk ^ (D == 64 ? (row >> 1 & 1) << 2 : (row & 3) << 2) ^ spread(row, chunk));
   };
   const int my_token = threadIdx.x / CC, my_chunk = threadIdx.x % CC;
   // Rows i of a thread are a multiple of 16 apart (or it has one): one address
