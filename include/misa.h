@@ -538,14 +538,14 @@ misa_status misa_block_read(const misa_cache* cache, int32_t block_tokens, int32
  *   q    [n, heads, d]  bf16         out [n, heads, d]  bf16, written
  *   idx  [n, k]  int32 (k > 0; k = 0: NULL)
  *   lse  [n, heads]  fp32, written if non-NULL
- * Scores, softmax and sums are fp32: q . codes and a score times log2(e) must be in
- * its range, and cached values below 2^90; a weight goes into its products in 16 or
- * 11 bits and never moves a sum by more than 2^-11 of itself, or 2^-31 of the
- * largest.  Values in blocks whose scale is less than 2^-60 of the largest one of
- * the row and head count to 2^-60 of that.  Limits: heads a multiple of kv_heads, heads <= 1024, n <= 2^20 and n * heads
- * <= 2^26, 0 <= k <= 2^20, |scale| <= 2^127.  ws must hold
- * misa_block_attend_workspace_bytes(...) bytes (0: invalid arguments or no workspace
- * needed); it carries nothing from one call to the next. */
+ * Scores, softmax and sums are fp32: q . k, q . codes and a score times log2(e) must
+ * be in its range, and cached values below 2^90.  A weight goes into its products
+ * in 16 bits where queries are worked on one by one (one new token a row, or lists);
+ * where several share a pass in 11 bits, or to 2^-32 of the largest weight times the
+ * largest value that the row's loudest block may hold.  Limits: heads a multiple of
+ * kv_heads, heads <= 1024, n <= 2^20, n * heads <= 2^26, 0 <= k <= 2^20, |scale| <=
+ * 2^127.  ws must hold misa_block_attend_workspace_bytes(...) bytes (0: invalid
+ * arguments or no workspace needed); it carries nothing from one call to the next. */
 size_t misa_block_attend_workspace_bytes(const misa_cache* cache, int32_t block_tokens,
                                          int32_t heads, int32_t n, int32_t most, int32_t k);
 misa_status misa_block_attend(const misa_cache* cache, int32_t block_tokens, int32_t heads,

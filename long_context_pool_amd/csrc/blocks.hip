@@ -187,64 +187,66 @@ struct ReadArgs {
   int32_t row_pages, pages, P, kv_heads, shift;  // 2^shift tokens a block
 };
 
-template <bool ONCE>
-__device__ __forceinline__ uint4 get(const uint8_t* p) {
-  const u32x4* q = reinterpret_cast<const u32x4*>(p);
-  return __builtin_bit_cast(uint4, ONCE ? __builtin_nontemporal_load(q) : *q);
-}
-template <bool ONCE, typename V>
-__device__ __forceinline__ void put(void* p, const V& x) {
-  const u32x4 y = __builtin_bit_cast(u32x4, x);
-  if constexpr (ONCE)
-    __builtin_nontemporal_store(y, static_cast<u32x4*>(p));
-  else
-    *static_cast<u32x4*>(p) = y;
+// A lane's load and store: as many codes as make 16 bytes of OUT, so that a wave's
+// stores are whole runs of the output (with 16 codes a lane, and stores of a lane's 64
+// bytes of fp32 one after the other, 200 MB took 130 us instead of 53).
+template <int OUT>
+constexpr int kPerLane = 16 / elem_bytes<OUT>();
+
+template <int N, bool ONCE>
+__device__ __forceinline__ void get(const uint8_t* p, uint32_t (&to)[N]) {
+  typedef __attribute__((ext_vector_type(N))) uint32_t V;
+  const V* q = reinterpret_cast<const V*>(p);
+  const V x = ONCE ? __builtin_nontemporal_load(q) : *q;
+#pragma unroll
+  for (int i = 0; i < N; ++i) to[i] = x[i];
 }
 
-// 16 codes -> 16 values of OUT at `dst`.
+// The codes of a lane -> 16 bytes of OUT at `dst`.
 template <int OUT, bool ONCE>
-__device__ __forceinline__ void put16(void* dst, int64_t at, uint4 c, float scale) {
+__device__ __forceinline__ void put(void* dst, const uint32_t (&c)[kPerLane<OUT> / 4], float scale) {
+  u32x4 x;
   if constexpr (OUT == kFP8) {
-    put<ONCE>(static_cast<uint8_t*>(dst) + at, c);
+    x = u32x4{c[0], c[1], c[2], c[3]};
   } else {
-    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-    float y[16];
+    float y[kPerLane<OUT>];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      y[4 * j] = fp8_to_f32(w[j]) * scale;
-      y[4 * j + 1] = __builtin_amdgcn_cvt_f32_fp8(w[j], 1) * scale;
-      y[4 * j + 2] = __builtin_amdgcn_cvt_f32_fp8(w[j], 2) * scale;
-      y[4 * j + 3] = __builtin_amdgcn_cvt_f32_fp8(w[j], 3) * scale;
+    for (int j = 0; j < kPerLane<OUT> / 4; ++j) {
+      y[4 * j] = fp8_to_f32(c[j]) * scale;
+      y[4 * j + 1] = __builtin_amdgcn_cvt_f32_fp8(c[j], 1) * scale;
+      y[4 * j + 2] = __builtin_amdgcn_cvt_f32_fp8(c[j], 2) * scale;
+      y[4 * j + 3] = __builtin_amdgcn_cvt_f32_fp8(c[j], 3) * scale;
     }
     if constexpr (OUT == kF32) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        put<ONCE>(static_cast<float*>(dst) + at + 4 * j, make_float4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]));
+      x = __builtin_bit_cast(u32x4, make_float4(y[0], y[1], y[2], y[3]));
     } else {
       typedef __attribute__((ext_vector_type(8))) __bf16 B8;
-      B8 lo, hi;
+      B8 b;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        lo[j] = static_cast<__bf16>(y[j]);
-        hi[j] = static_cast<__bf16>(y[8 + j]);
-      }
-      put<ONCE>(static_cast<uint16_t*>(dst) + at, lo);
-      put<ONCE>(static_cast<uint16_t*>(dst) + at + 8, hi);
+      for (int j = 0; j < 8; ++j) b[j] = static_cast<__bf16>(y[j]);
+      x = __builtin_bit_cast(u32x4, b);
     }
   }
+  if constexpr (ONCE)
+    __builtin_nontemporal_store(x, static_cast<u32x4*>(dst));
+  else
+    *static_cast<u32x4*>(dst) = x;
 }
 
-constexpr int kReadRounds = 2;
+// Rounds of a lane, whose loads are under way together (twice as many for bf16 and fp32:
+// 9.5 and 16.1 us for 2 rows of 2000 tokens of 8 heads, 8.8 and 13.2 with these).
+template <int OUT>
+constexpr int kRounds = OUT == kF32 ? 4 : 2;
 
-// D / 16 lanes per (packed token, kv head), 16 codes each, and two of those a lane,
-// whose loads are under way together.  The row of a workgroup's tokens, mostly one,
+// Lanes of a (packed token, kv head) that have kPerLane codes each.  The row of a workgroup's tokens, mostly one,
 // is looked up once: a lookup each cost 8 rows of 131072 keys (213 MB) 20 of 70 us.
 // Bound by HBM traffic, 5.1 TB/s there.
 //
 // ONCE: much is moved, and marked as not to be kept (41.7 us there, 47.1 without).
 template <int D, int OUT, bool ONCE>
 __global__ __launch_bounds__(256) void block_read_kernel(ReadArgs a) {
-  constexpr int LPR = D / 16, IP = 256 / LPR;  // lanes of an item, items of a round
+  constexpr int N = kPerLane<OUT>, kReadRounds = kRounds<OUT>;
+  constexpr int LPR = D / N, IP = 256 / LPR;  // lanes of an item, items of a round
   const int which = blockIdx.y;
   const int lane = threadIdx.x % LPR;
   const int64_t items = static_cast<int64_t>(a.rows.n) * a.kv_heads;
@@ -256,7 +258,7 @@ __global__ __launch_bounds__(256) void block_read_kernel(ReadArgs a) {
   const int32_t r0 = last_row(a.rows.rows, t0, offset);
   int32_t r1 = r0;
   if (a.rows.at(r0 + 1) <= t1) r1 = last_row(a.rows.rows, t1, offset);
-  uint4 code[kReadRounds];
+  uint32_t code[kReadRounds][N / 4];
   float unit[kReadRounds];
   int64_t item[kReadRounds];
   const auto fetch = [&](int i, int32_t r, int32_t t, int32_t head, int32_t begin, int32_t end, int32_t first, int32_t len)
@@ -271,14 +273,15 @@ __global__ __launch_bounds__(256) void block_read_kernel(ReadArgs a) {
     const int32_t page = a.table[static_cast<int64_t>(r) * a.row_pages + e];
     if (page < 0 || page >= a.pages) return;
     const int64_t slot = (static_cast<int64_t>(page) * a.kv_heads + head) * a.P + (p - static_cast<int64_t>(e) * a.P);
-    code[i] = get<ONCE>(a.pages_of[which] + slot * D + lane * 16);
+    get<N / 4, ONCE>(a.pages_of[which] + slot * D + lane * N, code[i]);
     unit[i] = a.scale[which][static_cast<uint32_t>(slot) >> a.shift];
   };
   const int32_t begin0 = a.rows.at(r0), end0 = a.rows.at(r0 + 1), first0 = a.first ? a.first[r0] : 0, len0 = a.lengths[r0];
 #pragma unroll
   for (int i = 0; i < kReadRounds; ++i) {
     item[i] = item0 + i * IP + threadIdx.x / LPR;
-    code[i] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int j = 0; j < N / 4; ++j) code[i][j] = 0;
     unit[i] = 1.f;
     if (item[i] >= items) {
       item[i] = -1;
@@ -303,7 +306,7 @@ __global__ __launch_bounds__(256) void block_read_kernel(ReadArgs a) {
 #pragma unroll
   for (int i = 0; i < kReadRounds; ++i) {
     if (item[i] < 0) continue;
-    put16<OUT, ONCE>(a.out[which], item[i] * D + lane * 16, code[i], unit[i]);
+    put<OUT, ONCE>(static_cast<uint8_t*>(a.out[which]) + (item[i] * D + lane * N) * elem_bytes<OUT>(), code[i], unit[i]);
     if (OUT == kFP8 && lane == 0) a.out_scale[which][item[i]] = unit[i];
   }
 }
@@ -313,7 +316,7 @@ constexpr int64_t kReadOnceBytes = int64_t{32} << 20;
 template <int D, int OUT>
 hipError_t launch_read_out(const ReadArgs& a, int32_t parts, hipStream_t st) {
   const int64_t items = static_cast<int64_t>(a.rows.n) * a.kv_heads;  // at most 2^28
-  const int per = 256 / (D / 16) * kReadRounds;
+  const int per = 256 / (D / kPerLane<OUT>)*kRounds<OUT>;
   const dim3 grid(static_cast<uint32_t>((items + per - 1) / per), parts);
   if (items * D * parts * (1 + elem_bytes<OUT>()) >= kReadOnceBytes)
     block_read_kernel<D, OUT, true><<<grid, 256, 0, st>>>(a);
