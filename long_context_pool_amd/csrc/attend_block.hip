@@ -78,14 +78,30 @@ __device__ __forceinline__ float halves_sum(float x) {
 //   S^T = K Q^T, O^T = V^T P^T  (32x32x16), a lane keeps one row (l % 32),
 // so that the softmax is within a lane but for its other half, and P^T's operand is
 // S^T's registers: of 16 tokens, lane half g holds 4g .. 4g+3 and 8+4g .. 8+4g+3,
-// and V's transposing reads give them in that order.
-// Weights are f16 (11 bits), lifted by 2^7 so that what f16 loses is below 2^-31 of
-// the largest; maximum, sums and O are fp32.  V's scale goes into the weights
+// and V's transposing reads give them in that order.  e4m3 codes are exact in both
+// types, K's with its scale.
+// Weights are f16, in one part of 11 bits, lifted by 2^7 so that what f16 loses is
+// 2^-32 of the largest; maximum, sums and O are fp32.  V's scale goes into the weights
 // relative to a reference exponent, `eref`, which O's registers are in units of and
-// which follows the blocks' scales when they leave its neighbourhood.
+// which follows the tiles' loudest scale when that leaves its neighbourhood.
+// NaN values of tokens that some rows do not see yet are left out as zeros, since a
+// weight of zero would not hide them, and put in at the end for the rows that see them.
+//
+// Bound by the matrix unit, LDS and the vector unit taking turns, at clocks that power
+// holds back (1.85 to 2.1 of 2.4 GHz): 8192 queries of three rows of up to 32768 tokens,
+// 64 heads on 8 of 128 (6.96 TFLOP), 7.5 to 8.1 ms on several boxes, 860 to 925 TFLOP/s,
+// 71 to 76% of what a large library product reaches; matrix unit busy 44%.  Of it the
+// values' products take 2.9 ms, the scores' 2.2, widening the tiles 1.6, the
+// exponentials 0.2.  Heads of 64 763 TFLOP/s, of 256 (one workgroup a CU) 620.
+// Tried and not kept: scores on the 8-bit matrix instructions with queries in two
+// e4m3 parts (10% less time, but sums of products off by 2^-18, more than fp32's);
+// 256 rows a workgroup, in step (9.4 ms) or in two groups that take turns (equal);
+// the next tile's scores beside this one's weights (9.2); three waves a SIMD (9.5).
 //
 // RW = 4: the waves have 32 rows each.  RW = 2: two have 32 rows and half the tokens of
 // a tile each, two the same rows and the other half; their sums are joined at the end.
+// By memory, then: 16 rows of up to 32768 tokens, 64 heads on 8, five drafts each (789
+// MB) 201 to 213 us, 3.7 to 3.9 TB/s.
 template <int D, int TK, int RW>
 __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attend_tiles_kernel(TileArgs a) {
   constexpr int kRowShift = row_shift(RW), kRows = 1 << kRowShift;
@@ -480,7 +496,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attend_tiles_kerne
 }
 
 // The splits of a query's heads joined: D / 4 threads a head, 1024 / D heads a
-// workgroup.
+// workgroup.  75 queries of 64 heads in four splits 5 us.
 template <int D>
 __global__ __launch_bounds__(256) void join_tiles_kernel(TileArgs a) {
   constexpr int T = D / 4;
@@ -519,6 +535,9 @@ __global__ __launch_bounds__(256) void join_tiles_kernel(TileArgs a) {
 constexpr int kSlots = 512;  // workgroups that the card holds at a time
 constexpr int kMaxParts = 32;
 
+// Two waves' rows where no row of the batch has more: 16 rows of 32768 tokens, 64 heads
+// on 8 of 128, eight new tokens each (64 pairs of query and head) 210 us, 262 with
+// four waves' rows; nine 376 and 277 us.
 int row_waves(const Cache& c, const BlockAttend& b) {
   return c.dk <= 128 && static_cast<int64_t>(b.most) * (b.heads / c.kv_heads) <= 64 ? 2 : 4;
 }
@@ -528,7 +547,8 @@ int64_t tile_units(const Cache& c, const BlockAttend& b) {
 }
 
 // As many splits as fill the card once, of the units that rows with up to `most` new
-// tokens can have.
+// tokens can have (counted with a unit more for each row of the table, as the grid is,
+// five drafts on 16 rows have two splits for four: 333 us for 215).
 int32_t tile_splits(const Cache& c, const BlockAttend& b) {
   const int64_t rows = 32 * row_waves(c, b), most = std::max(b.most, 1);
   const int64_t whole = ((b.n - 1) / most + 1) * ((most * (b.heads / c.kv_heads) - 1) / rows + 1);

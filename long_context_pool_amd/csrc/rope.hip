@@ -80,6 +80,10 @@ constexpr int kTurns = 2048;  // (cos, sin) pairs in LDS: of all of a workgroup'
 // rot / 2 apart), or 16 neighbours of the rest.  The heads of a token share its
 // angles: they are computed once into LDS while the values' loads are under way,
 // and the values stay in registers until the token's largest magnitude is known.
+//
+// Bound by memory traffic: 8192 tokens of 64 heads of 128, bf16 to e4m3 (201 MB) 41.6
+// us, 4.8 TB/s, to bf16 50.9 us, 5.3 TB/s; 32 tokens of 72 heads 4.2 us, a launch, the
+// angles and the loads.
 template <int X, int OUT, int TPR, int NI>
 __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a) {
   constexpr int TOKENS = 256 / TPR;
@@ -162,7 +166,8 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a) {
   }
 }
 
-// Any sizes and strides: a workgroup per token, a thread per pair or passing
+// Sizes and strides off the runs of 16 (4096 tokens of 32 heads of 72, 36 of them
+// turned: 21 us, 1.8 TB/s): a workgroup per token, a thread per pair or passing
 // element, angles computed where they are needed; an 8-bit output goes through the
 // values twice.
 template <int X, int OUT>
