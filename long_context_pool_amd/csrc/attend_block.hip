@@ -89,7 +89,7 @@ __device__ __forceinline__ float halves_sum(float x) {
 //
 // Bound by the matrix unit, LDS and the vector unit taking turns, at clocks that power
 // holds back (1.85 to 2.1 of 2.4 GHz): 8192 queries of three rows of up to 32768 tokens,
-// 64 heads on 8 of 128 (6.96 TFLOP), 7.5 to 8.1 ms on several boxes, 860 to 925 TFLOP/s,
+// 64 heads on 8 of 128 (6.96 TFLOP), 7.5 to 8.1 ms on several cards, 860 to 925 TFLOP/s,
 // 71 to 76% of what a large library product reaches; matrix unit busy 44%.  Of it the
 // values' products take 2.9 ms, the scores' 2.2, widening the tiles 1.6, the
 // exponentials 0.2.  Heads of 64 763 TFLOP/s, of 256 (one workgroup a CU) 620.
@@ -261,10 +261,13 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attend_tiles_kerne
     }
   };
   const auto widen_v = [&](int32_t tile, int b) {
-    bool whole = (tile + 1) * TK <= least;
+    // A NaN must not meet a weight of zero: tokens that no row sees are zeros, and where
+    // some rows do not see some token, NaN codes are.
+    const bool edge = (tile + 1) * TK > least;
+    bool whole = !edge;
 #pragma unroll
     for (int i = 0; i < NC; ++i) whole = whole && !__any(!there[i]);
-    if (!whole) {  // not every row sees every token: a NaN must not meet a weight of zero
+    if (!whole) {
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
@@ -272,7 +275,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attend_tiles_kerne
         uint32_t* w = reinterpret_cast<uint32_t*>(&vc[i]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const uint32_t bad = seen ? nan_bytes(w[j]) : 0u;
+          const uint32_t bad = seen && edge ? nan_bytes(w[j]) : 0u;
           if (bad) any_nan = 1;
           w[j] = seen ? w[j] & ~bad : 0u;
         }

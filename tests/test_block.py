@@ -561,6 +561,22 @@ def test_attend_nan_where_it_is_not_seen(misa, most, d):
 
 
 @gpu
+@pytest.mark.parametrize("most", [1, 3, MANY])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("lost", [1, 2])
+def test_attend_nan_beside_a_lost_page(misa, most, d, lost):
+    """A NaN value that every query sees, one or two pages from one that the row lost."""
+    _log(f"[gpu] block attend nan beside a lost page {most} {d} {lost}")
+    g = torch.Generator().manual_seed(22)
+    c, table, k, ks, v, vs = _pool(misa, g, [200], 16, 16, 1, d)
+    v.view(torch.uint8)[table[0, 0], 0, 5, 9] = 0x7F
+    v.view(torch.uint8)[table[0, 4], 0, 2, 3] = 0xFF
+    table[0, lost] = -1
+    q = torch.randn(2, 2, d, generator=g).bfloat16()
+    _check_attend(misa, c, 16, 2, 0, 0.1, _offsets([2]), q, (k, ks, v, vs), table, [200], None, most)
+
+
+@gpu
 @pytest.mark.parametrize("most", [1, 4, MANY])
 def test_attend_long_rows_in_splits(misa, most):
     """Few queries, long rows: parts that are joined, some of them without tokens."""
