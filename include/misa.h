@@ -516,7 +516,7 @@ misa_status misa_block_write(const misa_cache* cache, int32_t block_tokens, int3
  *                 ignored).  With one kv head of 128 and rows of L tokens (offsets
  *                 r * L) these are misa_*'s k and k_scale.
  * Keys alone: v_pages, v_scale, v_out and v_out_scale NULL.  n = 0 is a no-op; n *
- * kv_heads <= 2^28. */
+ * kv_heads <= 2^27. */
 misa_status misa_block_read(const misa_cache* cache, int32_t block_tokens, int32_t n,
                             int32_t out_dtype, const int32_t* offsets, const int32_t* first,
                             const int32_t* lengths, const void* k_pages, const float* k_scale,
@@ -543,8 +543,8 @@ misa_status misa_block_read(const misa_cache* cache, int32_t block_tokens, int32
  * in 16 bits where queries are worked on one by one (one new token a row, or lists);
  * where several share a pass in 11 bits, or to 2^-32 of the largest weight times the
  * largest value that the row's loudest block may hold.  Limits: heads a multiple of
- * kv_heads, heads <= 1024, n <= 2^20, n * heads <= 2^26, 0 <= k <= 2^20, |scale| <=
- * 2^127.  ws must hold misa_block_attend_workspace_bytes(...) bytes (0: invalid
+ * kv_heads, heads <= 1024, n <= 2^20, n * heads <= 2^26 (2^23 one by one; otherwise
+ * rows * kv_heads <= 2^23), 0 <= k <= 2^20, |scale| <= 2^127.  ws must hold misa_block_attend_workspace_bytes(...) bytes (0: invalid
  * arguments or no workspace needed); it carries nothing from one call to the next. */
 size_t misa_block_attend_workspace_bytes(const misa_cache* cache, int32_t block_tokens,
                                          int32_t heads, int32_t n, int32_t most, int32_t k);

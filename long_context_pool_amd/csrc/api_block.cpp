@@ -39,6 +39,11 @@ misa_status check_block_pools(const void* k_pages, const float* k_scale, const v
   return check_out(more, false);
 }
 
+// One query at a time where each has a list of its own, or a row has one new token (8
+// rows of 131072 tokens, 64 heads on 8: 297 us, 335 in tiles; 32 rows of 8192 86 and 98
+// us); otherwise tiles of a row's queries share its keys and values.
+bool one_by_one(const misa::BlockAttend& b) { return b.k > 0 || b.most <= 1; }
+
 misa_status check_block_attend(const misa_cache* cache, int32_t heads, misa::BlockAttend& b, Cache& c) {
   MISA_TRY(check_block_cache(cache, b.block, c));
   if (heads < 1 || b.k < 0 || b.n < 0 || b.most < 0 || heads % c.kv_heads != 0)
@@ -46,14 +51,14 @@ misa_status check_block_attend(const misa_cache* cache, int32_t heads, misa::Blo
   if (heads > 1024 || b.k > (1 << 20) || b.n > (1 << 20) ||
       static_cast<int64_t>(b.n) * heads > (int64_t{1} << 26))
     return MISA_ERR_UNSUPPORTED;
+  // A launch has fewer than 2^24 workgroups of 256: at most one for each query and
+  // head, or 2^20 of whole tiles and one more for each row and kv head.
+  if ((one_by_one(b) ? static_cast<int64_t>(b.n) * heads : static_cast<int64_t>(c.rows) * c.kv_heads) >
+      (int64_t{1} << 23))
+    return MISA_ERR_UNSUPPORTED;
   b.heads = heads;
   return MISA_OK;
 }
-
-// One query at a time where each has a list of its own, or a row has one new token (8
-// rows of 131072 tokens, 64 heads on 8: 297 us, 335 in tiles; 32 rows of 8192 86 and 98
-// us); otherwise tiles of a row's queries share its keys and values.
-bool one_by_one(const misa::BlockAttend& b) { return b.k > 0 || b.most <= 1; }
 
 size_t attend_need(const Cache& c, const misa::BlockAttend& b) {
   if (b.n == 0) return 0;
@@ -156,7 +161,7 @@ misa_status misa_block_read(const misa_cache* cache, int32_t block_tokens, int32
   Cache c;
   MISA_TRY(check_block_cache(cache, block_tokens, c));
   if (n < 0 || out_dtype < MISA_F32 || out_dtype > MISA_FP8_E4M3) return MISA_ERR_INVALID_ARG;
-  if (static_cast<int64_t>(n) * c.kv_heads > (int64_t{1} << 28)) return MISA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(n) * c.kv_heads > (int64_t{1} << 27)) return MISA_ERR_UNSUPPORTED;
   if (n == 0) return MISA_OK;
   MISA_TRY(check_block_pools(k_pages, k_scale, v_pages, v_scale, v_out));
   MISA_TRY(check_out(offsets, true));

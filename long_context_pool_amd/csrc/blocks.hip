@@ -319,7 +319,7 @@ constexpr int64_t kReadOnceBytes = int64_t{32} << 20;
 
 template <int D, int OUT>
 hipError_t launch_read_out(const ReadArgs& a, int32_t parts, hipStream_t st) {
-  const int64_t items = static_cast<int64_t>(a.rows.n) * a.kv_heads;  // at most 2^28
+  const int64_t items = static_cast<int64_t>(a.rows.n) * a.kv_heads;  // at most 2^27
   const int per = 256 / (D / kPerLane<OUT>)*kRounds<OUT>;
   const dim3 grid(static_cast<uint32_t>((items + per - 1) / per), parts);
   if (items * D * parts * (1 + elem_bytes<OUT>()) >= kReadOnceBytes)

@@ -173,6 +173,12 @@ def test_block_calls_refuse_arguments(misa):
     for change in (dict(heads=2048), dict(k=(1 << 20) + 1, idx=FAKE), dict(n=(1 << 20) + 1),
                    dict(n=1 << 20, heads=128), dict(scale=3e38)):
         assert attend(**change) == -2, change
+    # More workgroups than a launch holds.
+    for change in (dict(n=1 << 18, heads=64, k=4, idx=FAKE), dict(n=1 << 18, heads=64, most=1)):
+        assert attend(**change) == -2, change
+    many = misa.cache(65535, 8, 40, 64, 256, 128, 128, misa.MISA_FP8_E4M3)
+    assert _calls(misa, many)[2](n=2, heads=256, most=2) == -2
+    assert read(n=(1 << 26) + 1) == -2  # of two heads
     long = misa.cache(1, 4096, 5000, 64, 1, 128, 128, misa.MISA_FP8_E4M3)
     for most in (1, 5, 80):
         need = misa.misa_block_attend_workspace_bytes(long, 32, 8, most, most, 0)
