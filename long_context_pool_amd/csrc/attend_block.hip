@@ -19,7 +19,7 @@ constexpr int row_shift(int RW) { return RW == 4 ? 7 : 6; }
 constexpr float kLift = 7.f;  // weights go up to 2^(kSlack + kLift) < 65504, f16's largest
 constexpr float kNoGroup = -1e9f;  // the exponent of a group without a page
 constexpr float kFar = 60.f, kNear = 8.f;
-constexpr int kGroups = 128;  // groups of 16 tokens that are looked up at a time
+constexpr int kGroups = 64;  // groups of 16 tokens that are looked up at a time
 
 struct TileArgs {
   const uint16_t* q;
@@ -100,8 +100,10 @@ __device__ __forceinline__ float halves_sum(float x) {
 //
 // RW = 4: the waves have 32 rows each.  RW = 2: two have 32 rows and half the tokens of
 // a tile each, two the same rows and the other half; their sums are joined at the end.
-// By memory, then: 16 rows of up to 32768 tokens, 64 heads on 8, five drafts each (789
-// MB) 201 to 213 us, 3.7 to 3.9 TB/s.
+// By memory, then, with two tiles' loads under way: 16 rows of up to 32768 tokens, 64
+// heads on 8, five drafts each (789 MB) 198 us, 4 TB/s (213 with one tile's and look-ups
+// between the tiles, whose branches' ends waited for all loads; the prompt above 7.73 ms
+// against 7.87).
 template <int D, int TK, int RW>
 __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attend_tiles_kernel(TileArgs a) {
   constexpr int kRowShift = row_shift(RW), kRows = 1 << kRowShift;
@@ -179,9 +181,12 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attend_tiles_kerne
     qf[s] = as_bf16x8(x);
   }
 
-  // Groups of 16 tokens, which are in one page and block: a stage of them at a time
-  // is looked up, while the stage before is worked on.
+  // Groups of 16 tokens, which are in one page and block, are looked up a stage of 64 at
+  // a time, a lane each, and by the waves in turn: where stage s begins, the wave of stage
+  // s + 1 puts what it found into LDS and looks its next one's pages up, whose scales it
+  // loads two stages later.  No tile's loads wait for these.
   const int32_t* table = a.table + static_cast<int64_t>(r) * a.row_pages;
+  int32_t own = wave;  // the wave's stage
   int32_t group_page = -1;
   uint32_t group_slot = kHidden;
   float group_k = 0.f, group_v = 0.f;
@@ -189,27 +194,29 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attend_tiles_kerne
     const uint32_t in = static_cast<uint32_t>(t) - div_page(t, a.page) * a.page.P;
     return (static_cast<uint32_t>(page) * a.kv_heads + kvh) * a.page.P + in;
   };
-  const auto group_token = [&](int32_t stage) { return (t0 + stage * GT) * TK + static_cast<int32_t>(threadIdx.x) * 16; };
-  const auto find_page = [&](int32_t stage) {
-    const int32_t t = group_token(stage);
+  const auto group_token = [&] { return (static_cast<int64_t>(t0) + own * GT) * TK + lane * 16; };
+  const auto find_pages = [&] {
+    const int64_t t = group_token();
     group_page = -1;
-    if (threadIdx.x < kGroups && t < min(most, t1 * TK)) group_page = table[div_page(t, a.page)];
+    if (t < min(most, t1 * TK)) group_page = table[div_page(static_cast<int32_t>(t), a.page)];
   };
-  const auto find_scales = [&](int32_t stage) {
+  const auto find_scales = [&] {
     group_slot = kHidden;
     if (group_page >= 0 && group_page < a.pages) {
-      group_slot = slot_at(group_token(stage), group_page);
+      group_slot = slot_at(static_cast<int32_t>(group_token()), group_page);
       group_k = a.k_scale[group_slot >> a.shift];
       group_v = a.v_scale[group_slot >> a.shift];
     }
   };
-  const auto keep_groups = [&](int32_t stage) {
-    if (threadIdx.x >= kGroups) return;
-    slots[(stage & 1) * kGroups + threadIdx.x] = group_slot;
-    k_unit[(stage & 1) * kGroups + threadIdx.x] = group_k;
-    v_exp[(stage & 1) * kGroups + threadIdx.x] =
-        group_slot == kHidden ? kNoGroup : static_cast<float>(static_cast<int>(__float_as_uint(group_v) >> 23) - 127);
+  const auto keep_groups = [&] {
+    const int at = (own & 1) * kGroups + lane;
+    slots[at] = group_slot;
+    k_unit[at] = group_k;
+    v_exp[at] = group_slot == kHidden ? kNoGroup : static_cast<float>(static_cast<int>(__float_as_uint(group_v) >> 23) - 127);
+    own += kThreads / kWave;
+    find_pages();
   };
+  static_assert(kGroups == kWave && kThreads == 4 * kWave, "a lane each, of four waves");
 
   // Thread i has chunk i % CC of tokens i / CC, + kThreads / CC, ...
   // Swizzles of the chunks, so that 16 rows' reads of a chunk (K) and four rows' of
@@ -227,52 +234,54 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attend_tiles_kerne
   // within a group.
   const uint8_t* k_from = a.k_pages + (my_token % 16) * D + my_chunk * 16;
   const uint8_t* v_from = a.v_pages + (my_token % 16) * D + my_chunk * 16;
-  uint4 kc[NC], vc[NC];
-  float ku[NC];
-  bool there[NC];  // V's tokens
-  const auto load_k = [&](int32_t tile) {
+  struct Codes {  // a thread's part of a tile
+    uint4 k[NC], v[NC];
+    float unit[NC];
+    bool there[NC];  // V's tokens
+  };
+  const auto load_k = [&](int32_t tile, Codes& x) __attribute__((always_inline)) {
     const int32_t first = ((tile - t0) & (2 * GT - 1)) * NG + my_token / 16;
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const uint32_t s = slots[first + i * (kThreads / CC) / 16];
-      ku[i] = k_unit[first + i * (kThreads / CC) / 16];
+      x.unit[i] = k_unit[first + i * (kThreads / CC) / 16];
       const uint64_t off = static_cast<uint64_t>(s != kHidden ? s : 0) * D;  // some page: what it holds is not used
-      kc[i] = *reinterpret_cast<const uint4*>(k_from + off);
+      x.k[i] = *reinterpret_cast<const uint4*>(k_from + off);
     }
   };
-  const auto load_v = [&](int32_t tile) {
+  const auto load_v = [&](int32_t tile, Codes& x) __attribute__((always_inline)) {
     const int32_t first = ((tile - t0) & (2 * GT - 1)) * NG + my_token / 16;
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const uint32_t s = slots[first + i * (kThreads / CC) / 16];
-      there[i] = s != kHidden;
-      const uint64_t off = static_cast<uint64_t>(there[i] ? s : 0) * D;
-      vc[i] = *reinterpret_cast<const uint4*>(v_from + off);
+      x.there[i] = s != kHidden;
+      const uint64_t off = static_cast<uint64_t>(x.there[i] ? s : 0) * D;
+      x.v[i] = *reinterpret_cast<const uint4*>(v_from + off);
     }
   };
-  const auto widen_k = [&](int b) {
+  const auto widen_k = [&](int b, const Codes& x) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int row = my_token + i * (kThreads / CC);
       uint4 lo, hi;
-      widen<false>(kc[i], ku[i], lo, hi);
+      widen<false>(x.k[i], x.unit[i], lo, hi);
       kt[b][k_at(row, 2 * my_chunk)] = lo;
       kt[b][k_at(row, 2 * my_chunk + 1)] = hi;
     }
   };
-  const auto widen_v = [&](int32_t tile, int b) {
+  const auto widen_v = [&](int32_t tile, int b, Codes& x) __attribute__((always_inline)) {
     // A NaN must not meet a weight of zero: tokens that no row sees are zeros, and where
     // some rows do not see some token, NaN codes are.
     const bool edge = (tile + 1) * TK > least;
     bool whole = !edge;
 #pragma unroll
-    for (int i = 0; i < NC; ++i) whole = whole && !__any(!there[i]);
+    for (int i = 0; i < NC; ++i) whole = whole && !__any(!x.there[i]);
     if (!whole) {
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
-        const bool seen = there[i] && tile * TK + my_token + i * (kThreads / CC) < most;
-        uint32_t* w = reinterpret_cast<uint32_t*>(&vc[i]);
+        const bool seen = x.there[i] && tile * TK + my_token + i * (kThreads / CC) < most;
+        uint32_t* w = reinterpret_cast<uint32_t*>(&x.v[i]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const uint32_t bad = seen && edge ? nan_bytes(w[j]) : 0u;
@@ -285,7 +294,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attend_tiles_kerne
     for (int i = 0; i < NC; ++i) {
       const int row = my_token + i * (kThreads / CC);
       uint4 lo, hi;
-      widen<true>(vc[i], 1.f, lo, hi);
+      widen<true>(x.v[i], 1.f, lo, hi);
       vt[b][v_at(row, 2 * my_chunk)] = lo;
       vt[b][v_at(row, 2 * my_chunk + 1)] = hi;
     }
@@ -385,35 +394,29 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attend_tiles_kerne
         acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, w[i], acc[j], 0, 0, 0);
       }
   };
-  // The next stage's, over three tiles; before a tile's loads, for which the
-  // compiler's waits where the branches meet would otherwise be too.
-  const auto next_groups = [&](int32_t n) {
-    const int32_t stage = n / GT + 1;
-    if (t0 + stage * GT < t1) {
-      if (n % GT == 0) find_page(stage);
-      if (n % GT == 1) find_scales(stage);
-      if (n % GT == 2) keep_groups(stage);
-    }
-  };
-
   if (threadIdx.x == 0) any_nan = 0;
-  find_page(0);
-  find_scales(0);
-  keep_groups(0);
+  find_pages();
+  find_scales();
+  if (own < 2) keep_groups();
   __syncthreads();
-  load_k(t0);
-  load_v(t0);
-  widen_k(0);
-  f32x16 st[NH];
-  f16x8 w[2 * NH];
-  widen_v(t0, 0);
-  for (int32_t tile = t0; tile < t1; ++tile) {
-    const int32_t n = tile - t0;
-    __syncthreads();
-    next_groups(n);
-    load_k(min(tile + 1, t1 - 1));  // no branch: the compiler would wait where it ends
-    load_v(min(tile + 1, t1 - 1));
+  constexpr int AHEAD = RW < 4 ? 2 : 1;  // tiles whose loads are under way
+  Codes codes[AHEAD];
+  load_k(t0, codes[0]);
+  load_v(t0, codes[0]);
+  if constexpr (AHEAD > 1) {
+    load_k(min(t0 + 1, t1 - 1), codes[1]);
+    load_v(min(t0 + 1, t1 - 1), codes[1]);
+  }
+  widen_k(0, codes[0]);
+  widen_v(t0, 0, codes[0]);
+  __syncthreads();
+  // Tile `tile`, number n of the split's; loads of tile + AHEAD to `to`, the next tile's are in `next`.
+  const auto step = [&](int32_t tile, int n, Codes& to, Codes& next) __attribute__((always_inline)) {
+    load_k(min(tile + AHEAD, t1 - 1), to);  // no branch: the compiler would wait where it ends
+    load_v(min(tile + AHEAD, t1 - 1), to);
     if (busy) {
+      f32x16 st[NH];
+      f16x8 w[2 * NH];
       float ve[2 * NH];
       exponents(tile, ve);
       score(n & 1, st);
@@ -421,8 +424,27 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attend_tiles_kerne
       add_values(n & 1, w);
     }
     if (tile + 1 < t1) {
-      widen_k(n + 1 & 1);
-      widen_v(tile + 1, n + 1 & 1);
+      widen_k(n + 1 & 1, next);
+      widen_v(tile + 1, n + 1 & 1, next);
+    }
+    __syncthreads();
+  };
+  int32_t tile = t0;
+  for (int32_t stage = 0; tile < t1; ++stage) {
+    if (own == stage + 1) keep_groups();
+    if (own == stage + 3) find_scales();
+    const int32_t end = min(tile + GT, t1);
+    if constexpr (AHEAD == 1) {
+      for (; tile < end; ++tile) step(tile, tile - t0, codes[0], codes[0]);
+    } else {
+      for (; tile + 1 < end; tile += 2) {
+        step(tile, 0, codes[0], codes[1]);
+        step(tile + 1, 1, codes[1], codes[0]);
+      }
+      if (tile < end) {  // the split's last
+        step(tile, 0, codes[0], codes[1]);
+        ++tile;
+      }
     }
   }
 
