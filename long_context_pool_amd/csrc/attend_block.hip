@@ -30,9 +30,12 @@ struct TileArgs {
   Packed rows;
   uint16_t* out;
   float* lse;
-  float* part_o;    // [n, heads, splits, d] sums of a split
-  float2* part_ml;  // [n, heads, splits] maximum (log2) and sum; 0: nothing seen
-  int32_t heads, share, kv_heads, splits, row_pages, pages, shift;
+  float* part_o;    // [kv_heads, slots, part_rows, d] sums of a part of a unit's tokens
+  float2* part_ml;  // [kv_heads, slots, part_rows] maximum (log2) and sum; 0: nothing seen
+  int2* where;      // [units] a unit's first slot and its number of them
+  int32_t slots, full;  // workgroups of a kv head (0: one a unit, by its number), of them at work together
+  int32_t part_rows;    // rows that a unit can have
+  int32_t heads, share, kv_heads, row_pages, pages, shift;
   uint32_t q_and, q_xor;  // a negative scale turns the queries' signs, a zero one clears them
   float scale2;           // |scale| * log2(e), above zero
   Div page, by_share;
@@ -72,7 +75,119 @@ __device__ __forceinline__ float halves_sum(float x) {
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
-// One workgroup of four waves per (tile of 128 rows, split, kv head): a wave has 32
+// Row `r` of the batch, the first of its rows of pairs, their number, and what they see.
+struct Unit {
+  int32_t r, begin, count;
+  int64_t flat0, flats;  // first pair of the unit, pairs of the row (below 2^27)
+  int64_t before;        // tokens before the new ones
+  int32_t least, most;   // tokens that its first and its last pair see
+  __device__ __forceinline__ bool there() const { return flat0 >= 0 && flat0 < flats; }
+};
+
+__device__ __forceinline__ int32_t seen_by(const TileArgs& a, int64_t before, int32_t token) {
+  const int64_t n = before + token + 1, cap = static_cast<int64_t>(a.row_pages) * a.page.P;  // at most 2^30
+  return static_cast<int32_t>(n < 0 ? 0 : n < cap ? n : cap);
+}
+
+template <int SHIFT>
+__device__ __forceinline__ Unit unit_of(const TileArgs& a, int64_t unit, int32_t r, int32_t begin, int32_t end) {
+  Unit u;
+  u.r = r;
+  u.begin = begin;
+  u.count = end - begin;
+  u.flat0 = (unit - unit_base(begin, a.share, SHIFT, r, 1)) << SHIFT;
+  u.flats = static_cast<int64_t>(max(u.count, 0)) * a.share;
+  u.before = static_cast<int64_t>(a.lengths[r]) - u.count;
+  if (u.there()) {
+    const int32_t last = static_cast<int32_t>(min(u.flat0 + (1 << SHIFT), u.flats)) - 1;
+    u.least = seen_by(a, u.before, static_cast<int32_t>(div_page(static_cast<int32_t>(u.flat0), a.by_share)));
+    u.most = seen_by(a, u.before, static_cast<int32_t>(div_page(last, a.by_share)));
+  }
+  return u;
+}
+
+constexpr int kMaxUnits = 1024;  // that are shared out
+constexpr int kMaxParts = 32;    // of a unit
+constexpr int kLeastTokens = 256;  // of a part
+
+// Slot `slot` of a kv head's: units' tiles in parts of at most q, the smallest q that gives
+// no more parts than there are slots to work together.  Each workgroup finds it out for
+// itself: with as many parts for each unit instead, five drafts on 16 rows of 16384 to
+// 32768 tokens took 199 us for 189, four 179 for 163 (heads of 256 732 for 660), 32 tokens
+// 575 for 530; one prompt of 512 tokens 27.5 for 30.0.
+template <int TK, int SHIFT>
+__device__ __forceinline__ bool part_of(const TileArgs& a, int32_t units, int32_t slot, int32_t* lds, int64_t& unit,
+                                        int32_t& first, int32_t& parts) {
+  int32_t *offsets = lds, *tiles = lds + kMaxUnits + 4;  // -1: no such unit
+  const int32_t rows = a.rows.rows;                      // <= units
+  for (int32_t i = threadIdx.x; i <= rows; i += kThreads) offsets[i] = a.rows.at(i);
+  __syncthreads();
+  for (int32_t u = threadIdx.x; u < units; u += kThreads) {
+    int32_t lo = 0, hi = rows - 1;  // the last row whose units begin at or before u
+    while (lo < hi) {
+      const int32_t mid = lo + (hi - lo + 1) / 2;
+      if (unit_base(offsets[mid], a.share, SHIFT, mid, 1) <= u)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    const Unit x = unit_of<SHIFT>(a, u, lo, offsets[lo], offsets[lo + 1]);
+    tiles[u] = x.there() ? (x.most + TK - 1) / TK : -1;
+  }
+  __syncthreads();
+  const int lane = lane_id();
+  float active = 0.f, sum = 0.f, top = 0.f;
+  for (int32_t u = lane; u < units; u += kWave) {
+    const float n = static_cast<float>(tiles[u]);
+    active += n >= 0.f;
+    sum += fmaxf(n, 0.f);
+    top = fmaxf(top, n);
+  }
+  active = lanes_reduce<kWave, false>(active);
+  sum = lanes_reduce<kWave, false>(sum);
+  top = lanes_reduce<kWave, true>(top);
+  const float budget = fminf(a.slots, fmaxf(a.full, active));
+  const auto parts_with = [&](int32_t n, int32_t q) {
+    return n < 0 ? 0u : max(1u, static_cast<uint32_t>(n + q - 1) / static_cast<uint32_t>(q));
+  };
+  const int32_t least = max(kLeastTokens / TK, (static_cast<int32_t>(top) + kMaxParts - 1) / kMaxParts);
+  int32_t lo = max(least, static_cast<int32_t>(sum * 0.999f / budget));
+  // ceil(n / q) < n / q + 1: parts of this size fit; and so do whole units.
+  int32_t hi = static_cast<int32_t>(top);
+  if (budget > active) hi = static_cast<int32_t>(fminf(top, sum * 1.001f / (budget - active) + 1.f));
+  hi = max(hi, lo);
+  while (lo < hi) {
+    const int32_t q = lo + (hi - lo) / 2;
+    float n = 0.f;  // exact where it fits
+    for (int32_t u = lane; u < units; u += kWave) n += static_cast<float>(parts_with(tiles[u], q));
+    if (lanes_reduce<kWave, false>(n) <= budget)
+      hi = q;
+    else
+      lo = q + 1;
+  }
+  int32_t before = 0;
+  for (int32_t u0 = 0; u0 < units; u0 += kWave) {
+    const int32_t mine = u0 + lane < units ? static_cast<int32_t>(parts_with(tiles[u0 + lane], lo)) : 0;
+    int32_t end = mine;  // and of the lanes before
+#pragma unroll
+    for (int d = 1; d < kWave; d *= 2) {
+      const int32_t other = __shfl_up(end, d);
+      if (lane >= d) end += other;
+    }
+    const uint64_t has = __ballot(before + end - mine <= slot && slot < before + end);
+    if (has) {
+      const int at = __builtin_ctzll(has);
+      unit = __builtin_amdgcn_readfirstlane(u0 + at);
+      first = __builtin_amdgcn_readlane(before + end - mine, at);
+      parts = __builtin_amdgcn_readlane(mine, at);
+      return true;
+    }
+    before += __builtin_amdgcn_readlane(end, kWave - 1);
+  }
+  return false;
+}
+
+// One workgroup of four waves per (tile of 128 rows, part of their tokens, kv head): a wave has 32
 // rows, and all share the tiles of TK tokens in LDS, K widened to bf16 and V to f16
 // as they are staged, one of two buffers while the other is worked on.
 //   S^T = K Q^T, O^T = V^T P^T  (32x32x16), a lane keeps one row (l % 32),
@@ -101,9 +216,9 @@ __device__ __forceinline__ float halves_sum(float x) {
 // RW = 4: the waves have 32 rows each.  RW = 2: two have 32 rows and half the tokens of
 // a tile each, two the same rows and the other half; their sums are joined at the end.
 // By memory, then, with two tiles' loads under way: 16 rows of up to 32768 tokens, 64
-// heads on 8, five drafts each (789 MB) 198 us, 4 TB/s (213 with one tile's and look-ups
-// between the tiles, whose branches' ends waited for all loads; the prompt above 7.73 ms
-// against 7.87).
+// heads on 8, five drafts each (789 MB) 189 us, 4.2 TB/s, four 163 us, 4.85 TB/s (five 213
+// with one tile's and look-ups between the tiles, whose branches' ends waited for all
+// loads, and 198 without; the prompt above 7.87 and 7.73 ms).
 template <int D, int TK, int RW>
 __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attend_tiles_kernel(TileArgs a) {
   constexpr int kRowShift = row_shift(RW), kRows = 1 << kRowShift;
@@ -128,43 +243,44 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attend_tiles_kerne
   const int c = lane & 31, g = lane >> 5;
   const int wave_rows = 32 * (wave % RW), h0 = wave / RW * NH;  // first row, first half of the tokens
   const int kvh = blockIdx.x % a.kv_heads;
-  const int rest = blockIdx.x / a.kv_heads;
-  const int split = rest % a.splits;
   const int64_t units = unit_base(a.rows.n, a.share, kRowShift, a.rows.rows, 1);
-  const int64_t unit = units - 1 - rest / a.splits;  // the longest rows of a prompt first
+  const int32_t slot = blockIdx.x / a.kv_heads;
+  int64_t unit = units - 1 - slot;  // the longest rows of a prompt first
+  int32_t first = slot, parts = 1;
+  if (a.slots) {
+    static_assert(sizeof(kt) >= (2 * kMaxUnits + 4) * sizeof(int32_t), "rows' offsets and units' tiles");
+    if (!part_of<TK, kRowShift>(a, static_cast<int32_t>(units), slot, reinterpret_cast<int32_t*>(kt), unit, first, parts))
+      return;
+    if (kvh == 0 && slot == first && threadIdx.x == 0) a.where[unit] = make_int2(first, parts);
+  }
   const int32_t r = last_row(a.rows.rows, unit,
                              [&](int32_t x) { return unit_base(a.rows.at(x), a.share, kRowShift, x, 1); });
-  const int32_t begin = a.rows.at(r), count = a.rows.at(r + 1) - begin;
-  const int64_t flat0 = (unit - unit_base(begin, a.share, kRowShift, r, 1)) * kRows;
-  const int64_t flats = static_cast<int64_t>(max(count, 0)) * a.share;  // below 2^27
-  if (flat0 < 0 || flat0 >= flats) return;
-  const int32_t cap = a.row_pages * static_cast<int32_t>(a.page.P);
-  const int64_t before = static_cast<int64_t>(a.lengths[r]) - count;  // tokens before the new ones
-  const auto seen_by = [&](int32_t t) {
-    const int64_t n = before + t + 1;
-    return static_cast<int32_t>(n < 0 ? 0 : n < cap ? n : cap);
-  };
+  const Unit u = unit_of<kRowShift>(a, unit, r, a.rows.at(r), a.rows.at(r + 1));
+  if (!u.there()) return;
+  const int32_t least = u.least, most = u.most;
   const auto token_of = [&](int32_t flat) { return static_cast<int32_t>(div_page(flat, a.by_share)); };
-  const int32_t last = static_cast<int32_t>(min(flat0 + kRows, flats)) - 1;
-  const int32_t least = seen_by(token_of(static_cast<int32_t>(flat0))), most = seen_by(token_of(last));
-  const int32_t flat = static_cast<int32_t>(flat0) + wave_rows + c;
+  const int32_t last = static_cast<int32_t>(min(u.flat0 + kRows, u.flats)) - 1;
+  const int32_t flat = static_cast<int32_t>(u.flat0) + wave_rows + c;
   const bool mine = flat <= last;
   const int32_t token = token_of(min(flat, last));
-  const int32_t seen = seen_by(token);
-  const int64_t at = static_cast<int64_t>(begin + token) * a.heads + kvh * a.share + (min(flat, last) - token * a.share);
-  const bool busy = static_cast<int32_t>(flat0) + wave_rows <= last;  // the wave has rows
+  const int32_t seen = seen_by(a, u.before, token);
+  const int64_t at = static_cast<int64_t>(u.begin + token) * a.heads + kvh * a.share + (min(flat, last) - token * a.share);
+  const auto part_at = [&] { return (static_cast<int64_t>(kvh) * a.slots + slot) * a.part_rows + wave_rows + c; };
+  const bool busy = static_cast<int32_t>(u.flat0) + wave_rows <= last;  // the wave has rows
 
-  const int32_t tiles = (most + TK - 1) / TK, per = (tiles + a.splits - 1) / a.splits;
-  const int32_t t0 = split * per, t1 = min(t0 + per, tiles);
+  const int32_t tiles = (most + TK - 1) / TK, per = (tiles + parts - 1) / parts;
+  // Scalars, which the compiler does not see through the search above.
+  const int32_t t0 = __builtin_amdgcn_readfirstlane((slot - first) * per);
+  const int32_t t1 = __builtin_amdgcn_readfirstlane(min(t0 + per, tiles));
   if (t0 >= t1) {
     if (h0 > 0) return;
     if (mine && g == 0) {
-      if (a.splits > 1)
-        a.part_ml[at * a.splits + split] = make_float2(-INFINITY, 0.f);
+      if (parts > 1)
+        a.part_ml[part_at()] = make_float2(-INFINITY, 0.f);
       else if (a.lse)
         a.lse[at] = -INFINITY;
     }
-    if (mine && a.splits == 1)
+    if (mine && parts == 1)
       for (int i = 0; i < D / 16; ++i)
         *reinterpret_cast<uint4*>(a.out + at * D + (2 * i + g) * 8) = make_uint4(0, 0, 0, 0);
     return;
@@ -492,21 +608,21 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attend_tiles_kerne
     }
   }
   const float unit_o = __builtin_amdgcn_ldexpf(1.f, static_cast<int>(fmaxf(eref, -200.f) - kLift));
-  const int64_t part = at * a.splits + split;
+  const int64_t part = parts > 1 ? part_at() : 0;
   if (g == 0) {
-    if (a.splits > 1)
+    if (parts > 1)
       a.part_ml[part] = make_float2(m, l);
     else if (a.lse)
       a.lse[at] = l == 0.f ? -INFINITY : final_lse(m, l);
   }
-  const float f = a.splits > 1 ? unit_o : l == 0.f ? 0.f : unit_o / l;
+  const float f = parts > 1 ? unit_o : l == 0.f ? 0.f : unit_o / l;
 #pragma unroll
   for (int j = 0; j < NJ; ++j)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int d = 32 * j + 8 * e + 4 * g;
       const float4 o = make_float4(acc[j][4 * e] * f, acc[j][4 * e + 1] * f, acc[j][4 * e + 2] * f, acc[j][4 * e + 3] * f);
-      if (a.splits > 1) {
+      if (parts > 1) {
         *reinterpret_cast<float4*>(a.part_o + part * D + d) = o;
       } else {
         bf16x2 x, y;
@@ -520,9 +636,9 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attend_tiles_kerne
     }
 }
 
-// The splits of a query's heads joined: D / 4 threads a head, 1024 / D heads a
+// The parts of a query's heads joined: D / 4 threads a head, 1024 / D heads a
 // workgroup.  75 queries of 64 heads in four splits 5 us.
-template <int D>
+template <int D, int RW>
 __global__ __launch_bounds__(256) void join_tiles_kernel(TileArgs a) {
   constexpr int T = D / 4;
   const int32_t i = blockIdx.x;
@@ -531,14 +647,22 @@ __global__ __launch_bounds__(256) void join_tiles_kernel(TileArgs a) {
   const int head = blockIdx.y * (256 / T) + threadIdx.x / T, d = threadIdx.x % T * 4;
   if (head >= a.heads) return;
   const int64_t at = static_cast<int64_t>(i) * a.heads + head;
-  const float2* ml = a.part_ml + at * a.splits;
+  const int32_t kvh = head / a.share;
+  const int64_t flat = static_cast<int64_t>(i - begin) * a.share + (head - kvh * a.share);
+  int2 w = a.where[unit_base(begin, a.share, row_shift(RW), r, 1) + (flat >> row_shift(RW))];
+  if (w.y == 1) return;  // written already
+  w.y = min(max(w.y, 1), kMaxParts);  // whatever offsets that do not ascend left there
+  w.x = min(max(w.x, 0), a.slots - w.y);
+  if (w.x < 0) return;
+  const int64_t part = (static_cast<int64_t>(kvh) * a.slots + w.x) * a.part_rows + (flat & ((1 << row_shift(RW)) - 1));
+  const float2* ml = a.part_ml + part;
   float m = -INFINITY, l = 0.f;
-  for (int s = 0; s < a.splits; ++s) m = fmaxf(m, ml[s].x);
+  for (int s = 0; s < w.y; ++s) m = fmaxf(m, ml[static_cast<int64_t>(s) * a.part_rows].x);
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s = 0; s < a.splits; ++s) {
-    const float2 x = ml[s];
+  for (int s = 0; s < w.y; ++s) {
+    const float2 x = ml[static_cast<int64_t>(s) * a.part_rows];
     if (x.y == 0.f) continue;  // nothing seen, nothing written
-    const float4 y = *reinterpret_cast<const float4*>(a.part_o + (at * a.splits + s) * D + d);
+    const float4 y = *reinterpret_cast<const float4*>(a.part_o + (part + static_cast<int64_t>(s) * a.part_rows) * D + d);
     const float f = part_factor(x.x, x.y, m);
     l += x.y * f;
     o.x += y.x * f;
@@ -558,7 +682,6 @@ __global__ __launch_bounds__(256) void join_tiles_kernel(TileArgs a) {
 }
 
 constexpr int kSlots = 512;  // workgroups that the card holds at a time
-constexpr int kMaxParts = 32;
 
 // Two waves' rows where no row of the batch has more: 16 rows of 32768 tokens, 64 heads
 // on 8 of 128, eight new tokens each (64 pairs of query and head) 210 us, 262 with
@@ -571,34 +694,40 @@ int64_t tile_units(const Cache& c, const BlockAttend& b) {
   return unit_base(b.n, b.heads / c.kv_heads, row_shift(row_waves(c, b)), c.rows, 1);
 }
 
-// As many splits as fill the card once, of the units that rows with up to `most` new
-// tokens can have (counted with a unit more for each row of the table, as the grid is,
-// five drafts on 16 rows have two splits for four: 333 us for 215).
-int32_t tile_splits(const Cache& c, const BlockAttend& b) {
-  const int64_t rows = 32 * row_waves(c, b), most = std::max(b.most, 1);
+// Slots of a kv head where units are shared out in parts: if those that rows with up to
+// `most` new tokens can have leave half of the card without work; as many as the card
+// holds, or one a unit.  (Counted with a unit more for each row of the table, as the grid
+// is, five drafts on 16 rows had half the parts: 333 us for 215.)
+int32_t tile_slots(const Cache& c, const BlockAttend& b) {
+  const int64_t rows = 32 * row_waves(c, b), most = std::max(b.most, 1), units = tile_units(c, b);
   const int64_t whole = ((b.n - 1) / most + 1) * ((most * (b.heads / c.kv_heads) - 1) / rows + 1);
-  const int64_t groups = std::min(tile_units(c, b), whole) * c.kv_heads;
-  const int64_t longest = (static_cast<int64_t>(c.row_pages) * c.P + 255) / 256;  // four tiles a split
-  return static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>({kSlots / groups, longest, kMaxParts})));
+  const int64_t longest = (static_cast<int64_t>(c.row_pages) * c.P + kLeastTokens - 1) / kLeastTokens;
+  if (std::min(units, whole) * c.kv_heads > kSlots / 2 || longest < 2 || units > kMaxUnits) return 0;
+  const int64_t useful = units * std::min<int64_t>(longest, kMaxParts);
+  return static_cast<int32_t>(std::max(units, std::min<int64_t>(kSlots / c.kv_heads, useful)));
+}
+
+int32_t part_rows(const Cache& c, const BlockAttend& b) {
+  return static_cast<int32_t>(std::min<int64_t>(32 * row_waves(c, b), static_cast<int64_t>(b.n) * (b.heads / c.kv_heads)));
 }
 
 template <int D, int TK, int RW>
 hipError_t launch_tiles_dim(const TileArgs& a, uint32_t grid, hipStream_t st) {
   attend_tiles_kernel<D, TK, RW><<<grid, kThreads, 0, st>>>(a);
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess || a.splits == 1) return e;
+  if (e != hipSuccess || a.slots == 0) return e;
   const int per = 1024 / D;
-  join_tiles_kernel<D><<<dim3(a.rows.n, (a.heads + per - 1) / per), 256, 0, st>>>(a);
+  join_tiles_kernel<D, RW><<<dim3(a.rows.n, (a.heads + per - 1) / per), 256, 0, st>>>(a);
   return hipGetLastError();
 }
 
 }  // namespace
 
 size_t attend_tiles_ws_bytes(const Cache& c, const BlockAttend& b) {
-  const int32_t splits = tile_splits(c, b);
-  if (splits == 1) return 0;
-  const size_t parts = static_cast<size_t>(b.n) * b.heads * splits;
-  return align_up(parts * sizeof(float2)) + parts * c.dv * sizeof(float);
+  const int32_t slots = tile_slots(c, b);
+  if (slots == 0) return 0;
+  const size_t parts = static_cast<size_t>(slots) * c.kv_heads * part_rows(c, b);
+  return align_up(parts * sizeof(float2)) + align_up(parts * c.dv * sizeof(float)) + tile_units(c, b) * sizeof(int2);
 }
 
 hipError_t launch_attend_tiles(const Cache& c, const BlockAttend& b, hipStream_t st) {
@@ -616,10 +745,14 @@ hipError_t launch_attend_tiles(const Cache& c, const BlockAttend& b, hipStream_t
   a.heads = b.heads;
   a.share = b.heads / c.kv_heads;
   a.kv_heads = c.kv_heads;
-  a.splits = tile_splits(c, b);
-  const size_t parts = static_cast<size_t>(b.n) * b.heads * a.splits;
-  a.part_ml = static_cast<float2*>(b.ws);
-  a.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(b.ws) + align_up(parts * sizeof(float2)));
+  a.slots = tile_slots(c, b);
+  a.full = kSlots / c.kv_heads;
+  a.part_rows = part_rows(c, b);
+  const size_t parts = static_cast<size_t>(a.slots) * c.kv_heads * a.part_rows;
+  uint8_t* ws = static_cast<uint8_t*>(b.ws);
+  a.part_ml = reinterpret_cast<float2*>(ws);
+  a.part_o = reinterpret_cast<float*>(ws + align_up(parts * sizeof(float2)));
+  a.where = reinterpret_cast<int2*>(ws + align_up(parts * sizeof(float2)) + align_up(parts * c.dv * sizeof(float)));
   a.row_pages = c.row_pages;
   a.pages = c.pages;
   a.shift = __builtin_ctz(static_cast<uint32_t>(b.block));
@@ -628,7 +761,7 @@ hipError_t launch_attend_tiles(const Cache& c, const BlockAttend& b, hipStream_t
   a.scale2 = b.scale == 0.f ? 1.f : std::fabs(b.scale) * kLog2e;
   a.page = make_div(c.P);
   a.by_share = make_div(a.share);
-  const uint32_t grid = static_cast<uint32_t>(tile_units(c, b) * c.kv_heads * a.splits);
+  const uint32_t grid = static_cast<uint32_t>((a.slots ? a.slots : tile_units(c, b)) * c.kv_heads);
   const bool two = row_waves(c, b) == 2;
   switch (c.dk) {
     case 64: return two ? launch_tiles_dim<64, 64, 2>(a, grid, st) : launch_tiles_dim<64, 64, 4>(a, grid, st);

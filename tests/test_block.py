@@ -597,6 +597,25 @@ def test_attend_long_rows_in_splits(misa, most):
 
 
 @gpu
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("most", [2, 100])
+@pytest.mark.parametrize("lengths,counts", [
+    ([5000, 4, 0, 600, 2500, 300], [3, 4, 0, 1, 0, 2]),  # parts of one row and whole rows
+    ([900, 700], [60, 9]),  # units of one row, most of them alike
+    ([40, 7], [3, 5]),  # fewer tokens than a part's least
+    ([0, 1, 700], [2, 3, 2]),  # queries before the first token
+    ([700] * 5 + [0] * 1200, [2] * 5 + [0] * 1200),  # more rows than are shared out
+    ([300] + [60 + i % 50 for i in range(279)], [1] * 280),  # more units than workgroups at a time
+])
+def test_attend_parts(misa, d, most, lengths, counts):
+    _log(f"[gpu] block attend parts {d} {most} {lengths[:6]} {counts[:6]}")
+    g = torch.Generator().manual_seed(31)
+    c, table, *pools = _pool(misa, g, lengths, 32, 16, 2, d)
+    q = torch.randn(sum(counts) + 3, 6, d, generator=g).bfloat16()
+    _check_attend(misa, c, 16, 6, 0, 0.09, _offsets(counts), q, pools, table, lengths, None, most)
+
+
+@gpu
 @pytest.mark.parametrize("d,kv,heads,k", [(64, 1, 4, 7), (128, 2, 16, 40), (128, 1, 20, 130), (256, 1, 2, 64)])
 def test_attend_lists(misa, d, kv, heads, k):
     """A list per query: any order, padding, tokens it does not see yet, the same token twice."""
