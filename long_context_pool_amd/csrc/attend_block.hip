@@ -75,9 +75,9 @@ __device__ __forceinline__ float halves_sum(float x) {
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
-// Row `r` of the batch, the first of its rows of pairs, their number, and what they see.
+// Up to 2^SHIFT of a batch row's (query, query head of a kv head) pairs: a tile's rows.
 struct Unit {
-  int32_t r, begin, count;
+  int32_t r, begin, count;  // the batch row, its first packed query, its queries
   int64_t flat0, flats;  // first pair of the unit, pairs of the row (below 2^27)
   int64_t before;        // tokens before the new ones
   int32_t least, most;   // tokens that its first and its last pair see
