@@ -40,8 +40,9 @@ misa_status check_block_pools(const void* k_pages, const float* k_scale, const v
 }
 
 // One query at a time where each has a list of its own, or a row has one new token (8
-// rows of 131072 tokens, 64 heads on 8: 297 us, 335 in tiles; 32 rows of 8192 86 and 98
-// us); otherwise tiles of a row's queries share its keys and values.
+// rows of 131072 tokens, 64 heads on 8: 297 us, 310 in tiles; 32 rows of 8192 86 and 96
+// us); otherwise tiles of a row's queries share its keys and values (two on 16 rows of
+// 32768: 160 us, 278 one by one).
 bool one_by_one(const misa::BlockAttend& b) { return b.k > 0 || b.most <= 1; }
 
 misa_status check_block_attend(const misa_cache* cache, int32_t heads, misa::BlockAttend& b, Cache& c) {

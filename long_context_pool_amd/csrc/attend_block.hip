@@ -204,10 +204,10 @@ __device__ __forceinline__ bool part_of(const TileArgs& a, int32_t units, int32_
 //
 // Bound by the matrix unit, LDS and the vector unit taking turns, at clocks that power
 // holds back (1.85 to 2.1 of 2.4 GHz): 8192 queries of three rows of up to 32768 tokens,
-// 64 heads on 8 of 128 (6.96 TFLOP), 7.5 to 8.1 ms on several cards, 860 to 925 TFLOP/s,
-// 71 to 76% of what a large library product reaches; matrix unit busy 44%.  Of it the
+// 64 heads on 8 of 128 (6.96 TFLOP), 7.5 to 8.2 ms on several cards, 850 to 925 TFLOP/s,
+// 70 to 76% of what a large library product reaches; matrix unit busy 44%.  Of it the
 // values' products take 2.9 ms, the scores' 2.2, widening the tiles 1.6, the
-// exponentials 0.2.  Heads of 64 763 TFLOP/s, of 256 (one workgroup a CU) 620.
+// exponentials 0.2.  Heads of 64 780 to 810 TFLOP/s, of 256 (one workgroup a CU) 635.
 // Tried and not kept: scores on the 8-bit matrix instructions with queries in two
 // e4m3 parts (10% less time, but sums of products off by 2^-18, more than fp32's);
 // 256 rows a workgroup, in step (9.4 ms) or in two groups that take turns (equal);
@@ -704,8 +704,8 @@ __global__ __launch_bounds__(256) void join_tiles_kernel(TileArgs a) {
 constexpr int kSlots = 512;  // workgroups that the card holds at a time
 
 // Two waves' rows where no row of the batch has more: 16 rows of 32768 tokens, 64 heads
-// on 8 of 128, eight new tokens each (64 pairs of query and head) 210 us, 262 with
-// four waves' rows; nine 376 and 277 us.
+// on 8 of 128, eight new tokens each (64 pairs of query and head) 198 us, 223 with
+// four waves' rows; nine 334 and 252 us.
 int row_waves(const Cache& c, const BlockAttend& b) {
   return c.dk <= 128 && static_cast<int64_t>(b.most) * (b.heads / c.kv_heads) <= 64 ? 2 : 4;
 }
