@@ -542,7 +542,7 @@ misa_status misa_block_read(const misa_cache* cache, int32_t block_tokens, int32
  * be in its range, and cached values below 2^90.  A weight goes into its products
  * in 16 bits where queries are worked on one by one (one new token a row, or lists);
  * where several share a pass in 11 bits, or to 2^-32 of the largest weight times the
- * largest value that the row's loudest block may hold.  Limits: heads a multiple of
+ * largest value that the loudest block may hold of those that the query sees.  Limits: heads a multiple of
  * kv_heads, heads <= 1024, n <= 2^20, n * heads <= 2^26 (2^23 one by one; otherwise
  * rows * kv_heads <= 2^23), 0 <= k <= 2^20, |scale| <= 2^127.  ws must hold misa_block_attend_workspace_bytes(...) bytes (0: invalid
  * arguments or no workspace needed); it carries nothing from one call to the next. */

@@ -197,8 +197,9 @@ __device__ __forceinline__ bool part_of(const TileArgs& a, int32_t units, int32_
 // types, K's with its scale.
 // Weights are f16, in one part of 11 bits, lifted by 2^7 so that what f16 loses is
 // 2^-32 of the largest; maximum, sums and O are fp32.  V's scale goes into the weights
-// relative to a reference exponent, `eref`, which O's registers are in units of and
-// which follows the tiles' loudest scale when that leaves its neighbourhood.
+// relative to a reference exponent of the row, `eref`, which O's registers are in units of
+// and which follows the loudest scale that the row sees in a tile when that leaves its
+// neighbourhood.
 // NaN values of tokens that some rows do not see yet are left out as zeros, since a
 // weight of zero would not hide them, and put in at the end for the rows that see them.
 //
@@ -422,7 +423,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attend_tiles_kerne
 #pragma unroll
     for (int e = 0; e < 16; ++e) acc[j][e] = 0.f;
   float m = -INFINITY, l = 0.f;  // of this lane's row, and of its half of the tokens
-  float eref = kNoGroup, loudest = kNoGroup;  // whole numbers, uniform
+  float eref = kNoGroup, loudest = kNoGroup;  // whole numbers, of what this lane's row sees
   const int vrow = 4 * g + (lane & 15) / 4, vcol = 2 * (lane >> 4 & 1) + (lane & 3) / 2;  // transposing reads
 
   const auto score = [&](int b, f32x16 (&st)[NH]) __attribute__((always_inline)) {
@@ -436,7 +437,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attend_tiles_kerne
       for (int h = 0; h < NH; ++h)
         st[h] = mfma32_bf16(as_bf16x8(kt[b][k_at(32 * (h0 + h) + c, 2 * s + g)]), qf[s], st[h]);
   };
-  // The exponents of a tile's groups, uniform but in vector registers: as scalars they
+  // The exponents of a tile's groups, alike in all lanes but in vector registers: as scalars they
   // would cost the way there and its waits (a third of the weights' time).
   const auto exponents = [&](int32_t tile, float (&ve)[2 * NH]) __attribute__((always_inline)) {
     const int32_t first = ((tile - t0) & (2 * GT - 1)) * NG + 2 * h0;
@@ -444,15 +445,15 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attend_tiles_kerne
     for (int i = 0; i < 2 * NH; ++i) ve[i] = v_exp[first + i];
   };
   // Weights of a tile from its scores.
-  const auto weigh = [&](int32_t tile, const float (&ve)[2 * NH], f32x16 (&st)[NH], f16x8 (&w)[2 * NH]) __attribute__((always_inline)) {
-    float loud = ve[0], still = ve[0];
+  const auto weigh = [&](int32_t tile, float (&ve)[2 * NH], f32x16 (&st)[NH], f16x8 (&w)[2 * NH]) __attribute__((always_inline)) {
+    float still = ve[0];
 #pragma unroll
-    for (int i = 1; i < 2 * NH; ++i) {
-      loud = fmaxf(loud, ve[i]);
-      still = fminf(still, ve[i]);
-    }
+    for (int i = 1; i < 2 * NH; ++i) still = fminf(still, ve[i]);
     if ((tile + 1) * TK > least || __any(still == kNoGroup)) {  // some row does not see some token
       __builtin_amdgcn_sched_barrier(0);  // a branch, not 32 selects in every tile
+      // A block behind what a row sees has no part in that row's reference, however loud.
+#pragma unroll
+      for (int i = 0; i < 2 * NH; ++i) ve[i] = tile * TK + 32 * h0 + 16 * i < seen ? ve[i] : kNoGroup;
 #pragma unroll
       for (int h = 0; h < NH; ++h)
 #pragma unroll
@@ -460,6 +461,9 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attend_tiles_kerne
           st[h][e] = tile * TK + 32 * (h0 + h) + 8 * (e / 4) + 4 * g + e % 4 < seen && ve[2 * h + e / 8] != kNoGroup
                          ? st[h][e] : -INFINITY;
     }
+    float loud = ve[0];
+#pragma unroll
+    for (int i = 1; i < 2 * NH; ++i) loud = fmaxf(loud, ve[i]);
     float high = -INFINITY;
 #pragma unroll
     for (int h = 0; h < NH; ++h)

@@ -539,6 +539,25 @@ def test_attend_blocks_of_far_scales(misa, most):
 
 @gpu
 @pytest.mark.parametrize("most", [1, 3, MANY])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("heads", [1, 6])
+@pytest.mark.parametrize("far", [20, 40])
+def test_attend_loud_blocks_that_are_not_seen_yet(misa, most, d, heads, far):
+    """New tokens over several blocks of one tile of tokens (of 32 or 64), the later blocks 2^far louder: a query
+    that sees the quiet ones alone loses nothing by what is behind it."""
+    _log(f"[gpu] block attend loud blocks behind {most} {d} {heads} {far}")
+    g = torch.Generator().manual_seed(41)
+    lengths, counts = [64, 150, 70, 200], [64, 40, 3, 32]
+    c, table, k, ks, v, vs = _pool(misa, g, lengths, 16, 16, 1, d)
+    vs *= 2.0 ** -20
+    for r, page in ((0, 2), (0, 3), (1, 8), (1, 9), (2, 4), (3, 11)):
+        vs[table[r, page].item()] *= 2.0 ** far
+    q = torch.randn(sum(counts), heads, d, generator=g).bfloat16()
+    _check_attend(misa, c, 16, heads, 0, 0.05, _offsets(counts), q, (k, ks, v, vs), table, lengths, None, most)
+
+
+@gpu
+@pytest.mark.parametrize("most", [1, 3, MANY])
 @pytest.mark.parametrize("d", [64, 128])
 def test_attend_nan_where_it_is_not_seen(misa, most, d):
     """NaN behind the row's end, in pages it lost, and at tokens that only later queries see."""
