@@ -455,7 +455,9 @@ typedef enum {
  * Efficient Context Window Extension of Large Language Models", section 3.2):
  * pairs that turn `fast` times and more in `original` positions keep f_i, those
  * that turn `slow` times and fewer have f_i / factor, with a linear ramp over i
- * between; and an amplitude of 1 + 0.1 ln(factor). */
+ * between, from the last whole i that turns `fast` times (or 0) to the first that turns
+ * `slow` times, beyond the last pair if need be (rot - 1 at most); and an amplitude of
+ * 1 + 0.1 ln(factor). */
 typedef struct {
   int32_t kind, rot; /* a misa_rope_kind; rot as in misa_rope_spec */
   double base;       /* > 1 */

@@ -119,16 +119,20 @@ misa_status misa_rope_frequencies(const misa_rope_scaling* scaling, double* freq
   const auto pair_of = [&](double turns) {
     return s.rot * std::log(s.original / (2.0 * M_PI * turns)) / (2.0 * std::log(s.base));
   };
-  double low = 0.0, high = 1.0;
+  // The ramp's ends.  Its upper one lies behind the last pair where that one turns often
+  // enough, as far as the rotated size less one.
+  double first = 0.0, last = 0.0, low = 0.0, high = 1.0;
   if (s.kind == MISA_ROPE_PARTS) {
-    low = std::max(std::floor(pair_of(s.fast)), 0.0);
-    high = std::min(std::ceil(pair_of(s.slow)), pairs - 1.0);
+    first = pair_of(s.fast);
+    last = pair_of(s.slow);
+    low = std::max(std::floor(first), 0.0);
+    high = std::min(std::ceil(last), s.rot - 1.0);
   }
   for (int32_t i = 0; i < pairs; ++i) {
     const double f = std::pow(s.base, -2.0 * i / s.rot);
     double slowed = s.kind == MISA_ROPE_LINEAR ? 1.0 : 0.0;  // share of f / factor
-    if (s.kind == MISA_ROPE_PARTS)
-      slowed = std::min(std::max((i - low) / std::max(high - low, 1e-3), 0.0), 1.0);
+    if (s.kind == MISA_ROPE_PARTS && i > first)  // i >= last: also where no pair turns `slow` times
+      slowed = i >= last ? 1.0 : std::min(std::max((i - low) / std::max(high - low, 1e-3), 0.0), 1.0);
     freq[i] = s.kind == MISA_ROPE_PLAIN ? f : f * (1.0 - slowed + slowed / s.factor);
   }
   *amplitude = s.kind == MISA_ROPE_PARTS ? static_cast<float>(1.0 + 0.1 * std::log(s.factor)) : 1.f;

@@ -89,6 +89,41 @@ def test_rope_frequencies(misa):
     assert all(math.isfinite(f) for f in got[0])
 
 
+@pytest.mark.parametrize("rot,base,factor,original,fast,slow", [
+    (64, 1e4, 4.0, 65536.0, 32.0, 1.0),  # the last pair turns 1.39 times: the ramp ends behind it
+    (64, 1e4, 4.0, 131072.0, 32.0, 1.0),
+    (128, 1e4, 4.0, 131072.0, 32.0, 1.0),
+    (128, 1e4, 4.0, 65536.0, 32.0, 1.0),
+    (64, 1e4, 4.0, 32768.0, 32.0, 1.0),
+    (96, 5e5, 8.0, 8192.0, 4.0, 1.0),
+    (64, 1e4, 40.0, 20.0, 32.0, 1.0),  # no pair turns `fast` times
+    (64, 1e4, 40.0, 5.0, 2.0, 1.0),  # every pair turns fewer than `slow` times
+    (2, 1e4, 4.0, 5.0, 2.0, 1.0),
+    (2, 1e4, 4.0, 100.0, 32.0, 1.0),
+])
+def test_rope_frequencies_by_parts(misa, rot, base, factor, original, fast, slow):
+    """The header's rule: pairs that turn `fast` times keep f, those that turn `slow` times and fewer have
+    f / factor, and what lies between is on one line over the pairs' numbers."""
+    freq, _ = misa.misa_rope_frequencies(misa.rope_scaling(misa.MISA_ROPE_PARTS, rot, base, factor, original, fast, slow))
+    plain = [base ** (-2.0 * i / rot) for i in range(rot // 2)]
+    turns = [original * f / (2 * math.pi) for f in plain]
+    share = [(1 - f / p) / (1 - 1 / factor) for f, p in zip(freq, plain)]  # of f / factor
+    ramp = []
+    for i in range(rot // 2):
+        if turns[i] >= fast:
+            assert share[i] == pytest.approx(0, abs=1e-12), i
+        elif turns[i] <= slow:
+            assert share[i] == pytest.approx(1, abs=1e-12), i
+        else:
+            ramp.append((i, share[i]))
+            assert share[i] < 1, i
+    # its ends: the pairs (of any whole number) next to those that turn `fast` and `slow` times
+    at = [rot * math.log(original / (2 * math.pi * x)) / (2 * math.log(base)) for x in (fast, slow)]
+    low, high = max(math.floor(at[0]), 0), math.ceil(at[1])
+    for i, x in ramp:
+        assert x == pytest.approx((i - low) / (high - low), abs=1e-12), i
+
+
 def test_rope_frequencies_refuse(misa):
     out, amplitude = (ctypes.c_double * 1024)(), ctypes.c_float()
 
