@@ -138,7 +138,9 @@ __device__ __forceinline__ bool part_of(const TileArgs& a, int32_t units, int32_
   const int lane = lane_id();
   float active = 0.f, sum = 0.f, top = 0.f;
   for (int32_t u = lane; u < units; u += kWave) {
-    const float n = static_cast<float>(tiles[u]);
+    // Up to 2^25; beyond 2^24 fp32 holds even numbers alone, and none may be counted short.
+    const int32_t whole = tiles[u];
+    const float n = static_cast<float>(whole > 1 << 24 ? whole + (whole & 1) : whole);
     active += n >= 0.f;
     sum += fmaxf(n, 0.f);
     top = fmaxf(top, n);

@@ -689,6 +689,32 @@ def test_attend_parts(misa, d, most, lengths, counts):
 
 
 @gpu
+def test_attend_rows_of_more_tiles_than_fp32_counts(misa):
+    """Heads of 256, a row of 2^24 + 1 tiles of 32 tokens beside a short one: 32 parts hold all of them.  Every
+    score is 0 and every value a power of two, so that sums are exact but for the logarithm and the division."""
+    _log("[gpu] block attend 2^24 + 1 tiles")
+    P, d = 4096, 256
+    width = 1 << 18
+    length = (1 << 29) + 1
+    c = misa.cache(2, width, 3, P, 1, d, d, misa.MISA_FP8_E4M3)
+    table = torch.zeros(2, width, dtype=torch.int32)
+    table[0, length // P * 31 // 32:] = 1  # the last thirty-second and what is behind it
+    table[1] = 2
+    k = torch.zeros(3, 1, P, d).to(E4M3)
+    v = torch.tensor([1.0, -1.0, 2.0]).view(3, 1, 1, 1).expand(3, 1, P, d).contiguous().to(E4M3)
+    ks, vs = torch.ones(3, 1, P // 128), torch.ones(3, 1, P // 128)
+    out, lse = torch.empty(3, 1, d, dtype=torch.bfloat16, device="cuda"), torch.empty(3, 1, device="cuda")
+    ws = torch.empty(misa.misa_block_attend_workspace_bytes(c, 128, 1, 3, 2, 0), dtype=torch.uint8, device="cuda")
+    misa.misa_block_attend(c, 128, 1, 3, 2, 0, 1.0, *_cuda(_offsets([2, 1]), torch.ones(3, 1, d).bfloat16(), k, ks, v, vs, table,
+                           torch.tensor([length, 40]).int()), None, out, lse, ws)
+    quiet = length // P * 31 // 32 * P
+    for i, (n, mean) in enumerate([(length - 1, (2 * quiet - length + 1) / (length - 1)), (length, (2 * quiet - length) / length),
+                                   (40, 2.0)]):
+        assert abs(lse[i, 0].item() - math.log(n)) <= 2.0 ** -18, (i, lse[i, 0].item(), math.log(n))
+        assert torch.all((out[i].cpu().double() - mean).abs() <= abs(mean) * 2.0 ** -8 * (1 + 2.0 ** -8)), i
+
+
+@gpu
 @pytest.mark.parametrize("d,kv,heads,k", [(64, 1, 4, 7), (128, 2, 16, 40), (128, 1, 20, 130), (256, 1, 2, 64)])
 def test_attend_lists(misa, d, kv, heads, k):
     """A list per query: any order, padding, tokens it does not see yet, the same token twice."""
