@@ -722,15 +722,19 @@ int64_t tile_units(const Cache& c, const BlockAttend& b) {
 
 // Slots of a kv head where units are shared out in parts: if those that rows with up to
 // `most` new tokens can have leave half of the card without work; as many as the card
-// holds, or one a unit.  (Counted with a unit more for each row of the table, as the grid
-// is, five drafts on 16 rows had half the parts: 333 us for 215.)
+// holds, or one a unit that can have work.  A row's c pairs are floor(c / size) + 1 units
+// at most, so that those are a unit more for each query or row, whichever are fewer.
+// (With a unit more for each row of the table, as units are numbered, five drafts on 16
+// rows had half the parts, 333 us for 215; and four queries of 1024 heads on 64, in a table of
+// 1000 rows, a workspace of 2.0 GiB for 16 MiB.)
 int32_t tile_slots(const Cache& c, const BlockAttend& b) {
   const int64_t rows = 32 * row_waves(c, b), most = std::max(b.most, 1), units = tile_units(c, b);
   const int64_t whole = ((b.n - 1) / most + 1) * ((most * (b.heads / c.kv_heads) - 1) / rows + 1);
   const int64_t longest = (static_cast<int64_t>(c.row_pages) * c.P + kLeastTokens - 1) / kLeastTokens;
   if (std::min(units, whole) * c.kv_heads > kSlots / 2 || longest < 2 || units > kMaxUnits) return 0;
-  const int64_t useful = units * std::min<int64_t>(longest, kMaxParts);
-  return static_cast<int32_t>(std::max(units, std::min<int64_t>(kSlots / c.kv_heads, useful)));
+  const int64_t working = unit_base(b.n, b.heads / c.kv_heads, row_shift(row_waves(c, b)), std::min(c.rows, b.n), 1);
+  const int64_t useful = working * std::min<int64_t>(longest, kMaxParts);
+  return static_cast<int32_t>(std::max(working, std::min<int64_t>(kSlots / c.kv_heads, useful)));
 }
 
 int32_t part_rows(const Cache& c, const BlockAttend& b) {

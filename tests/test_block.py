@@ -223,6 +223,22 @@ def test_block_calls_refuse_arguments(misa):
         assert attend(n=most, most=most, ws=FAKE + 8) == -1
 
 
+def test_block_workspace_follows_the_queries(misa):
+    """A few queries on a table of many rows need about what they need on a table of few."""
+    def need(rows, n, heads, kv, most):
+        c = misa.cache(rows, 512, 4096, 64, kv, 128, 128, misa.MISA_FP8_E4M3)
+        return misa.misa_block_attend_workspace_bytes(c, 32, heads, n, most, 0)
+
+    for n, heads, kv, most in ((80, 64, 8, 5), (80, 64, 8, 80), (4, 1024, 64, 4), (2, 8, 8, 2)):
+        few, many = need(32, n, heads, kv, most), need(900, n, heads, kv, most)
+        # parts for all workgroups at a time, or for each unit that can have work: sums of (pairs of a query's row) x 128;
+        # and 8 bytes a unit, of which the table's rows have one each
+        pairs = min(128, n * heads // kv)
+        working = (n * heads // kv >> 6) + n
+        assert 0 < few <= many <= max(few, max(512, kv * working) * (pairs * (128 * 4 + 8) + 8)) + 900 * 8 + 1024, (n, few, many)
+        assert many <= 1 << 28
+
+
 # ------------------------------------------------------------------ rotary positions
 
 
@@ -685,6 +701,22 @@ def test_attend_parts(misa, d, most, lengths, counts):
     g = torch.Generator().manual_seed(31)
     c, table, *pools = _pool(misa, g, lengths, 32, 16, 2, d)
     q = torch.randn(sum(counts) + 3, 6, d, generator=g).bfloat16()
+    _check_attend(misa, c, 16, 6, 0, 0.09, _offsets(counts), q, pools, table, lengths, None, most)
+
+
+@gpu
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("most", [2, MANY])
+def test_attend_few_queries_of_a_table_of_many_rows(misa, d, most):
+    """Parts are numbered by the queries' units of work, of which there are far fewer than rows of the table."""
+    _log(f"[gpu] block attend few of many rows {d} {most}")
+    g = torch.Generator().manual_seed(32)
+    lengths, counts = [0] * 900, [0] * 900
+    for r, length, count in ((0, 70, 0), (3, 2900, 2), (450, 5, 1), (451, 1200, 3), (899, 33, 2)):
+        lengths[r], counts[r] = length, count
+    c, table, *pools = _pool(misa, g, lengths, 32, 16, 2, d)
+    assert misa.misa_block_attend_workspace_bytes(c, 16, 6, 8, most, 0) > 0
+    q = torch.randn(8, 6, d, generator=g).bfloat16()
     _check_attend(misa, c, 16, 6, 0, 0.09, _offsets(counts), q, pools, table, lengths, None, most)
 
 
