@@ -516,6 +516,30 @@ def test_read(misa, case, out):
         assert ref.same_codes(ko.cpu()[written], code[written])
 
 
+@gpu
+@pytest.mark.parametrize("out", [0, 1, 2])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_read_of_many_tokens(misa, out, d):
+    """32 MB and more, marked as not to be kept: rows that end inside a workgroup's tokens, a lost page."""
+    P, B, kv = 128, 64, 4
+    n = (33 << 20) // (2 * kv * d * (1 + (4, 2, 1)[out])) + 1
+    lengths = [n - 7000, 5, 0, 6995]
+    _log(f"[gpu] read {n} tokens {d} {out}")
+    g = torch.Generator().manual_seed(54)
+    c, table, k, ks, v, vs = _pool(misa, g, lengths, P, B, kv, d)
+    table[3, 2] = -1
+    ko, vo = (torch.zeros(n, kv, d, device="cuda").to(TYPES[out]) for _ in range(2))
+    kos, vos = (torch.zeros(n, kv, device="cuda") if out == 2 else None for _ in range(2))
+    misa.misa_block_read(c, B, n, out, _offsets(lengths).cuda(), None, torch.tensor(lengths).int().cuda(),
+                         *_cuda(k, ks, v, vs, table), ko, kos, vo, vos)
+    for pool, scale, got, units in ((k, ks, ko, kos), (v, vs, vo, vos)):
+        code, unit, _ = ref.read(c, B, _offsets(lengths), None, lengths, pool, scale, table, n)
+        if out == 2:
+            assert ref.same_codes(got.cpu(), code) and torch.equal(units.cpu(), unit)
+        else:
+            assert torch.equal(got.cpu(), (code.float() * unit[..., None]).to(TYPES[out]))
+
+
 # ------------------------------------------------------------------ attention
 
 
@@ -744,6 +768,53 @@ def test_attend_rows_of_more_tiles_than_fp32_counts(misa):
                                    (40, 2.0)]):
         assert abs(lse[i, 0].item() - math.log(n)) <= 2.0 ** -18, (i, lse[i, 0].item(), math.log(n))
         assert torch.all((out[i].cpu().double() - mean).abs() <= abs(mean) * 2.0 ** -8 * (1 + 2.0 ** -8)), i
+
+
+@gpu
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("most", [2, MANY])
+@pytest.mark.parametrize("lengths,counts", [
+    ([9000, 0, 6200], [3, 0, 2]),  # nine and seven stages of 1024 tokens in one workgroup
+    ([7169, 1024, 1025, 2049], [40, 2, 1, 3]),  # a stage's last and first token
+])
+def test_attend_whole_rows_of_many_stages(misa, d, most, lengths, counts):
+    """More rows in the table than are shared out, so that long rows stay whole: pages and scales are looked up
+    by the waves in turn, stage after stage; pages of their own scales, some of them lost."""
+    _log(f"[gpu] block attend stages {d} {most} {lengths}")
+    g = torch.Generator().manual_seed(51)
+    idle = [0] * 1200
+    lengths, counts = lengths + idle, counts + idle
+    c, table, *pools = _pool(misa, g, lengths, 32, 16, 1, d)
+    assert misa.misa_block_attend_workspace_bytes(c, 16, 2, sum(counts), most, 0) == 0
+    table[0, 6500 // 32], table[0, 100] = -1, c.pages
+    q = torch.randn(sum(counts), 2, d, generator=g).bfloat16()
+    _check_attend(misa, c, 16, 2, 0, 0.09, _offsets(counts), q, pools, table, lengths, None, most)
+
+
+@gpu
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("most", [3, MANY])
+def test_attend_most_parts(misa, d, most):
+    """One row in the 32 parts that are the most, joined eight at a time."""
+    _log(f"[gpu] block attend 32 parts {d} {most}")
+    g = torch.Generator().manual_seed(52)
+    c, table, *pools = _pool(misa, g, [20011], 32, 32, 1, d)
+    table[0, 300] = -1
+    q = torch.randn(3, 2, d, generator=g).bfloat16()
+    _check_attend(misa, c, 32, 2, 0, 0.09, _offsets([3]), q, pools, table, [20011], None, most)
+
+
+@gpu
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_attend_single_tokens_of_large_caches(misa, d):
+    """A table of 64 MB of tokens and more, whose loads are marked as not to be kept; the rows are shorter."""
+    _log(f"[gpu] block attend large table {d}")
+    g = torch.Generator().manual_seed(53)
+    lengths, counts = [3000, 0, 70, 1], [1, 0, 1, 1]
+    width = (64 << 20) // (3 * 32 * 2 * 2 * d) + 1
+    c, table, *pools = _pool(misa, g, lengths, 32, 16, 2, d, width=width)
+    q = torch.randn(3, 8, d, generator=g).bfloat16()
+    _check_attend(misa, c, 16, 8, 0, 0.09, _offsets(counts), q, pools, table, lengths, None, 1)
 
 
 @gpu
@@ -1018,6 +1089,45 @@ def test_calls_on_streams_of_their_own(misa):
     torch.cuda.synchronize()
     for i in range(4):
         assert torch.equal(outs[i], alone[i % 2])
+
+
+@gpu
+def test_calls_at_once_against_the_reference(misa):
+    """A prompt, drafts, single tokens, lists and writes at once on streams of their own: each against what the
+    reference gives for it."""
+    _log("[gpu] calls at once")
+    g = torch.Generator().manual_seed(61)
+    jobs = []
+    for most, k, lengths, counts in ((1, 0, [2500, 900], [1, 1]), (5, 0, [1500, 40], [5, 3]), (150, 0, [700], [150]),
+                                     (2, 30, [300, 20], [2, 1])):
+        c, table, *pools = _pool(misa, g, lengths, 32, 16, 2, 64)
+        n = sum(counts)
+        q = torch.randn(n, 6, 64, generator=g).bfloat16()
+        idx = torch.randint(-1, 300, (n, k), generator=g).int() if k else None
+        want = ref.attend(misa, c, 16, 6, k, 0.1, _offsets(counts), q, *pools, table, lengths, idx)
+        on = _cuda(_offsets(counts), q, *pools, table, torch.tensor(lengths).int(), idx)
+        ws = torch.empty(misa.misa_block_attend_workspace_bytes(c, 16, 6, n, most, k), dtype=torch.uint8, device="cuda")
+        jobs.append((c, n, most, k, on, torch.empty_like(on[1]), torch.empty(n, 6, device="cuda"), ws, want))
+    lengths, counts = [100, 64, 65, 200], [37, 64, 1, 90]
+    c, table, pool, scale, _, _ = _pool(misa, g, lengths, 64, 32, 2, 128)
+    new = torch.randn(sum(counts), 2, 128, generator=g).bfloat16()
+    codes, units = ref.write(c, 32, _offsets(counts), lengths, new, pool, scale, table)
+    writes = [_cuda(_offsets(counts), torch.tensor(lengths).int(), new, pool, scale, table) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(6)]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for (cc, n, most, k, on, out, lse, ws, _), stream in zip(jobs, streams):
+            misa.misa_block_attend(cc, 16, 6, n, most, k, 0.1, *on, out, lse, ws, stream)
+    for (off, ln, kn, kp, ks, tb), stream in zip(writes, streams[4:]):
+        misa.misa_block_write(c, 32, len(new), off, ln, kn, None, kp, ks, None, None, tb, stream)
+    torch.cuda.synchronize()
+    for _, _, most, k, _, out, lse, _, (wo, wl, out_tol, lse_tol, wide, _) in jobs:
+        tol = out_tol + wide if k == 0 and most > 1 else out_tol
+        assert torch.all((out.cpu().double() - wo).abs() <= tol + 1e-30)
+        empty = wl == -math.inf
+        assert torch.equal(lse.cpu() == -math.inf, empty) and torch.all(((lse.cpu().double() - wl).abs() <= lse_tol) | empty)
+    for _, _, _, kp, ks, _ in writes:
+        assert torch.equal(ks.cpu(), units) and ref.same_codes(kp.cpu(), codes)
 
 
 @gpu
