@@ -483,7 +483,8 @@ misa_status misa_rope_frequencies(const misa_rope_scaling* scaling, double* freq
  * ..copy) are those of misa_cache; codes and scales are buffers of misa_page_copy.
  *
  * A scale is a power of two: the smallest 2^e, e >= -100, with amax <= 448 * 2^e
- * over the finite values that the block got so far.  A code is x / scale rounded
+ * over the finite values that the block got so far.  misa_block_write leaves such
+ * scales, and misa_block_attend takes no others.  A code is x / scale rounded
  * to nearest even; infinities and NaN become NaN codes and set no scale.
  *
  * Batches of rows come packed: offsets [rows + 1] int32, ascending; entries

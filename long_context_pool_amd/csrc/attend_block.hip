@@ -33,7 +33,7 @@ struct TileArgs {
   float* part_o;    // [kv_heads, slots, part_rows, d] sums of a part of a unit's tokens
   float2* part_ml;  // [kv_heads, slots, part_rows] maximum (log2) and sum; 0: nothing seen
   int2* where;      // [units] a unit's first slot and its number of them
-  int32_t slots, full;  // workgroups of a kv head (0: one a unit, by its number), of them at work together
+  int32_t slots, full;  // workgroups of a kv head (0: one a unit, by its number), of them for parts (kSlots)
   int32_t part_rows;    // rows that a unit can have
   int32_t heads, share, kv_heads, row_pages, pages, shift;
   uint32_t q_and, q_xor;  // a negative scale turns the queries' signs, a zero one clears them
@@ -111,7 +111,7 @@ constexpr int kMaxParts = 32;    // of a unit
 constexpr int kLeastTokens = 256;  // of a part
 
 // Slot `slot` of a kv head's: units' tiles in parts of at most q, the smallest q that gives
-// no more parts than there are slots to work together.  Each workgroup finds it out for
+// no more parts than there are slots for them.  Each workgroup finds it out for
 // itself: with as many parts for each unit instead, five drafts on 16 rows of 16384 to
 // 32768 tokens took 199 us for 189, four 179 for 163 (heads of 256 732 for 660), 32 tokens
 // 575 for 530; one prompt of 512 tokens 27.5 for 30.0.
@@ -707,7 +707,11 @@ __global__ __launch_bounds__(256) void join_tiles_kernel(TileArgs a) {
       make_uint2(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, y));
 }
 
-constexpr int kSlots = 512;  // workgroups that the card holds at a time
+// Workgroups that units are shared out to: those that the card holds at a time, two a CU.
+// It holds one of heads of 256, whose parts run in two rounds: with 256 of them four new
+// tokens on 20 rows of up to 8192, 64 heads on 8, took 405 us for 234 and on 16 of 32768 767 for
+// 655, but on 8 of 2000 37 for 47, and a prompt of 512 40 for 61.
+constexpr int kSlots = 512;
 
 // Two waves' rows where no row of the batch has more: 16 rows of 32768 tokens, 64 heads
 // on 8 of 128, eight new tokens each (64 pairs of query and head) 198 us, 223 with
@@ -721,8 +725,8 @@ int64_t tile_units(const Cache& c, const BlockAttend& b) {
 }
 
 // Slots of a kv head where units are shared out in parts: if those that rows with up to
-// `most` new tokens can have leave half of the card without work; as many as the card
-// holds, or one a unit that can have work.  A row's c pairs are floor(c / size) + 1 units
+// `most` new tokens can have are half of kSlots at most; as many as the card
+// holds (kSlots), or one a unit that can have work.  A row's c pairs are floor(c / size) + 1 units
 // at most, so that those are a unit more for each query or row, whichever are fewer.
 // (With a unit more for each row of the table, as units are numbered, five drafts on 16
 // rows had half the parts, 333 us for 215; and four queries of 1024 heads on 64, in a table of

@@ -45,7 +45,8 @@ struct WriteArgs {
 // Units go by blocks (a row's c tokens touch at most floor(c / B) + 2) or, where
 // there are fewer of them, by tokens: the first of a row and those that begin a
 // block are at work, the other workgroups leave (32 rows with a token each: 32
-// units for 64).
+// units for 64, 6.3 us for 7.1 a call; 1024 rows 30.6 us for 36.7; 256 rows with four each go by
+// blocks, 13.0 us, by tokens 30.9; 8192 tokens of three rows 12.1 and 101).
 //
 // Bound by memory traffic: 8192 tokens of 8 heads of 128 (50 MB) 11.8 us, 4.3 TB/s (13
 // us with keys and values in workgroups of their own); 32 rows with a token each 4.5 us,
@@ -246,7 +247,9 @@ constexpr int kRounds = OUT == kF32 ? 4 : 2;
 // is looked up once: a lookup each cost 8 rows of 131072 keys (213 MB) 20 of 70 us.
 // Bound by HBM traffic, 5.1 TB/s there.
 //
-// ONCE: much is moved, and marked as not to be kept (41.7 us there, 47.1 without).
+// ONCE: much is moved, and marked as not to be kept (41.7 us there, 47.1 without; bf16
+// rows, 98 MB 25.4 and 27.3 us, 31 MB 10.7 and 9.9; between 32 and 64 MB plain loads are still
+// ahead where the cache is on the chip from the call before: 49 MB 14.6 and 12.6).
 template <int D, int OUT, bool ONCE>
 __global__ __launch_bounds__(256) void block_read_kernel(ReadArgs a) {
   constexpr int N = kPerLane<OUT>, kReadRounds = kRounds<OUT>;
