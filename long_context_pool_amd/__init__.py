@@ -428,7 +428,8 @@ def rope_scaling(kind, rot, base, factor=1.0, original=0.0, fast=0.0, slow=0.0) 
 
 def misa_rope_frequencies(scaling):
     """(radians a position of each pair, as a list, and the amplitude)."""
-    freq, amplitude = (ctypes.c_double * max(1, scaling.rot // 2))(), _F32()
+    # More than 1024 turned elements are refused before anything is written.
+    freq, amplitude = (ctypes.c_double * min(max(1, scaling.rot // 2), 512))(), _F32()
     _check(_lib.misa_rope_frequencies(ctypes.byref(scaling), freq, ctypes.byref(amplitude)), "misa_rope_frequencies")
     return list(freq), amplitude.value
 

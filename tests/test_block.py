@@ -144,6 +144,21 @@ def test_rope_frequencies_refuse(misa):
     assert misa.lib().misa_rope_frequencies(ctypes.byref(s), out, None) == -1
 
 
+def test_rope_frequencies_refuse_cheaply(misa):
+    """A size that is refused takes no memory first."""
+    import tracemalloc
+
+    tracemalloc.start()
+    try:
+        for rot in (1026, 1 << 27, (1 << 31) - 2, -4):
+            with pytest.raises(misa.MisaError):
+                misa.misa_rope_frequencies(misa.rope_scaling(0, rot, 1e4))
+        assert tracemalloc.get_traced_memory()[1] < 1 << 20
+    finally:
+        tracemalloc.stop()
+    assert len(misa.misa_rope_frequencies(misa.rope_scaling(0, 1024, 1e4))[0]) == 512
+
+
 def _calls(misa, c, block=32):
     """The block calls with good arguments, to be changed one at a time."""
     lib, r = misa.lib(), ctypes.byref(c)
