@@ -56,7 +56,7 @@ __device__ __forceinline__ void load8(const void* p, int64_t at, float* y) {
 }
 
 template <int OUT>
-__device__ __forceinline__ void store8(void* p, int64_t at, const float* y) {
+__device__ __forceinline__ void store8(void* p, int64_t at, const float* y, float mult) {
   if constexpr (OUT == kF32) {
     float4* q = reinterpret_cast<float4*>(static_cast<float*>(p) + at);
     q[0] = make_float4(y[0], y[1], y[2], y[3]);
@@ -69,7 +69,7 @@ __device__ __forceinline__ void store8(void* p, int64_t at, const float* y) {
     *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + at) = __builtin_bit_cast(uint4, b);
   } else {
     *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p) + at) =
-        make_uint2(e4m3_pack4(y[0], y[1], y[2], y[3], 1.f), e4m3_pack4(y[4], y[5], y[6], y[7], 1.f));
+        make_uint2(e4m3_pack4(y[0], y[1], y[2], y[3], mult), e4m3_pack4(y[4], y[5], y[6], y[7], mult));
   }
 }
 
@@ -147,8 +147,8 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a) {
       for (int j = 0; j < 16; ++j) top = amax_step(top, y[i][j]);
     }
   }
+  float scale = 1.f, mult = 1.f;
   if constexpr (OUT == kFP8) {
-    float scale, mult;
     top = lanes_reduce<(TPR < kWave ? TPR : kWave), true>(top);
     if constexpr (TPR > kWave) {
       if (lane_id() == 0) tops[threadIdx.x / kWave] = top;
@@ -157,17 +157,12 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a) {
     }
     e4m3_scale(top, scale, mult);
     if (sub == 0 && live) a.out_scale[t] = scale;
-    const float rest = e4m3_rest(top, mult);  // bf16 values that pass: quotients midway between two codes
-#pragma unroll
-    for (int i = 0; i < NI; ++i)
-#pragma unroll
-      for (int j = 0; j < 16; ++j) y[i][j] = __builtin_fmaf(y[i][j], mult, y[i][j] * rest);
   }
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
     if (at[i] < 0) continue;
-    store8<OUT>(a.out, to + at[i], y[i]);
-    store8<OUT>(a.out, to + at[i] + gap[i], y[i] + 8);
+    store8<OUT>(a.out, to + at[i], y[i], mult);
+    store8<OUT>(a.out, to + at[i] + gap[i], y[i] + 8, mult);
   }
 }
 
@@ -184,7 +179,7 @@ __global__ __launch_bounds__(256) void rope_any_kernel(RopeArgs a) {
   const int64_t from = static_cast<int64_t>(t) * s.x_stride, to = static_cast<int64_t>(t) * s.out_stride;
   const int half = s.rot / 2, per_head = s.d - half;  // pairs, then the rest
   const int32_t pos = a.pos[t];
-  float scale = 1.f, mult = 1.f, rest = 0.f, top = 0.f;
+  float scale = 1.f, mult = 1.f, top = 0.f;
   for (int round = OUT == kFP8 ? 0 : 1; round < 2; ++round) {
     for (int i = threadIdx.x; i < s.heads * per_head; i += 256) {
       const int head = i / per_head, e = i - head * per_head;
@@ -213,7 +208,7 @@ __global__ __launch_bounds__(256) void rope_any_kernel(RopeArgs a) {
         static_cast<__bf16*>(a.out)[to + p] = static_cast<__bf16>(x0);
         if (q >= 0) static_cast<__bf16*>(a.out)[to + q] = static_cast<__bf16>(x1);
       } else {
-        const uint32_t code = e4m3_pack4(__builtin_fmaf(x0, mult, x0 * rest), __builtin_fmaf(x1, mult, x1 * rest), 0.f, 0.f, 1.f);
+        const uint32_t code = e4m3_pack4(x0, x1, 0.f, 0.f, mult);
         static_cast<uint8_t*>(a.out)[to + p] = static_cast<uint8_t>(code);
         if (q >= 0) static_cast<uint8_t*>(a.out)[to + q] = static_cast<uint8_t>(code >> 8);
       }
@@ -222,9 +217,7 @@ __global__ __launch_bounds__(256) void rope_any_kernel(RopeArgs a) {
       top = lanes_reduce<kWave, true>(top);
       if (lane_id() == 0) tops[threadIdx.x / kWave] = top;
       __syncthreads();
-      top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-      e4m3_scale(top, scale, mult);
-      rest = e4m3_rest(top, mult);
+      e4m3_scale(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])), scale, mult);
       if (threadIdx.x == 0) a.out_scale[t] = scale;
     }
   }

@@ -323,25 +323,6 @@ def test_rope(misa, case):
 
 
 @gpu
-@pytest.mark.parametrize("pairs", [0, 1])
-@pytest.mark.parametrize("d,rot", [(128, 64), (72, 36), (512, 32)])
-def test_rope_codes_midway(misa, d, rot, pairs):
-    """Codes of passing bf16 values are the exact quotients' (64 bits tell one from a tie), ties to even."""
-    n, heads = 300, 3
-    _log(f"[gpu] rope ties {d} {rot} {pairs}")
-    g = torch.Generator().manual_seed(d)
-    x = torch.randn(n, heads, d, generator=g).bfloat16()
-    top = 16 + torch.arange(n) % 128 / 8  # exact in bf16, above every turned value
-    x[:, 1, rot + 1] = top.bfloat16()
-    spec = misa.rope_spec(heads, d, 0, rot, pairs, 1, 2, heads * d, heads * d)
-    out, scale = torch.zeros(n, heads, d, device="cuda").to(E4M3), torch.zeros(n, device="cuda")
-    freq = torch.tensor([10000.0 ** (-2.0 * i / rot) for i in range(rot // 2)], dtype=torch.float64, device="cuda")
-    misa.misa_rope(spec, n, x.cuda(), torch.arange(n).int().cuda(), freq, out, scale)
-    want = (x[..., rot:].double() * 448 / top.double()[:, None, None]).to(E4M3).float()
-    assert torch.equal(out.cpu().float()[..., rot:], want)
-
-
-@gpu
 def test_rope_turns_back_and_keeps_distances(misa):
     """Rotations by p and -p cancel, and q . k depends on the distance alone."""
     n, heads, d = 16, 2, 64
