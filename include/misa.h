@@ -438,7 +438,8 @@ typedef struct {
  *   out   [n, heads, d], out_stride apart  MISA_F32, MISA_BF16 or MISA_FP8_E4M3,
  *         written; may be x itself (same type and stride)
  *   out_scale  [n]   fp32, written (fp8 only, else ignored): one scale per token
- *         over its heads, as misa_*'s q_scale and k_scale
+ *         over its heads, amax / 448, as misa_*'s q_scale and k_scale; a code is the
+ *         value divided by it (in fp32), rounded to nearest even
  * 0 <= n < 2^24 (0: no-op); 1 <= heads, heads * d <= 32768; rot even, 0 < rot <=
  * 1024, first + rot <= d; strides of at least heads * d (out_stride of an fp8 out
  * exactly that) and below 2^31; rotated values in fp32's normal range. */

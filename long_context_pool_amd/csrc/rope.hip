@@ -56,7 +56,7 @@ __device__ __forceinline__ void load8(const void* p, int64_t at, float* y) {
 }
 
 template <int OUT>
-__device__ __forceinline__ void store8(void* p, int64_t at, const float* y, float mult) {
+__device__ __forceinline__ void store8(void* p, int64_t at, const float* y) {
   if constexpr (OUT == kF32) {
     float4* q = reinterpret_cast<float4*>(static_cast<float*>(p) + at);
     q[0] = make_float4(y[0], y[1], y[2], y[3]);
@@ -69,7 +69,7 @@ __device__ __forceinline__ void store8(void* p, int64_t at, const float* y, floa
     *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + at) = __builtin_bit_cast(uint4, b);
   } else {
     *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p) + at) =
-        make_uint2(e4m3_pack4(y[0], y[1], y[2], y[3], mult), e4m3_pack4(y[4], y[5], y[6], y[7], mult));
+        make_uint2(e4m3_pack4(y[0], y[1], y[2], y[3], 1.f), e4m3_pack4(y[4], y[5], y[6], y[7], 1.f));
   }
 }
 
@@ -147,7 +147,6 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a) {
       for (int j = 0; j < 16; ++j) top = amax_step(top, y[i][j]);
     }
   }
-  float scale = 1.f, mult = 1.f;
   if constexpr (OUT == kFP8) {
     top = lanes_reduce<(TPR < kWave ? TPR : kWave), true>(top);
     if constexpr (TPR > kWave) {
@@ -155,14 +154,20 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a) {
       __syncthreads();
       top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
     }
+    float scale, mult;
     e4m3_scale(top, scale, mult);
     if (sub == 0 && live) a.out_scale[t] = scale;
+    const Quotient by_scale(scale);
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) y[i][j] = by_scale.of(y[i][j]);
   }
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
     if (at[i] < 0) continue;
-    store8<OUT>(a.out, to + at[i], y[i], mult);
-    store8<OUT>(a.out, to + at[i] + gap[i], y[i] + 8, mult);
+    store8<OUT>(a.out, to + at[i], y[i]);
+    store8<OUT>(a.out, to + at[i] + gap[i], y[i] + 8);
   }
 }
 
@@ -208,7 +213,8 @@ __global__ __launch_bounds__(256) void rope_any_kernel(RopeArgs a) {
         static_cast<__bf16*>(a.out)[to + p] = static_cast<__bf16>(x0);
         if (q >= 0) static_cast<__bf16*>(a.out)[to + q] = static_cast<__bf16>(x1);
       } else {
-        const uint32_t code = e4m3_pack4(x0, x1, 0.f, 0.f, mult);
+        const Quotient by_scale(scale);
+        const uint32_t code = e4m3_pack4(by_scale.of(x0), by_scale.of(x1), 0.f, 0.f, 1.f);
         static_cast<uint8_t*>(a.out)[to + p] = static_cast<uint8_t>(code);
         if (q >= 0) static_cast<uint8_t*>(a.out)[to + q] = static_cast<uint8_t>(code >> 8);
       }

@@ -323,6 +323,35 @@ def test_rope(misa, case):
 
 
 @gpu
+@pytest.mark.parametrize("pairs", [0, 1])
+@pytest.mark.parametrize("d,rot", [(128, 64), (72, 36), (512, 32)])
+def test_rope_codes_are_the_nearest(misa, d, rot, pairs):
+    """Codes of passing values are their fp32 quotients by the token's scale, rounded to nearest even, and the
+    scale is amax / 448: both to the bit, and a zero token, one with an infinity and one with NaN as well."""
+    n, heads = 300, 3
+    _log(f"[gpu] rope codes {d} {rot} {pairs}")
+    g = torch.Generator().manual_seed(d)
+    x = torch.randn(n, heads, d, generator=g).bfloat16()
+    top = 16 + torch.arange(n) % 128 / 8  # exact in bf16, above every turned value
+    x[:, 1, rot + 1] = top.bfloat16()
+    x[40] = 0
+    x[41, 0, rot] = math.inf
+    x[42, 2, d - 1] = math.nan
+    x[43:60] *= 2.0 ** 90
+    x[60:80] *= 2.0 ** -80
+    spec = misa.rope_spec(heads, d, 0, rot, pairs, 1, 2, heads * d, heads * d)
+    out, scale = torch.zeros(n, heads, d, device="cuda").to(E4M3), torch.zeros(n, device="cuda")
+    freq = torch.tensor([10000.0 ** (-2.0 * i / rot) for i in range(rot // 2)], dtype=torch.float64, device="cuda")
+    misa.misa_rope(spec, n, x.cuda(), torch.arange(n).int().cuda(), freq, out, scale)
+    y = x.float()
+    amax = torch.where(y.isnan(), 0.0, y.abs()).flatten(1).amax(1)
+    amax[42] = top[42]
+    unit = torch.where(amax > 0, amax / 448, 1.0)
+    assert torch.equal(scale.cpu(), unit)
+    assert ref.same_codes(out.cpu()[..., rot:].contiguous(), (y / unit[:, None, None]).to(E4M3)[..., rot:].contiguous())
+
+
+@gpu
 def test_rope_turns_back_and_keeps_distances(misa):
     """Rotations by p and -p cancel, and q . k depends on the distance alone."""
     n, heads, d = 16, 2, 64
