@@ -78,8 +78,8 @@ __device__ __forceinline__ int value_dim(int c, int j) {
 //
 // PACKED (misa_block_attend): a unit is a query of a packed batch instead of a row,
 // and the scales are those of blocks of tokens.  8 rows of up to 131072 tokens of 8 heads
-// of 128 (1.68 GB) 293 to 304 us, 5.5 to 5.7 TB/s.  Of one prompt's 512 queries with 2048
-// listed tokens each, 64 heads on 8, 221 to 260 us on several boxes: 2.1 GB come out of L2, a third of it
+// of 128 (1.68 GB) 290 to 304 us, 5.5 to 5.8 TB/s.  Of one prompt's 512 queries with 2048
+// listed tokens each, 64 heads on 8, 220 to 265 us on several boxes: 2.1 GB come out of L2, a third of it
 // from behind, 9 to 9.7 TB/s, bound by those loads' latency (f16 weights in one part, a
 // fifth fewer instructions: the same; four waves a SIMD: 252 us).
 template <int D, int DT, int RT, bool ONCE, bool PACKED>

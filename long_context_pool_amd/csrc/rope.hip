@@ -186,6 +186,7 @@ __global__ __launch_bounds__(256) void rope_any_kernel(RopeArgs a) {
   const int32_t pos = a.pos[t];
   float scale = 1.f, mult = 1.f, top = 0.f;
   for (int round = OUT == kFP8 ? 0 : 1; round < 2; ++round) {
+    const Quotient by_scale(scale);  // known from the first round
     for (int i = threadIdx.x; i < s.heads * per_head; i += 256) {
       const int head = i / per_head, e = i - head * per_head;
       int p = s.first + e, q = -1;
@@ -213,7 +214,6 @@ __global__ __launch_bounds__(256) void rope_any_kernel(RopeArgs a) {
         static_cast<__bf16*>(a.out)[to + p] = static_cast<__bf16>(x0);
         if (q >= 0) static_cast<__bf16*>(a.out)[to + q] = static_cast<__bf16>(x1);
       } else {
-        const Quotient by_scale(scale);
         const uint32_t code = e4m3_pack4(by_scale.of(x0), by_scale.of(x1), 0.f, 0.f, 1.f);
         static_cast<uint8_t*>(a.out)[to + p] = static_cast<uint8_t>(code);
         if (q >= 0) static_cast<uint8_t*>(a.out)[to + q] = static_cast<uint8_t>(code >> 8);
